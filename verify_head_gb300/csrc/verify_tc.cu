@@ -27,22 +27,18 @@
 // Every wait is bounded (about 2 s of %globaltimer); on expiry the waiting
 // thread sets the workspace error word, skips the rest of its work, and the
 // CTA still drains its copies, frees TMEM and returns.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <atomic>
-#include <mutex>
 
 #include "vh_kernels.h"
 #include "vh_verify.h"
 #include "vh_ptx.cuh"
+#include "vh_tc.cuh"
 
 namespace vh {
 namespace tc {
 
 constexpr int kBlockM = 128;      // W rows per tile (MMA M)
-constexpr int kBlockK = 64;       // K per stage (one 128 B swizzle atom of bf16)
 constexpr int kMaxN = 256;        // hidden rows per launch (MMA N <= 256)
 constexpr int kMaxStagesTc = 8;    // deepest ring of any instance
 constexpr int kThreadsTc = 192;
@@ -82,7 +78,7 @@ struct TcArgs {
 };
 
 // ---------------------------------------------------------------------------
-// tcgen05 / TMA wrappers (barriers and bulk copies: vh_ptx.cuh).
+// tcgen05 / TMA wrappers: vh_tc.cuh (barriers and bulk copies: vh_ptx.cuh).
 
 using ptx::globaltimer;
 using ptx::mbar_arrive;
@@ -94,76 +90,6 @@ using ptx::mbar_wait;
 using ptx::policy_evict_first;
 using ptx::policy_evict_last;
 using ptx::smem_u32;
-
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, unsigned long long* bar, int x, int y,
-                                            unsigned long long policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<unsigned long long>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "l"(policy)
-        : "memory");
-}
-
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
-// 1024 bytes apart (SBO), tile base 1024-byte aligned.
-__device__ __forceinline__ unsigned long long smem_desc_sw128(uint32_t saddr) {
-    unsigned long long d = 0;
-    d |= (unsigned long long)((saddr >> 4) & 0x3FFFu);          // start address
-    d |= (unsigned long long)(16u >> 4) << 16;                   // leading byte offset (unused here)
-    d |= (unsigned long long)(1024u >> 4) << 32;                 // stride byte offset
-    d |= 1ull << 46;                                             // descriptor version (tcgen05)
-    d |= 2ull << 61;                                             // 128-byte swizzle
-    return d;
-}
-
-// Instruction descriptor, kind::f16: bf16 A and B, fp32 D, both K-major.
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
-    return (1u << 4)                     // D format: f32
-           | (1u << 7)                   // A format: bf16
-           | (1u << 10)                  // B format: bf16
-           | ((uint32_t)(N >> 3) << 17)  // N / 8
-           | ((uint32_t)(M >> 4) << 24); // M / 16
-}
-
-__device__ __forceinline__ void mma_bf16(uint32_t tmem_d, unsigned long long adesc, unsigned long long bdesc,
-                                         uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(unsigned long long* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 32 lanes x 32 columns of fp32 from TMEM: thread t gets lane (base + t),
-// columns col .. col+31.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ float redux_max_f32(float x) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 // Column argmax over the warp's 32 W rows for 32 hidden columns at once.
 // v[j] is this lane's (W row's) score for column j.  For every column the
@@ -422,56 +348,6 @@ struct alignas(8) Barriers2 {
 
 constexpr size_t kSmem2 = 1024 + (size_t)kStages2 * (kStageA2 + kStageB2) + sizeof(Barriers2) + kMaxN * 8 + 64;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// Shared-memory address of the same object in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// TMA load into this CTA's shared memory, completing on a barrier that may
-// live in the peer CTA (cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int x, int y,
-                                                 unsigned long long policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<unsigned long long>(map)), "r"(bar_cluster), "r"(x), "r"(y), "l"(policy)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_bf16_pair(uint32_t tmem_d, unsigned long long adesc, unsigned long long bdesc,
-                                              uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// Arrive on the barrier at this offset in both CTAs once all prior MMAs are done.
-__device__ __forceinline__ void mma_commit_pair(unsigned long long* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"((unsigned short)3)
-        : "memory");
-}
-
 __global__ void __launch_bounds__(kThreadsTc, 1)
     k_verify_tc2(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const TcArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -651,36 +527,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Host side: tensor maps through the driver entry point (no libcuda link).
-
-static PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-// 2-D bf16 row-major [rows][H] map with a [box_rows][64] box, 128 B swizzle.
-static bool make_map(CUtensorMap* m, const void* base, int rows, int H, int box_rows) {
-    auto enc = get_encode();
-    if (!enc) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)H, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)H * 2};
-    cuuint32_t box[2] = {(cuuint32_t)kBlockK, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
+// Host side.
 
 // CTA-pair launch (R in 129..256): clusters of 2, grid = 2 x the resident clusters.
 static cudaError_t launch_verify_tc2(const uint16_t* X, int R, int H, const uint16_t* W, int V, Workspace ws,
