@@ -384,6 +384,137 @@ VH_API vh_status spec_verify_greedy_nvfp4_packed(const void* hidden, const void*
                                                  int32_t* accept_len, int32_t* next_ids, float* row_maxlogit,
                                                  void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators on either side of the head: the residual addition and RMS norm
+ * that produce its hidden rows, and log probabilities of its scores.  No
+ * counterpart in the source pages (their path starts at the hidden row and
+ * ends at the argmax); a server returns log probabilities with its tokens,
+ * and a draft head is trained through them.
+ *
+ * Element type of rows; sums, softmax statistics and norms are fp32 in every
+ * case, and a result is rounded to the row type once.  Strides are in
+ * elements between rows; the elements of a row are contiguous.  Any width,
+ * stride and element-aligned address is taken; 16-byte aligned rows of whole
+ * 16-byte vectors are read fastest.
+ * ------------------------------------------------------------------------ */
+typedef enum { VH_F32 = 0, VH_BF16 = 1, VH_F16 = 2 } vh_dtype;
+
+/* Output of vh_add_rmsnorm: the rows' own type, or 8 bits with one scale per
+ * row (OCP e4m3 or signed int8). */
+typedef enum { VH_NORM_SAME = 0, VH_NORM_INT8 = 1, VH_NORM_E4M3 = 2 } vh_norm_out;
+
+/*
+ * Residual addition and root-mean-square norm of T rows of width H:
+ *     h = x + residual                        (residual NULL: h = x)
+ *     u = h * (weight + weight_offset)        (weight NULL: ones)
+ *     rstd = 1 / sqrt(mean(h^2) + eps)
+ *     VH_NORM_SAME:  y = u * rstd
+ *     8 bits:        y = code of u * (Q * (1 / max|u|)), scales[t] = max|u| * rstd / Q, Q = 127 or 448,
+ *                    rounded to nearest even, so that code * scale stands for u * rstd
+ * The norm is taken of the fp32 sum; h is written rounded.  A row of zeros
+ * has codes and scale 0; a row with an infinite or NaN element has scale NaN.
+ *
+ *  x, residual  device, dtype [T][H] (residual may be NULL)
+ *  weight       device, [H] of dtype, or fp32 when weight_f32 != 0; may be NULL
+ *  weight_offset  0, or 1 for zero-centred weights
+ *  y            device, dtype [T][H], or 8-bit codes [T][H] (out)
+ *  h            device, dtype [T][H] (out) or NULL; may be x or residual itself (same address and stride)
+ *  scales       device, fp32 [T] (out), 8-bit outputs only (else ignored)
+ *  T >= 1, 1 <= H <= 2^24; strides >= H; eps >= 0, finite
+ *  y in the rows' type may be x or residual itself; 8-bit codes may not
+ *  overlap the inputs.
+ */
+VH_API vh_status vh_add_rmsnorm(const void* x, const void* residual, const void* weight, int dtype, int weight_f32,
+                                int T, int H, int64_t x_stride, int64_t residual_stride, float eps,
+                                float weight_offset, void* y, int64_t y_stride, int out, void* h, int64_t h_stride,
+                                float* scales, void* stream);
+
+/* Workspace of vh_add_rmsnorm_grad (the tokens' shares of dweight); need not
+ * be zeroed.  0 for T < 1 or H < 1. */
+VH_API size_t vh_add_rmsnorm_grad_workspace_bytes(int T, int H);
+
+/*
+ * Gradient of vh_add_rmsnorm (VH_NORM_SAME), with n = h * rstd and
+ * g = dy * (weight + weight_offset):
+ *     dx = rstd * (g - n * mean(g * n)) + dh      (the gradient of x and of residual alike)
+ *     dweight = sum over rows of dy * n           (fp32, summed in a fixed order)
+ * h is the sum the forward pass wrote; dh the gradient that reaches it from
+ * the residual stream, or NULL.
+ *
+ *  dy, h, dh, dx  device, dtype [T][H]; dx may be dy, h or dh itself
+ *  dweight        device, fp32 [H] (out) or NULL: not computed, ws may then be NULL
+ *  ws             device, 16-byte aligned, >= vh_add_rmsnorm_grad_workspace_bytes(T, H)
+ */
+VH_API vh_status vh_add_rmsnorm_grad(const void* dy, const void* h, const void* weight, const void* dh, int dtype,
+                                     int weight_f32, int T, int H, int64_t dy_stride, int64_t h_stride,
+                                     int64_t dh_stride, float eps, float weight_offset, void* dx, int64_t dx_stride,
+                                     float* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace of vh_logits_logprobs: 16-byte aligned, zeroed once by the caller
+ * after allocation; every call leaves its counters zero again, and a buffer
+ * serves calls of any sizes that need no more bytes.  Not to be shared with
+ * another operator.  0 for a size out of range. */
+VH_API size_t vh_logits_logprobs_workspace_bytes(int R, int V, int top_n);
+
+/*
+ * Log probabilities of given tokens from logits, with entropy and
+ * alternatives.  For each row r < R, p = softmax(logits[r]):
+ *     logprob[r] = log p[tokens[r]]
+ *     entropy[r] = - sum_v p_v log p_v
+ *     lse[r]     = log sum_v exp(logits[r,v])
+ *     top_ids[r], top_logprobs[r]: the top_n largest logits, descending, equal
+ *                  ones by lowest id (past the V-th: id -1, log probability -inf)
+ * -inf marks a place as impossible; NaN counts as -inf.  A row with no other
+ * value has lse and every log probability -inf and entropy 0; a row with +inf
+ * has lse, entropy and every log probability NaN (-inf at NaN places).  A
+ * token outside [0, V) (a padding position) has logprob 0.
+ *
+ *  logits  device, dtype [R][V], stride elements between rows
+ *  tokens  device, int32 [R], or NULL with logprob NULL
+ *  logprob, entropy, lse   device, fp32 [R] (out), each may be NULL
+ *  top_n   0..32;  top_ids int32, top_logprobs fp32: device [R][top_n] (out), ignored for 0
+ *  R >= 1, 1 <= V <= 2^31 - 1024, stride >= V
+ */
+VH_API vh_status vh_logits_logprobs(const void* logits, int dtype, int R, int V, int64_t stride, const int32_t* tokens,
+                                    int top_n, float* logprob, float* entropy, float* lse, int32_t* top_ids,
+                                    float* top_logprobs, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of vh_logits_logprobs with respect to the logits:
+ *     dlogits[r,v] = g_logprob[r] * ([v == tokens[r]] - p_v) - g_entropy[r] * p_v * (log p_v + entropy[r])
+ * from the forward pass's lse and entropy.  Either gradient may be NULL (then
+ * tokens, or entropy, may be too).  Masked places have p = 0; a token outside
+ * [0, V) contributes nothing; a row whose lse is -inf has gradient 0, one
+ * whose lse is NaN has NaN.
+ *
+ *  logits   device, dtype [R][V]; dlogits device, dtype [R][V] (out), may be logits itself
+ */
+VH_API vh_status vh_logits_logprobs_grad(const void* logits, int dtype, int R, int V, int64_t stride,
+                                         const int32_t* tokens, const float* lse, const float* entropy,
+                                         const float* g_logprob, const float* g_entropy, void* dlogits,
+                                         int64_t dlogits_stride, void* stream);
+
+/* Workspace of vh_head_logprobs: 16-byte aligned, its first 16 bytes zeroed
+ * once by the caller (the error word, see vh_workspace_error_offset); about
+ * 4 * V bytes per row (up to 1,024 rows) when alternatives are wanted.  A
+ * buffer serves calls of any sizes that need no more bytes.  0 for a size out
+ * of range. */
+VH_API size_t vh_head_logprobs_workspace_bytes(int R, int V, int top_n);
+
+/*
+ * vh_logits_logprobs over the scores of an output head, which are never
+ * returned: logits[r,v] = sum_h hidden[r,h] * W_full[v,h] (fp32 accumulation
+ * on the tensor cores).  One pass over the head per 1,024 hidden rows.
+ *
+ *  hidden  device, bf16 [R][H], 16-byte aligned
+ *  W_full  device, bf16 [V][H] row-major, 32-byte aligned
+ *  tokens, top_n, outputs: as for vh_logits_logprobs
+ *  R >= 1;  H: 16 <= H <= 65536, H % 16 == 0;  1 <= V <= 2^31 - 1024
+ */
+VH_API vh_status vh_head_logprobs(const void* hidden, const void* W_full, const int32_t* tokens, int R, int H, int V,
+                                  int top_n, float* logprob, float* entropy, float* lse, int32_t* top_ids,
+                                  float* top_logprobs, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

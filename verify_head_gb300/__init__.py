@@ -7,7 +7,9 @@ library is missing, every call raises: there is no fallback.
 
 Entry points mirror the C ABI in include/verifyhead.h:
     mtp_draft_head_argmax, mtp_draft_head_argmax_nvfp4,
-    spec_verify_greedy (spec_verify_greedy_path), vh_workspace_bytes.
+    spec_verify_greedy (spec_verify_greedy_path), vh_workspace_bytes,
+    vh_add_rmsnorm (add_rmsnorm, add_rmsnorm_q8, add_rmsnorm_grad),
+    vh_logits_logprobs (logits_logprobs, logits_logprobs_grad), vh_head_logprobs (head_logprobs).
 """
 from __future__ import annotations
 
@@ -31,6 +33,14 @@ VH_PATH_CUDA_CORE = 1
 VH_PATH_TENSOR = 2
 VH_PATH_WARP_MMA = 3
 
+VH_F32 = 0
+VH_BF16 = 1
+VH_F16 = 2
+
+VH_NORM_SAME = 0
+VH_NORM_INT8 = 1
+VH_NORM_E4M3 = 2
+
 # Every symbol the header declares (checked by the ABI tests).
 EXPORTS = (
     "vh_version", "vh_status_string", "vh_workspace_bytes", "mtp_draft_head_argmax",
@@ -39,6 +49,9 @@ EXPORTS = (
     "vh_selftest_bounded_wait", "spec_verify_greedy_nvfp4", "vh_verify_nvfp4_workspace_bytes",
     "mtp_draft_head_argmax_nvfp4_path", "vh_nvfp4_packed_bytes", "vh_nvfp4_pack",
     "mtp_draft_head_argmax_nvfp4_packed", "spec_verify_greedy_nvfp4_packed",
+    "vh_add_rmsnorm", "vh_add_rmsnorm_grad", "vh_add_rmsnorm_grad_workspace_bytes", "vh_logits_logprobs",
+    "vh_logits_logprobs_workspace_bytes", "vh_logits_logprobs_grad", "vh_head_logprobs",
+    "vh_head_logprobs_workspace_bytes",
 )
 
 
@@ -133,6 +146,24 @@ def _declare(L):
     L.spec_verify_greedy_nvfp4_packed.restype = i32
     L.spec_verify_greedy_nvfp4_packed.argtypes = [vp, vp, ctypes.c_float, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz,
                                                   vp]
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    L.vh_add_rmsnorm.restype = i32
+    L.vh_add_rmsnorm.argtypes = [vp, vp, vp, i32, i32, i32, i32, i64, i64, f32, f32, vp, i64, i32, vp, i64, vp, vp]
+    L.vh_add_rmsnorm_grad_workspace_bytes.restype = sz
+    L.vh_add_rmsnorm_grad_workspace_bytes.argtypes = [i32, i32]
+    L.vh_add_rmsnorm_grad.restype = i32
+    L.vh_add_rmsnorm_grad.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i64, i64, i64, f32, f32, vp, i64, vp, vp, sz,
+                                      vp]
+    L.vh_logits_logprobs_workspace_bytes.restype = sz
+    L.vh_logits_logprobs_workspace_bytes.argtypes = [i32, i32, i32]
+    L.vh_logits_logprobs.restype = i32
+    L.vh_logits_logprobs.argtypes = [vp, i32, i32, i32, i64, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.vh_logits_logprobs_grad.restype = i32
+    L.vh_logits_logprobs_grad.argtypes = [vp, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp, i64, vp]
+    L.vh_head_logprobs_workspace_bytes.restype = sz
+    L.vh_head_logprobs_workspace_bytes.argtypes = [i32, i32, i32]
+    L.vh_head_logprobs.restype = i32
+    L.vh_head_logprobs.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
     L.spec_verify_greedy_path.restype = i32
     L.spec_verify_greedy_path.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp, i32]
 
@@ -397,3 +428,270 @@ def spec_verify_greedy_nvfp4_packed(hidden, packed, tensor_scale, draft_ids, B: 
                                                ws.numel(), _stream_ptr(stream))
     _check(st, "spec_verify_greedy_nvfp4_packed")
     return accept_len, next_ids, row_maxlogit
+
+
+# ----------------------------------------------------------------------------
+# Norm and log probabilities.
+
+_dtypes = {}  # torch dtype -> vh_dtype
+
+
+def _dtype(t, name):
+    if not _dtypes:
+        torch = _torch()
+        _dtypes.update({torch.float32: VH_F32, torch.bfloat16: VH_BF16, torch.float16: VH_F16})
+    d = _dtypes.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name}: float32, bfloat16 or float16 wanted, not {t.dtype}")
+    return d
+
+
+def _device(t):
+    """Device index of a call's first tensor, which must be the current device (the launch goes there)."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("verify_head_gb300 takes CUDA tensors only")
+    if d != _torch().cuda.current_device():
+        raise ValueError(f"the tensors are on device {d}, not on the current device")
+    return d
+
+
+def _place(t, name, dev):
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: a CUDA tensor on device {dev} wanted")
+
+
+def _rows(t, name, dev, shape=None, dtype=None):
+    """Checks a 2-D CUDA tensor whose rows are contiguous; returns the elements between rows."""
+    _place(t, name, dev)
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name}: shape mismatch")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} wanted, not {t.dtype}")
+    rows, width = t.shape
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.stride(0) if rows > 1 else max(width, 1)
+
+
+def _vector(t, name, dev, n, dtype):
+    """Checks a contiguous CUDA tensor of n elements (None passes)."""
+    if t is None:
+        return
+    _place(t, name, dev)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: {n} contiguous elements wanted")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} wanted, not {t.dtype}")
+
+
+def _workspace(ws, dev):
+    """Checks a workspace given by the caller; returns its size."""
+    _place(ws, "ws", dev)
+    if not ws.is_contiguous() or ws.element_size() != 1:
+        raise ValueError("ws: a contiguous uint8 tensor wanted")
+    return ws.numel()
+
+
+def _allocating(stream):
+    """Tensors made in this block belong to the stream the call runs on (they are cleared and reused in its order)."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
+def _norm_weight(weight, x, dev):
+    """(pointer, whether it is fp32) of a norm's weight."""
+    if weight is None:
+        return None, 0
+    f32 = _torch().float32
+    _vector(weight, "weight", dev, x.shape[1], f32 if weight.dtype == f32 else x.dtype)
+    return weight.data_ptr(), int(weight.dtype == f32)
+
+
+def _empty_rows(x):
+    return _torch().empty(x.shape, dtype=x.dtype, device=x.device)
+
+
+def _add_rmsnorm(where, x, residual, weight, eps, weight_offset, y, kind, h, scales, stream):
+    dev = _device(x)
+    dt = _dtype(x, "x")
+    xs = _rows(x, "x", dev)
+    T, H = x.shape
+    rs = _rows(residual, "residual", dev, x.shape, x.dtype) if residual is not None else 0
+    hs = _rows(h, "h", dev, x.shape, x.dtype) if h is not None else 0
+    ys = _rows(y, "y", dev, x.shape)
+    _vector(scales, "scales", dev, T, _torch().float32)
+    w, w32 = _norm_weight(weight, x, dev)
+    st = lib().vh_add_rmsnorm(_ptr(x), _ptr(residual), w, dt, w32, T, H, xs, rs, eps, weight_offset, _ptr(y), ys, kind,
+                              _ptr(h), hs, _ptr(scales), _stream_ptr(stream))
+    _check(st, where)
+
+
+def add_rmsnorm(x, residual=None, weight=None, eps: float = 1e-6, weight_offset: float = 0.0, y=None, h=None,
+                stream=None):
+    """y = rmsnorm(x + residual) * (weight + weight_offset) and the sum h, both in x's type.
+    x, residual [T,H] fp32 / bf16 / fp16 (rows may be strided), weight [H] of x's type or fp32.
+    h may be `residual` itself (updated in place); without a residual h is x and nothing is written.
+    -> (y, h)"""
+    if y is None or (residual is not None and h is None):
+        with _allocating(stream):
+            y = _empty_rows(x) if y is None else y
+            h = _empty_rows(x) if residual is not None and h is None else h
+    if y.dtype != x.dtype:
+        raise ValueError(f"y: {x.dtype} wanted, not {y.dtype}")
+    _add_rmsnorm("add_rmsnorm", x, residual, weight, eps, weight_offset, y, VH_NORM_SAME, h, None, stream)
+    return y, (x if h is None else h)
+
+
+def add_rmsnorm_q8(x, residual=None, weight=None, eps: float = 1e-6, weight_offset: float = 0.0, q=None, scales=None,
+                   h=None, dtype=None, stream=None):
+    """add_rmsnorm with 8-bit rows: q [T,H] (torch.int8, or torch.float8_e4m3fn; `dtype` where q is not given) and
+    scales [T] fp32 with q * scales[:, None] standing for the normed rows.  -> (q, scales, h)"""
+    torch = _torch()
+    if q is None or scales is None or (residual is not None and h is None):
+        with _allocating(stream):
+            q = torch.empty(x.shape, dtype=dtype or torch.int8, device=x.device) if q is None else q
+            scales = torch.empty(x.shape[0], dtype=torch.float32, device=x.device) if scales is None else scales
+            h = _empty_rows(x) if residual is not None and h is None else h
+    if dtype is not None and q.dtype != dtype:
+        raise ValueError(f"q: {dtype} wanted, not {q.dtype}")
+    kind = {torch.int8: VH_NORM_INT8, torch.float8_e4m3fn: VH_NORM_E4M3}.get(q.dtype)
+    if kind is None:
+        raise ValueError(f"q: int8 or float8_e4m3fn wanted, not {q.dtype}")
+    _add_rmsnorm("add_rmsnorm_q8", x, residual, weight, eps, weight_offset, q, kind, h, scales, stream)
+    return q, scales, (x if h is None else h)
+
+
+def add_rmsnorm_grad_workspace(T: int, H: int, device=None):
+    torch = _torch()
+    return torch.empty(int(lib().vh_add_rmsnorm_grad_workspace_bytes(T, H)), dtype=torch.uint8, device=device or "cuda")
+
+
+def add_rmsnorm_grad(dy, h, weight=None, eps: float = 1e-6, weight_offset: float = 0.0, dh=None, dx=None, dweight=None,
+                     ws=None, stream=None):
+    """Gradient of add_rmsnorm from the sum h that it returned: dx [T,H] is the gradient of x and of the residual
+    alike (dh, the gradient that reaches h, included), dweight [H] fp32 (None without a weight).  -> (dx, dweight)"""
+    torch = _torch()
+    dev = _device(h)
+    dt = _dtype(h, "h")
+    hs = _rows(h, "h", dev)
+    T, H = h.shape
+    dys = _rows(dy, "dy", dev, h.shape, h.dtype)
+    dhs = _rows(dh, "dh", dev, h.shape, h.dtype) if dh is not None else 0
+    w, w32 = _norm_weight(weight, h, dev)
+    if weight is None and dweight is not None:
+        raise ValueError("dweight without a weight")
+    if dx is None or (weight is not None and (dweight is None or ws is None)):
+        with _allocating(stream):
+            dx = _empty_rows(h) if dx is None else dx
+            if weight is not None:
+                dweight = torch.empty(H, dtype=torch.float32, device=h.device) if dweight is None else dweight
+                ws = add_rmsnorm_grad_workspace(T, H, h.device) if ws is None else ws
+    dxs = _rows(dx, "dx", dev, h.shape, h.dtype)
+    _vector(dweight, "dweight", dev, H, torch.float32)
+    st = lib().vh_add_rmsnorm_grad(_ptr(dy), _ptr(h), w, _ptr(dh), dt, w32, T, H, dys, hs, dhs, eps, weight_offset,
+                                   _ptr(dx), dxs, _ptr(dweight), _ptr(ws), 0 if ws is None else _workspace(ws, dev),
+                                   _stream_ptr(stream))
+    _check(st, "add_rmsnorm_grad")
+    return dx, dweight
+
+
+def _logprob_outputs(R, top_n, like, dev, stream, given, make_ws):
+    """The five outputs and the workspace, those not given newly made; then checked."""
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    if any(g is None for g in given):
+        with _allocating(stream):
+            shapes = ((R,), (R,), (R,), (R, top_n), (R, top_n))
+            outs = [torch.empty(s, dtype=i32 if i == 3 else f32, device=like.device) if g is None else g
+                    for i, (s, g) in enumerate(zip(shapes, given))]
+            ws = make_ws() if given[5] is None else given[5]
+    else:
+        outs, ws = given[:5], given[5]
+    _vector(outs[0], "logprob", dev, R, f32)
+    _vector(outs[1], "entropy", dev, R, f32)
+    _vector(outs[2], "lse", dev, R, f32)
+    _vector(outs[3], "top_ids", dev, R * top_n, i32)
+    _vector(outs[4], "top_logprobs", dev, R * top_n, f32)
+    return (*outs, ws)
+
+
+def _logprob_results(outs, tokens):
+    return tuple(outs) if tokens is not None else (None, *outs[1:])
+
+
+def logits_logprobs_workspace(R: int, V: int, top_n: int = 0, device=None):
+    """A zeroed workspace for logits_logprobs calls of this R, V and top_n."""
+    torch = _torch()
+    n = int(lib().vh_logits_logprobs_workspace_bytes(R, V, top_n))
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def logits_logprobs(logits, tokens, top_n: int = 0, logprob=None, entropy=None, lse=None, top_ids=None,
+                    top_logprobs=None, ws=None, stream=None):
+    """logits [R,V] fp32 / bf16 / fp16 (rows may be strided), tokens [R] int32 (outside [0,V): no token, logprob 0;
+    None: logprob is None)  -> (logprob [R], entropy [R], lse [R], top_ids [R,top_n] int32, top_logprobs [R,top_n])."""
+    torch = _torch()
+    dev = _device(logits)
+    stride = _rows(logits, "logits", dev)
+    R, V = logits.shape
+    dt = _dtype(logits, "logits")
+    _vector(tokens, "tokens", dev, R, torch.int32)
+    *outs, ws = _logprob_outputs(R, top_n, logits, dev, stream, (logprob, entropy, lse, top_ids, top_logprobs, ws),
+                                 lambda: logits_logprobs_workspace(R, V, top_n, logits.device))
+    st = lib().vh_logits_logprobs(_ptr(logits), dt, R, V, stride, _ptr(tokens), top_n,
+                                  _ptr(outs[0]) if tokens is not None else None, _ptr(outs[1]),
+                                  _ptr(outs[2]), _ptr(outs[3]) if top_n else None, _ptr(outs[4]) if top_n else None,
+                                  _ptr(ws), _workspace(ws, dev), _stream_ptr(stream))
+    _check(st, "logits_logprobs")
+    return _logprob_results(outs, tokens)
+
+
+def logits_logprobs_grad(logits, tokens, lse, entropy=None, g_logprob=None, g_entropy=None, dlogits=None, stream=None):
+    """Gradient of logits_logprobs' logprob and entropy (their gradients [R] fp32, either may be None) with respect to
+    the logits, from the lse and entropy it returned; dlogits may be `logits` itself.  -> dlogits [R,V]"""
+    torch = _torch()
+    dev = _device(logits)
+    stride = _rows(logits, "logits", dev)
+    R, V = logits.shape
+    dt = _dtype(logits, "logits")
+    _vector(tokens, "tokens", dev, R, torch.int32)
+    for t, name in ((lse, "lse"), (entropy, "entropy"), (g_logprob, "g_logprob"), (g_entropy, "g_entropy")):
+        _vector(t, name, dev, R, torch.float32)
+    if dlogits is None:
+        with _allocating(stream):
+            dlogits = _empty_rows(logits)
+    ds = _rows(dlogits, "dlogits", dev, logits.shape, logits.dtype)
+    st = lib().vh_logits_logprobs_grad(_ptr(logits), dt, R, V, stride, _ptr(tokens), _ptr(lse), _ptr(entropy),
+                                       _ptr(g_logprob), _ptr(g_entropy), _ptr(dlogits), ds, _stream_ptr(stream))
+    _check(st, "logits_logprobs_grad")
+    return dlogits
+
+
+def head_logprobs_workspace(R: int, V: int, top_n: int = 0, device=None):
+    """A workspace for head_logprobs calls of this R, V and top_n (about 4 V bytes per row with alternatives)."""
+    torch = _torch()
+    ws = torch.empty(int(lib().vh_head_logprobs_workspace_bytes(R, V, top_n)), dtype=torch.uint8, device=device or "cuda")
+    ws[:16].zero_()
+    return ws
+
+
+def head_logprobs(hidden, W_full, tokens, top_n: int = 0, logprob=None, entropy=None, lse=None, top_ids=None,
+                  top_logprobs=None, ws=None, stream=None):
+    """logits_logprobs of the scores hidden @ W_full.T, which are not returned: hidden [R,H] bf16, W_full [V,H] bf16,
+    tokens [R] int32 -> (logprob [R], entropy [R], lse [R], top_ids [R,top_n] int32, top_logprobs [R,top_n])."""
+    torch = _torch()
+    dev = _device(hidden)
+    _place(W_full, "W_full", dev)
+    _require_cuda(hidden, W_full)
+    R, H = hidden.shape
+    V = W_full.shape[0]
+    if W_full.shape[1] != H or hidden.dtype != torch.bfloat16 or W_full.dtype != torch.bfloat16:
+        raise ValueError("shape/dtype mismatch")
+    _vector(tokens, "tokens", dev, R, torch.int32)
+    *outs, ws = _logprob_outputs(R, top_n, hidden, dev, stream, (logprob, entropy, lse, top_ids, top_logprobs, ws),
+                                 lambda: head_logprobs_workspace(R, V, top_n, hidden.device))
+    st = lib().vh_head_logprobs(_ptr(hidden), _ptr(W_full), _ptr(tokens), R, H, V, top_n,
+                                _ptr(outs[0]) if tokens is not None else None, _ptr(outs[1]), _ptr(outs[2]), _ptr(outs[3]) if top_n else None, _ptr(outs[4]) if top_n else None,
+                                _ptr(ws), _workspace(ws, dev), _stream_ptr(stream))
+    _check(st, "head_logprobs")
+    return _logprob_results(outs, tokens)

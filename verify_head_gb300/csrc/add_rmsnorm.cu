@@ -1,0 +1,489 @@
+// Root-mean-square norm with the residual's addition, with output in the
+// input's type or in 8 bits with one scale per token, and its gradient.
+//
+//     h = x + r            u = h (w + offset)        rstd = 1 / sqrt(mean h^2 + eps)
+//     y = u rstd           8 bits: code = round(u (Q (1 / max|u|))), scale = max|u| rstd / Q
+//
+// The scale of a token is a maximum over the same row that the norm divides
+// by, so rstd cancels in the codes: they depend on h and w alone, not on the
+// order in which the squares are summed.  Q is 127 (int8) or 448 (e4m3).
+//
+// Gradient, with n = h rstd, g = dy (w + offset):
+//     dx = rstd (g - n mean(g n)) + dh        dw = sum over tokens of dy n
+//
+// Bound: memory.  The forward pass reads x, r and writes h, y once (the row
+// stays in registers between the sum and the output); the gradient reads dy,
+// h, dh and writes dx once.  Every sum is in 32 bits.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "vh_kernels.h"
+#include "vh_rows.cuh"
+
+namespace vh {
+namespace norm {
+
+constexpr int kMaxThreads = 512;  // register-resident rows: up to 128 registers a thread
+constexpr int kWideThreads = 512;
+
+// Sums of two values over the warps of one row (threadIdx.y) of the CTA.
+// `max_second`: the second value is a maximum instead of a sum.  All threads
+// of the CTA call it; `slot` alternates between calls.
+template <bool MAX_SECOND>
+__device__ __forceinline__ float2 reduce_row(float a, float b, float2 (*red)[32], int slot) {
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, m);
+        const float o = __shfl_xor_sync(0xFFFFFFFFu, b, m);
+        b = MAX_SECOND ? fmaxf(b, o) : b + o;
+    }
+    const int wpr = blockDim.x >> 5;
+    if (wpr == 1) return make_float2(a, b);
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    float2* row = red[slot] + threadIdx.y * wpr;
+    if (lane == 0) row[w] = make_float2(a, b);
+    __syncthreads();
+    float2 v = lane < wpr ? row[lane] : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) {
+        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, m);
+        const float o = __shfl_xor_sync(0xFFFFFFFFu, v.y, m);
+        v.y = MAX_SECOND ? fmaxf(v.y, o) : v.y + o;
+    }
+    return v;
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_weight(const void* w, int w32, size_t i, float off, float (&f)[VEC]) {
+    if (w == nullptr) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) f[k] = 1.0f + off;
+    } else if (w32) {
+        const float* p = static_cast<const float*>(w) + i;
+        if constexpr (VEC == 1) {
+            f[0] = __ldg(p) + off;
+        } else {
+#pragma unroll
+            for (int k = 0; k < VEC; k += 4) {
+                const float4 q = __ldg(reinterpret_cast<const float4*>(p + k));
+                f[k] = q.x + off;
+                f[k + 1] = q.y + off;
+                f[k + 2] = q.z + off;
+                f[k + 3] = q.w + off;
+            }
+        }
+    } else {
+        RawVec<T, VEC> v;
+        v.load(static_cast<const T*>(w) + i);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) f[k] = v.get(k) + off;
+    }
+}
+
+// How a row's largest |u| becomes codes: u is multiplied by `pre` and then by
+// `inv`.  pre is 1 unless the row is so small that Q / max|u| would overflow.
+struct Quant {
+    float pre, inv;
+};
+__device__ __forceinline__ Quant make_quant(float amax, float q) {
+    Quant z;
+    z.pre = amax < 1e-30f ? 18446744073709551616.0f : 1.0f;
+    z.inv = amax > 0.0f ? q * (1.0f / (amax * z.pre)) : 0.0f;
+    return z;
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&u)[VEC], const Quant& z, int out) {
+    uint32_t b[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        const float v = (u[k] * z.pre) * z.inv;
+        b[k] = out == VH_NORM_INT8 ? (uint32_t)(max(-127, min(127, __float2int_rn(v))) & 0xFF)
+                                   : (uint32_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+    }
+    if constexpr (VEC == 1) {
+        p[0] = (uint8_t)b[0];
+    } else {
+        uint32_t w[VEC / 4];
+#pragma unroll
+        for (int k = 0; k < VEC / 4; ++k)
+            w[k] = b[4 * k] | (b[4 * k + 1] << 8) | (b[4 * k + 2] << 16) | (b[4 * k + 3] << 24);
+        if constexpr (VEC == 8)
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint32_t*>(p) = w[0];
+    }
+}
+
+// One row per threadIdx.y, NV vectors of VEC elements per thread, the row in registers.
+template <typename T, int VEC, int NV>
+__global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a) {
+    __shared__ float2 red[1][32];
+    rows_launch_dependents();
+    rows_wait();
+    const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    const bool live = row < a.T;
+    const int nvec = a.H / VEC;
+    const T* x = static_cast<const T*>(a.x) + (live ? row : 0) * a.x_stride;
+    const T* r = static_cast<const T*>(a.r) + (live ? row : 0) * a.r_stride;
+    T* h = static_cast<T*>(a.h) + (live ? row : 0) * a.h_stride;
+    RawVec<T, VEC> xv[NV], rv[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        if (live && v < nvec) {
+            xv[j].load(x + (size_t)v * VEC);
+            if (a.r != nullptr) rv[j].load(r + (size_t)v * VEC);
+        }
+    }
+    float u[NV][VEC];
+    float ss = 0.f, amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        if (live && v < nvec) {
+            float w[VEC];
+            load_weight<T, VEC>(a.w, a.w32, (size_t)v * VEC, a.w_offset, w);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) u[j][k] = xv[j].get(k) + (a.r != nullptr ? rv[j].get(k) : 0.f);
+            if (a.h != nullptr) {
+                RawVec<T, VEC> o;
+                pack_vec<T, VEC>(o, u[j]);
+                o.store(h + (size_t)v * VEC);
+            }
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                ss = fmaf(u[j][k], u[j][k], ss);
+                u[j][k] *= w[k];
+                amax = fmaxf(amax, fabsf(u[j][k]));
+            }
+        }
+    }
+    const float2 tot = reduce_row<true>(ss, amax, red, 0);
+    const float rstd = 1.0f / sqrtf(tot.x / (float)a.H + a.eps);
+    if (!live) return;
+    if (a.out == VH_NORM_SAME) {
+        T* y = static_cast<T*>(a.y) + row * a.y_stride;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            if (v < nvec) {
+                float f[VEC];
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) f[k] = u[j][k] * rstd;
+                RawVec<T, VEC> o;
+                pack_vec<T, VEC>(o, f);
+                o.store(y + (size_t)v * VEC);
+            }
+        }
+    } else {
+        const float q = a.out == VH_NORM_INT8 ? 127.0f : 448.0f;
+        const Quant z = make_quant(tot.y, q);
+        uint8_t* y = static_cast<uint8_t*>(a.y) + row * a.y_stride;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            if (v < nvec) store_codes<VEC>(y + (size_t)v * VEC, u[j], z, a.out);
+        }
+        if (threadIdx.x == 0) a.scales[row] = tot.y * rstd / q;
+    }
+}
+
+// Rows too wide for registers: one CTA per row, read twice.  Every thread
+// reads an element for the last time just before it writes it, so the outputs
+// may lie on the inputs as in the kernel above.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kWideThreads) k_norm_wide(const NormArgs a) {
+    __shared__ float2 red[1][32];
+    rows_launch_dependents();
+    rows_wait();
+    const long long row = blockIdx.x;
+    const int nvec = a.H / VEC;
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    const T* r = static_cast<const T*>(a.r) + row * a.r_stride;
+    auto load = [&](int v, float (&hv)[VEC], float (&w)[VEC]) {
+        RawVec<T, VEC> xv, rv;
+        xv.load(x + (size_t)v * VEC);
+        if (a.r != nullptr) rv.load(r + (size_t)v * VEC);
+        load_weight<T, VEC>(a.w, a.w32, (size_t)v * VEC, a.w_offset, w);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) hv[k] = xv.get(k) + (a.r != nullptr ? rv.get(k) : 0.f);
+    };
+    float ss = 0.f, amax = 0.f;
+    for (int v = threadIdx.x; v < nvec; v += kWideThreads) {
+        float hv[VEC], w[VEC];
+        load(v, hv, w);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            ss = fmaf(hv[k], hv[k], ss);
+            amax = fmaxf(amax, fabsf(hv[k] * w[k]));
+        }
+    }
+    const float2 tot = reduce_row<true>(ss, amax, red, 0);
+    const float rstd = 1.0f / sqrtf(tot.x / (float)a.H + a.eps);
+    const float q = a.out == VH_NORM_INT8 ? 127.0f : 448.0f;
+    const Quant z = make_quant(tot.y, q);
+    for (int v = threadIdx.x; v < nvec; v += kWideThreads) {
+        float hv[VEC], w[VEC];
+        load(v, hv, w);
+        if (a.h != nullptr) {
+            RawVec<T, VEC> o;
+            pack_vec<T, VEC>(o, hv);
+            o.store(static_cast<T*>(a.h) + row * a.h_stride + (size_t)v * VEC);
+        }
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) hv[k] *= w[k];
+        if (a.out == VH_NORM_SAME) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) hv[k] *= rstd;
+            RawVec<T, VEC> o;
+            pack_vec<T, VEC>(o, hv);
+            o.store(static_cast<T*>(a.y) + row * a.y_stride + (size_t)v * VEC);
+        } else {
+            store_codes<VEC>(static_cast<uint8_t*>(a.y) + row * a.y_stride + (size_t)v * VEC, hv, z, a.out);
+        }
+    }
+    if (a.out != VH_NORM_SAME && threadIdx.x == 0) a.scales[row] = tot.y * rstd / q;
+}
+
+// ---------------------------------------------------------------------------
+// Gradient.  CTA c takes tokens c, c + grid, ...; a thread keeps its columns'
+// share of dw in registers and leaves it in part[c][H]; a second kernel adds
+// the shares in CTA order, so the sums do not change from call to call.
+
+template <typename T, int VEC, int NV>
+__global__ void __launch_bounds__(kMaxThreads) k_norm_grad(const NormGradArgs a) {
+    __shared__ float2 red[2][32];
+    rows_launch_dependents();
+    rows_wait();
+    const int nvec = a.H / VEC;
+    float dw[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) dw[j][k] = 0.f;
+    int slot = 0;
+    for (long long row = blockIdx.x; row < a.T; row += gridDim.x, slot ^= 1) {
+        const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
+        const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
+        const T* dh = static_cast<const T*>(a.dh) + row * a.dh_stride;
+        RawVec<T, VEC> hv[NV], yv[NV], ev[NV];
+        float w[NV][VEC];
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            if (v < nvec) {
+                hv[j].load(h + (size_t)v * VEC);
+                yv[j].load(dy + (size_t)v * VEC);
+                if (a.dh != nullptr) ev[j].load(dh + (size_t)v * VEC);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            if (v < nvec) {
+                load_weight<T, VEC>(a.w, a.w32, (size_t)v * VEC, a.w_offset, w[j]);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) {
+                    const float f = hv[j].get(k);
+                    ss = fmaf(f, f, ss);
+                    dot = fmaf(yv[j].get(k) * w[j][k], f, dot);
+                }
+            }
+        }
+        const float2 tot = reduce_row<false>(ss, dot, red, slot);
+        const float rstd = 1.0f / sqrtf(tot.x / (float)a.H + a.eps);
+        const float mean = tot.y * rstd / (float)a.H;  // mean(g n)
+        T* dx = static_cast<T*>(a.dx) + row * a.dx_stride;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            if (v < nvec) {
+                float f[VEC];
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) {
+                    const float n = hv[j].get(k) * rstd, d = yv[j].get(k);
+                    dw[j][k] = fmaf(d, n, dw[j][k]);
+                    f[k] = fmaf(rstd, fmaf(-n, mean, d * w[j][k]), a.dh != nullptr ? ev[j].get(k) : 0.f);
+                }
+                RawVec<T, VEC> o;
+                pack_vec<T, VEC>(o, f);
+                o.store(dx + (size_t)v * VEC);
+            }
+        }
+    }
+    if (a.part == nullptr) return;
+    float* p = a.part + (size_t)blockIdx.x * a.H;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        if (v < nvec)
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) p[(size_t)v * VEC + k] = dw[j][k];
+    }
+}
+
+// Rows too wide for registers: read twice; the CTA's share of dw lives in its
+// part[c] row, each element touched by one thread only.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kWideThreads) k_norm_grad_wide(const NormGradArgs a) {
+    __shared__ float2 red[2][32];
+    rows_launch_dependents();
+    rows_wait();
+    const int nvec = a.H / VEC;
+    float* p = a.part == nullptr ? nullptr : a.part + (size_t)blockIdx.x * a.H;
+    int slot = 0;
+    bool first = true;
+    for (long long row = blockIdx.x; row < a.T; row += gridDim.x, slot ^= 1, first = false) {
+        const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
+        const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
+        const T* dh = static_cast<const T*>(a.dh) + row * a.dh_stride;
+        T* dx = static_cast<T*>(a.dx) + row * a.dx_stride;
+        float ss = 0.f, dot = 0.f;
+        for (int v = threadIdx.x; v < nvec; v += kWideThreads) {
+            RawVec<T, VEC> hv, yv;
+            float w[VEC];
+            hv.load(h + (size_t)v * VEC);
+            yv.load(dy + (size_t)v * VEC);
+            load_weight<T, VEC>(a.w, a.w32, (size_t)v * VEC, a.w_offset, w);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                const float f = hv.get(k);
+                ss = fmaf(f, f, ss);
+                dot = fmaf(yv.get(k) * w[k], f, dot);
+            }
+        }
+        const float2 tot = reduce_row<false>(ss, dot, red, slot);
+        const float rstd = 1.0f / sqrtf(tot.x / (float)a.H + a.eps);
+        const float mean = tot.y * rstd / (float)a.H;
+        for (int v = threadIdx.x; v < nvec; v += kWideThreads) {
+            RawVec<T, VEC> hv, yv, ev;
+            float w[VEC], f[VEC];
+            hv.load(h + (size_t)v * VEC);
+            yv.load(dy + (size_t)v * VEC);
+            if (a.dh != nullptr) ev.load(dh + (size_t)v * VEC);
+            load_weight<T, VEC>(a.w, a.w32, (size_t)v * VEC, a.w_offset, w);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                const float n = hv.get(k) * rstd, d = yv.get(k);
+                if (p != nullptr) {
+                    float* q = p + (size_t)v * VEC + k;
+                    *q = fmaf(d, n, first ? 0.f : *q);
+                }
+                f[k] = fmaf(rstd, fmaf(-n, mean, d * w[k]), a.dh != nullptr ? ev.get(k) : 0.f);
+            }
+            RawVec<T, VEC> o;
+            pack_vec<T, VEC>(o, f);
+            o.store(dx + (size_t)v * VEC);
+        }
+    }
+}
+
+// dweight[c] = sum of part[0..n)[c], in order: 32 columns x 16 row groups per CTA.
+constexpr int kSumGroups = 16;
+__global__ void __launch_bounds__(32 * kSumGroups) k_sum_parts(const float* part, int n, int H, float* out) {
+    __shared__ float s[kSumGroups][33];
+    rows_launch_dependents();
+    rows_wait();
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    float v = 0.f;
+    if (c < H)
+        for (int r = threadIdx.y; r < n; r += kSumGroups) v += part[(size_t)r * H + c];
+    s[threadIdx.y][threadIdx.x] = v;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < H) {
+        float t = 0.f;
+#pragma unroll
+        for (int g = 0; g < kSumGroups; ++g) t += s[g][threadIdx.x];
+        out[c] = t;
+    }
+}
+
+template <typename... P, typename... A>
+static cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+static inline bool mult16(const void* p, long long stride_elems, int size) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (stride_elems * size) % 16 == 0;
+}
+
+// Threads per row (a multiple of 32) for nvec vectors, nv per thread.
+static inline int row_threads(int nvec, int nv) { return ((nvec + nv - 1) / nv + 31) / 32 * 32; }
+
+template <typename T, int VEC>
+static cudaError_t norm_vec(const NormArgs& a, cudaStream_t s) {
+    const int nvec = a.H / VEC;
+    auto go = [&](auto kernel, int nv) {
+        const int tx = row_threads(nvec, nv);
+        const int ty = std::max(1, 128 / tx);
+        return launch(kernel, dim3((unsigned)((a.T + ty - 1) / ty)), dim3(tx, ty), s, a);
+    };
+    if (nvec <= kMaxThreads) return go(k_norm<T, VEC, 1>, 1);
+    if (nvec <= kMaxThreads * 2) return go(k_norm<T, VEC, 2>, 2);
+    if (nvec <= kMaxThreads * 4) return go(k_norm<T, VEC, 4>, 4);
+    return launch(k_norm_wide<T, VEC>, dim3((unsigned)a.T), dim3(kWideThreads), s, a);
+}
+
+template <typename T>
+static cudaError_t norm_type(const NormArgs& a, cudaStream_t s) {
+    constexpr int V = kVecOf<T>;
+    const int size = (int)sizeof(T);
+    const bool q8 = a.out != VH_NORM_SAME;
+    const bool vec = a.H % V == 0 && mult16(a.x, a.x_stride, size) && (!a.r || mult16(a.r, a.r_stride, size)) &&
+                     (!a.h || mult16(a.h, a.h_stride, size)) && (!a.w || mult16(a.w, 0, size)) &&
+                     (q8 ? (reinterpret_cast<uintptr_t>(a.y) % V == 0 && a.y_stride % V == 0)
+                         : mult16(a.y, a.y_stride, size));
+    return vec ? norm_vec<T, V>(a, s) : norm_vec<T, 1>(a, s);
+}
+
+template <typename T, int VEC>
+static cudaError_t grad_vec(const NormGradArgs& a, cudaStream_t s) {
+    const int nvec = a.H / VEC;
+    const dim3 grid((unsigned)norm_grad_parts(a.T));
+    if (nvec <= kMaxThreads) return launch(k_norm_grad<T, VEC, 1>, grid, dim3(row_threads(nvec, 1)), s, a);
+    if (nvec <= kMaxThreads * 2) return launch(k_norm_grad<T, VEC, 2>, grid, dim3(row_threads(nvec, 2)), s, a);
+    return launch(k_norm_grad_wide<T, VEC>, grid, dim3(kWideThreads), s, a);
+}
+
+template <typename T>
+static cudaError_t grad_type(const NormGradArgs& a, cudaStream_t s) {
+    constexpr int V = kVecOf<T>;
+    const int size = (int)sizeof(T);
+    const bool vec = a.H % V == 0 && mult16(a.h, a.h_stride, size) && mult16(a.dy, a.dy_stride, size) &&
+                     (!a.dh || mult16(a.dh, a.dh_stride, size)) && mult16(a.dx, a.dx_stride, size) &&
+                     (!a.w || mult16(a.w, 0, size));
+    return vec ? grad_vec<T, V>(a, s) : grad_vec<T, 1>(a, s);
+}
+
+}  // namespace norm
+
+int norm_grad_parts(int T) { return std::min(T, kNormGradParts); }
+
+cudaError_t launch_add_rmsnorm(const NormArgs& a, int dtype, cudaStream_t s) {
+    if (dtype == VH_BF16) return norm::norm_type<__nv_bfloat16>(a, s);
+    if (dtype == VH_F16) return norm::norm_type<__half>(a, s);
+    return norm::norm_type<float>(a, s);
+}
+
+cudaError_t launch_add_rmsnorm_grad(const NormGradArgs& a, int dtype, float* dweight, cudaStream_t s) {
+    cudaError_t e = dtype == VH_BF16  ? norm::grad_type<__nv_bfloat16>(a, s)
+                    : dtype == VH_F16 ? norm::grad_type<__half>(a, s)
+                                      : norm::grad_type<float>(a, s);
+    if (e != cudaSuccess || dweight == nullptr) return e;
+    return norm::launch(norm::k_sum_parts, dim3((unsigned)((a.H + 31) / 32)), dim3(32, norm::kSumGroups), s,
+                        (const float*)a.part, norm_grad_parts(a.T), a.H, dweight);
+}
+
+}  // namespace vh

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "../../include/verifyhead.h"
 #include "vh_kernels.h"
@@ -20,6 +21,10 @@ constexpr int kMmaRows = 16;   // hidden rows per warp-MMA launch (8 when H > 51
 constexpr int kTcFp4Rows = 16;  // hidden rows per tensor-core 4-bit draft launch
 constexpr int kMmaFp4Rows = 8;  // hidden rows per warp-level-MMA 4-bit launch
 constexpr int kPackedRows = 16;  // hidden rows per pass over a tiled 4-bit head
+constexpr int kMaxNormH = 1 << 24;              // width of a normed row
+constexpr int kMaxLogprobV = 2147483647 - 1023;  // vocabulary of the log probabilities: tile ends stay in 31 bits
+inline bool known_dtype(int d) { return d == VH_F32 || d == VH_BF16 || d == VH_F16; }
+inline uintptr_t dtype_size(int d) { return d == VH_F32 ? 4 : 2; }
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 vh_status check_device() {
@@ -432,6 +437,179 @@ vh_status spec_verify_greedy(const void* hidden, const void* W_full, const int32
                              size_t ws_bytes, void* stream) {
     return spec_verify_greedy_path(hidden, W_full, draft_ids, B, k, H, V, accept_len, next_ids, row_maxlogit, ws,
                                    ws_bytes, stream, VH_PATH_AUTO);
+}
+
+// ---------------------------------------------------------------------------
+// Norm and log probabilities.
+
+vh_status vh_add_rmsnorm(const void* x, const void* residual, const void* weight, int dtype, int weight_f32, int T,
+                         int H, int64_t x_stride, int64_t residual_stride, float eps, float weight_offset, void* y,
+                         int64_t y_stride, int out, void* h, int64_t h_stride, float* scales, void* stream) {
+    if (!x || !y) return VH_ERR_NULL;
+    if (!known_dtype(dtype) || out < VH_NORM_SAME || out > VH_NORM_E4M3) return VH_ERR_SHAPE;
+    if (out != VH_NORM_SAME && !scales) return VH_ERR_NULL;
+    if (T < 1 || H < 1 || H > kMaxNormH) return VH_ERR_SHAPE;
+    if (x_stride < H || y_stride < H || (residual && residual_stride < H) || (h && h_stride < H)) return VH_ERR_SHAPE;
+    if (!(eps >= 0.0f) || !(eps < 3.0e38f) || !(std::fabs(weight_offset) < 3.0e38f)) return VH_ERR_SHAPE;
+    const uintptr_t sz = dtype_size(dtype);
+    if (!aligned(x, sz) || !aligned(residual, sz) || !aligned(weight, weight_f32 ? 4 : sz) || !aligned(h, sz) ||
+        !aligned(y, out == VH_NORM_SAME ? sz : 1) || (out != VH_NORM_SAME && !aligned(scales, 4)))
+        return VH_ERR_ALIGN;
+    vh_status st = check_device();
+    if (st != VH_OK) return st;
+    vh::NormArgs a{};
+    a.x = x;
+    a.r = residual;
+    a.w = weight;
+    a.h = h;
+    a.y = y;
+    a.scales = scales;
+    a.x_stride = x_stride;
+    a.r_stride = residual_stride;
+    a.h_stride = h_stride;
+    a.y_stride = y_stride;
+    a.T = T;
+    a.H = H;
+    a.w32 = weight_f32 != 0 || dtype == VH_F32;
+    a.out = out;
+    a.eps = eps;
+    a.w_offset = weight_offset;
+    return launch_status(vh::launch_add_rmsnorm(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t vh_add_rmsnorm_grad_workspace_bytes(int T, int H) {
+    if (T < 1 || H < 1) return 0;
+    return vh::round16((size_t)vh::norm_grad_parts(T) * (size_t)H * 4);
+}
+
+vh_status vh_add_rmsnorm_grad(const void* dy, const void* h, const void* weight, const void* dh, int dtype,
+                              int weight_f32, int T, int H, int64_t dy_stride, int64_t h_stride, int64_t dh_stride,
+                              float eps, float weight_offset, void* dx, int64_t dx_stride, float* dweight, void* ws,
+                              size_t ws_bytes, void* stream) {
+    if (!dy || !h || !dx || (dweight && !ws)) return VH_ERR_NULL;
+    if (!known_dtype(dtype) || T < 1 || H < 1 || H > kMaxNormH) return VH_ERR_SHAPE;
+    if (dy_stride < H || h_stride < H || dx_stride < H || (dh && dh_stride < H)) return VH_ERR_SHAPE;
+    if (!(eps >= 0.0f) || !(eps < 3.0e38f) || !(std::fabs(weight_offset) < 3.0e38f)) return VH_ERR_SHAPE;
+    const uintptr_t sz = dtype_size(dtype);
+    if (!aligned(dy, sz) || !aligned(h, sz) || !aligned(dh, sz) || !aligned(dx, sz) ||
+        !aligned(weight, weight_f32 ? 4 : sz) || !aligned(dweight, 4) || (dweight && !aligned(ws, 16)))
+        return VH_ERR_ALIGN;
+    if (dweight && ws_bytes < vh_add_rmsnorm_grad_workspace_bytes(T, H)) return VH_ERR_WORKSPACE;
+    vh_status st = check_device();
+    if (st != VH_OK) return st;
+    vh::NormGradArgs a{};
+    a.dy = dy;
+    a.h = h;
+    a.w = weight;
+    a.dh = dh;
+    a.dx = dx;
+    a.part = dweight ? static_cast<float*>(ws) : nullptr;
+    a.dy_stride = dy_stride;
+    a.h_stride = h_stride;
+    a.dh_stride = dh_stride;
+    a.dx_stride = dx_stride;
+    a.T = T;
+    a.H = H;
+    a.w32 = weight_f32 != 0 || dtype == VH_F32;
+    a.eps = eps;
+    a.w_offset = weight_offset;
+    return launch_status(vh::launch_add_rmsnorm_grad(a, dtype, dweight, static_cast<cudaStream_t>(stream)));
+}
+
+size_t vh_logits_logprobs_workspace_bytes(int R, int V, int top_n) {
+    if (R < 1 || V < 1 || V > kMaxLogprobV || top_n < 0 || top_n > vh::kMaxTop) return 0;
+    return vh::logits_logprobs_ws_bytes(R, V, top_n);
+}
+
+vh_status vh_logits_logprobs(const void* logits, int dtype, int R, int V, int64_t stride, const int32_t* tokens,
+                             int top_n, float* logprob, float* entropy, float* lse, int32_t* top_ids,
+                             float* top_logprobs, void* ws, size_t ws_bytes, void* stream) {
+    if (!logits || !ws || (logprob && !tokens) || (top_n > 0 && (!top_ids || !top_logprobs))) return VH_ERR_NULL;
+    if (!known_dtype(dtype) || R < 1 || V < 1 || V > kMaxLogprobV || stride < V || top_n < 0 || top_n > vh::kMaxTop)
+        return VH_ERR_SHAPE;
+    if (!aligned(logits, dtype_size(dtype)) || !aligned(tokens, 4) || !aligned(logprob, 4) || !aligned(entropy, 4) ||
+        !aligned(lse, 4) || (top_n > 0 && (!aligned(top_ids, 4) || !aligned(top_logprobs, 4))) || !aligned(ws, 16))
+        return VH_ERR_ALIGN;
+    if (ws_bytes < vh_logits_logprobs_workspace_bytes(R, V, top_n)) return VH_ERR_WORKSPACE;
+    vh_status st = check_device();
+    if (st != VH_OK) return st;
+    vh::LogprobArgs a{};
+    a.logits = logits;
+    a.stride = stride;
+    a.R = R;
+    a.V = V;
+    a.top_n = top_n;
+    a.tokens = tokens;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.lse = lse;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.ws = ws;
+    return launch_status(vh::launch_logits_logprobs(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+vh_status vh_logits_logprobs_grad(const void* logits, int dtype, int R, int V, int64_t stride, const int32_t* tokens,
+                                  const float* lse, const float* entropy, const float* g_logprob,
+                                  const float* g_entropy, void* dlogits, int64_t dlogits_stride, void* stream) {
+    if (!logits || !lse || !dlogits || (g_logprob && !tokens) || (g_entropy && !entropy)) return VH_ERR_NULL;
+    if (!known_dtype(dtype) || R < 1 || V < 1 || V > kMaxLogprobV || stride < V || dlogits_stride < V)
+        return VH_ERR_SHAPE;
+    const uintptr_t sz = dtype_size(dtype);
+    if (!aligned(logits, sz) || !aligned(dlogits, sz) || !aligned(tokens, 4) || !aligned(lse, 4) ||
+        !aligned(entropy, 4) || !aligned(g_logprob, 4) || !aligned(g_entropy, 4))
+        return VH_ERR_ALIGN;
+    vh_status st = check_device();
+    if (st != VH_OK) return st;
+    vh::LogprobGradArgs a{};
+    a.logits = logits;
+    a.dlogits = dlogits;
+    a.stride = stride;
+    a.d_stride = dlogits_stride;
+    a.R = R;
+    a.V = V;
+    a.tokens = tokens;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.g_logprob = g_logprob;
+    a.g_entropy = g_entropy;
+    return launch_status(vh::launch_logits_logprobs_grad(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t vh_head_logprobs_workspace_bytes(int R, int V, int top_n) {
+    if (R < 1 || V < 1 || V > kMaxLogprobV || top_n < 0 || top_n > vh::kMaxTop) return 0;
+    return vh::head_logprobs_ws_bytes(R, V, top_n);
+}
+
+vh_status vh_head_logprobs(const void* hidden, const void* W_full, const int32_t* tokens, int R, int H, int V,
+                           int top_n, float* logprob, float* entropy, float* lse, int32_t* top_ids,
+                           float* top_logprobs, void* ws, size_t ws_bytes, void* stream) {
+    if (!hidden || !W_full || !ws || (logprob && !tokens) || (top_n > 0 && (!top_ids || !top_logprobs)))
+        return VH_ERR_NULL;
+    if (R < 1 || H < 16 || H > kMaxH || H % 16 != 0 || V < 1 || V > kMaxLogprobV || top_n < 0 || top_n > vh::kMaxTop)
+        return VH_ERR_SHAPE;
+    if (!aligned(hidden, 16) || !aligned(W_full, 32) || !aligned(tokens, 4) || !aligned(logprob, 4) ||
+        !aligned(entropy, 4) || !aligned(lse, 4) ||
+        (top_n > 0 && (!aligned(top_ids, 4) || !aligned(top_logprobs, 4))) || !aligned(ws, 16))
+        return VH_ERR_ALIGN;
+    if (ws_bytes < vh_head_logprobs_workspace_bytes(R, V, top_n)) return VH_ERR_WORKSPACE;
+    vh_status st = check_device();
+    if (st != VH_OK) return st;
+    vh::HeadLogprobArgs a{};
+    a.x = static_cast<const uint16_t*>(hidden);
+    a.W = static_cast<const uint16_t*>(W_full);
+    a.R = R;
+    a.H = H;
+    a.V = V;
+    a.top_n = top_n;
+    a.tokens = tokens;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.lse = lse;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.ws = ws;
+    return launch_status(vh::launch_head_logprobs(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

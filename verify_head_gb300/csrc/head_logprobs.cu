@@ -1,0 +1,666 @@
+// Log probabilities of given tokens straight from hidden rows and the output
+// head: the scores S = W Xt come from the tensor cores (tcgen05 + TMEM + TMA)
+// and are reduced to each row's softmax statistics as they leave TMEM.
+//
+//     S[r,v] = sum_h X[r,h] W[v,h]     lse, logprob, entropy, alternatives of S[r,:]
+//
+// Contraction.  As in verification: A = 128 head rows per CTA (K-major, ring
+// of 64-element K stages by TMA), B = the hidden rows, fp32 accumulators in
+// two TMEM buffers, so that the epilogue of a tile runs under the MMAs of the
+// next.  Up to 128 hidden rows: one CTA per tile of 128 head rows.  More: CTA
+// pairs (cta_group::2) on 256 head rows x 256 hidden rows, and up to four
+// groups of 256 hidden rows per pass over the head: pair p takes row group
+// p % groups, so the pairs that need the same head tile ask for it at about
+// the same time and it comes from HBM once.
+//
+// Epilogue.  An accumulator lane is a head row and a column a hidden row, but
+// a row's softmax runs over head rows.  Each warp turns its 32 x 32 blocks in
+// shared memory (row pitch 36 floats: neither side has bank conflicts) and
+// then lane = hidden row: 32 scores in registers, a running maximum and the
+// sums of Stat per hidden row, kept across tiles.  That costs about 10
+// instructions per score and thread, under a tenth of the MMA time at H = 2048.
+//
+// Alternatives.  Where they are wanted each block of 32 head rows (a segment)
+// leaves its maximum and its 32 scores per hidden row in the workspace.  The
+// n largest scores of a row lie in the n segments with the largest maxima (see
+// the logits' kernel), so the finishing kernel reads the maxima and n blocks
+// of 128 bytes per row.
+//
+// Every wait is bounded; on expiry the workspace error word is set and the
+// CTA drains its copies, frees TMEM and returns.
+#include <algorithm>
+#include <atomic>
+
+#include "vh_kernels.h"
+#include "vh_rows.cuh"
+#include "vh_tc.cuh"
+
+namespace vh {
+namespace hlp {
+
+using namespace tc;
+using ptx::mbar_arrive;
+using ptx::mbar_arrive_expect_tx;
+using ptx::mbar_drain;
+using ptx::mbar_init;
+using ptx::mbar_wait;
+using ptx::policy_evict_first;
+using ptx::policy_evict_last;
+
+constexpr int kTileM = 128;             // head rows per CTA and tile
+constexpr int kPairTile = 2 * kTileM;   // head rows per pair and tile
+constexpr int kGroup = 256;             // hidden rows per row group (MMA N)
+constexpr int kMaxGroups = 4;           // row groups per pass over the head
+constexpr int kPassRows = kGroup * kMaxGroups;
+constexpr int kOneCtaRows = 128;
+constexpr int kThreadsH = 192;
+constexpr int kMaxStages = 8;
+constexpr int kStageW = kTileM * kBlockK * 2;  // 16 KiB
+constexpr int kTmemCols = 512;
+constexpr int kSeg = 32;                // head rows per segment
+constexpr int kPitch = 36;              // floats per hidden row of a transposed block
+constexpr int kTransBytes = 32 * kPitch * 4;  // per epilogue warp
+constexpr int kMaxParts = 512;          // CTAs that leave statistics of one row
+static_assert(kGroup * 3 * 4 <= kTransBytes, "a warp's statistics fit its block");
+
+struct alignas(8) Bars {
+    unsigned long long full[kMaxStages];
+    unsigned long long empty[kMaxStages];
+    unsigned long long tmem_full[2];
+    unsigned long long tmem_empty[2];
+    unsigned long long mma_done;
+    unsigned int tmem_base;
+    unsigned int pad;
+};
+
+struct Args {
+    int R;       // hidden rows of this pass
+    int Rp;      // row pitch of the workspace arrays
+    int N;       // one CTA: MMA N (R rounded up to 16)
+    int H, V;
+    int groups;  // row groups (pairs)
+    const int32_t* tokens;
+    float* tok_score;  // [Rp]
+    float4* part;      // [CTA of the row group][Rp]: c, s, t
+    float* seg_max;    // [segment][Rp], null: no alternatives
+    float* scores;     // [segment][Rp][32]
+    unsigned int* err;
+};
+
+__host__ __device__ constexpr size_t smem_bytes(int stages, int nmax) {
+    return 1024 + (size_t)stages * (kStageW + (size_t)nmax * kBlockK * 2) + sizeof(Bars) + 4 * kTransBytes + 64;
+}
+
+// ---------------------------------------------------------------------------
+// Epilogue of one warp: NG groups of 32 hidden rows (row = row0 + 32 g + lane).
+
+template <int NG>
+struct Epilogue {
+    Stat st[NG];
+    int tok[NG];
+    float* tr;
+
+    __device__ __forceinline__ void begin(const Args& a, int row0, float* tr_) {
+        tr = tr_;
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const int row = row0 + g * 32 + lane;
+            st[g] = stat_none();
+            tok[g] = (a.tokens != nullptr && row < a.R) ? a.tokens[row] : -1;
+        }
+    }
+
+    // v[j]: the score of head row v0 + lane for column j of group g.
+    __device__ __forceinline__ void block(const Args& a, int g, int row0, int v0, const float (&v)[32]) {
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) tr[j * kPitch + lane] = v[j];
+        __syncwarp();
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 q = *reinterpret_cast<const float4*>(tr + lane * kPitch + 4 * i);
+            x[4 * i] = q.x;
+            x[4 * i + 1] = q.y;
+            x[4 * i + 2] = q.z;
+            x[4 * i + 3] = q.w;
+        }
+        const int row = row0 + g * 32 + lane;
+        const int n = a.V - v0;  // head rows of this block
+        const unsigned int at = (unsigned int)(tok[g] - v0);
+        if (at < 32u && (int)at < n && row < a.R) a.tok_score[row] = tr[lane * kPitch + at];
+        if (n < 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i >= n) x[i] = neg_inf();
+        }
+        float m = neg_inf();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m = fmaxf(m, x[i]);
+        if (a.seg_max != nullptr && row < a.R) {
+            const size_t o = (size_t)(v0 / kSeg) * a.Rp + row;
+            a.seg_max[o] = m;
+            float4* p = reinterpret_cast<float4*>(a.scores + o * kSeg);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        }
+        if (m > st[g].c) stat_shift(st[g], m);
+        if (st[g].c != neg_inf()) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) stat_add(st[g], x[i]);
+        }
+    }
+
+    // The warp's statistics of every hidden row, for the CTA to join.
+    __device__ __forceinline__ void leave() {
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            float* p = tr + (g * 32 + lane) * 3;
+            p[0] = st[g].c;
+            p[1] = st[g].s;
+            p[2] = st[g].t;
+        }
+    }
+};
+
+// After __syncthreads: join the four warps' statistics of rows row0 .. row0 + n.
+__device__ __forceinline__ void publish(const Args& a, const float* trans, int slot, int row0, int n) {
+    for (int r = threadIdx.x; r < n; r += blockDim.x) {
+        Stat s = stat_none();
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float* p = trans + w * (kTransBytes / 4) + r * 3;
+            s = stat_join(s, Stat{p[0], p[1], p[2]});
+        }
+        a.part[(size_t)slot * a.Rp + row0 + r] = make_float4(s.c, s.s, s.t, 0.f);
+    }
+}
+
+__device__ __forceinline__ void init_bars(Bars* b, int stages, int empty_arrivals) {
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&b->full[s], 1);
+            mbar_init(&b->empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b->tmem_full[i], 1);
+            mbar_init(&b->tmem_empty[i], empty_arrivals);
+        }
+        mbar_init(&b->mma_done, 1);
+        ptx::fence_barrier_init();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Up to 128 hidden rows: one CTA per tile.  Warp 0 = TMA producer, warp 1 =
+// TMEM owner and MMA issuer, warps 2..5 = epilogue (TMEM lane quarter = warp % 4).
+
+template <int STAGES, int NMAX>
+__global__ void __launch_bounds__(kThreadsH, 1)
+    k_head_logprobs(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a) {
+    constexpr int kStageX = NMAX * kBlockK * 2;
+    constexpr int NG = NMAX / 32;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* stage_w = smem;
+    uint8_t* stage_x = smem + (size_t)STAGES * kStageW;
+    float* trans = reinterpret_cast<float*>(stage_x + (size_t)STAGES * kStageX);
+    Bars* bars = reinterpret_cast<Bars*>(reinterpret_cast<uint8_t*>(trans) + 4 * kTransBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int k_stages = (a.H + kBlockK - 1) / kBlockK;  // TMA fills past H with zeros
+    const int n_tiles = (a.V + kTileM - 1) / kTileM;
+
+    init_bars(bars, STAGES, 4);
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&bars->tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = bars->tmem_base;
+    rows_launch_dependents();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // The head is read before the previous kernel is waited for, everything else after.
+            const unsigned long long pol_w = policy_evict_first(), pol_x = policy_evict_last();
+            uint32_t it = 0;
+            bool ok = true, waited = false;
+            auto release_first_ring = [&](uint32_t n) {
+                rows_wait();
+                for (uint32_t j = 0; j < n; ++j)
+                    tma_load_2d(stage_x + (size_t)j * kStageX, &map_x, &bars->full[j], (int)(j % k_stages) * kBlockK, 0,
+                                pol_x);
+                waited = true;
+            };
+            for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
+                for (int ks = 0; ks < k_stages; ++ks, ++it) {
+                    const int s = it % STAGES;
+                    if (!mbar_wait(&bars->empty[s], ((it / STAGES) & 1u) ^ 1u, a.err)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&bars->full[s], (uint32_t)(kStageW + a.N * kBlockK * 2));
+                    tma_load_2d(stage_w + (size_t)s * kStageW, &map_w, &bars->full[s], ks * kBlockK, tile * kTileM, pol_w);
+                    if (waited)
+                        tma_load_2d(stage_x + (size_t)s * kStageX, &map_x, &bars->full[s], ks * kBlockK, 0, pol_x);
+                    else if (it + 1 == (uint32_t)STAGES)
+                        release_first_ring(it + 1);
+                }
+            }
+            if (!waited) release_first_ring(it);
+            for (uint32_t j = (it > (uint32_t)STAGES ? it - STAGES : 0); j < it; ++j)
+                mbar_drain(&bars->full[j % STAGES], (j / STAGES) & 1u);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16(kTileM, a.N);
+            uint32_t it = 0, local = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x, ++local) {
+                const uint32_t buf = local & 1u;
+                if (!mbar_wait(&bars->tmem_empty[buf], ((local >> 1) & 1u) ^ 1u, a.err)) break;
+                tc_fence_after();
+                for (int ks = 0; ks < k_stages; ++ks, ++it) {
+                    const int s = it % STAGES;
+                    if (!mbar_wait(&bars->full[s], (it / STAGES) & 1u, a.err)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sw = smem_u32(stage_w + (size_t)s * kStageW);
+                    const uint32_t sx = smem_u32(stage_x + (size_t)s * kStageX);
+#pragma unroll
+                    for (int kk = 0; kk < kBlockK / 16; ++kk)
+                        mma_bf16(tmem_base + buf * 256u, smem_desc_sw128(sw + kk * 32), smem_desc_sw128(sx + kk * 32),
+                                 idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(&bars->empty[s]);
+                }
+                if (ok) mma_commit(&bars->tmem_full[buf]);
+            }
+            mma_commit(&bars->mma_done);
+            mbar_drain(&bars->mma_done, 0u);
+        }
+    } else {
+        rows_wait();
+        const int quarter = warp & 3;
+        Epilogue<NG> ep;
+        ep.begin(a, 0, trans + quarter * (kTransBytes / 4));
+        const int ngroups = (a.N + 31) / 32;
+        uint32_t local = 0;
+        for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x, ++local) {
+            const uint32_t buf = local & 1u;
+            if (!mbar_wait(&bars->tmem_full[buf], (local >> 1) & 1u, a.err)) break;
+            tc_fence_after();
+            const int v0 = tile * kTileM + quarter * 32;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                if (g < ngroups) {
+                    float v[32];
+                    tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * 256u + g * 32u, v);
+                    if (g + 1 == ngroups) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars->tmem_empty[buf]);
+                    }
+                    if (v0 < a.V) ep.block(a, g, 0, v0, v);
+                }
+            }
+        }
+        ep.leave();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols)
+                     : "memory");
+    }
+    rows_wait();
+    publish(a, trans, blockIdx.x, 0, a.R);
+}
+
+// ---------------------------------------------------------------------------
+// More hidden rows: CTA pairs.  Each CTA stages its 128 head rows and half of
+// the row group's hidden rows; the leader issues the MMAs; each CTA's TMEM
+// holds the accumulators of its own head rows.
+
+constexpr int kStages2 = 6;
+constexpr int kStageX2 = 128 * kBlockK * 2;
+
+__global__ void __launch_bounds__(kThreadsH, 1)
+    k_head_logprobs_pair(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                         const Args a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* stage_w = smem;
+    uint8_t* stage_x = smem + (size_t)kStages2 * kStageW;
+    float* trans = reinterpret_cast<float*>(stage_x + (size_t)kStages2 * kStageX2);
+    Bars* bars = reinterpret_cast<Bars*>(reinterpret_cast<uint8_t*>(trans) + 4 * kTransBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1;
+    const int row0 = (pair % a.groups) * kGroup;             // first hidden row of the row group
+    const int tile0 = pair / a.groups, step = (int)(gridDim.x >> 1) / a.groups;
+    const int n_tiles = (a.V + kPairTile - 1) / kPairTile;
+    const int k_stages = (a.H + kBlockK - 1) / kBlockK;
+
+    init_bars(bars, kStages2, 8);  // four epilogue warps in each CTA
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&bars->tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync();  // both CTAs' barriers are initialised before any remote use
+    tc_fence_after();
+    const uint32_t tmem_base = bars->tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const unsigned long long pol_w = policy_evict_first(), pol_x = policy_evict_last();
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = tile0; tile < n_tiles && ok; tile += step) {
+                for (int ks = 0; ks < k_stages; ++ks, ++it) {
+                    const int s = it % kStages2;
+                    if (!mbar_wait(&bars->empty[s], ((it / kStages2) & 1u) ^ 1u, a.err)) { ok = false; break; }
+                    const uint32_t full = map_to_rank(smem_u32(&bars->full[s]), 0);
+                    if (leader) mbar_arrive_expect_tx(&bars->full[s], 2u * (uint32_t)(kStageW + kStageX2));
+                    tma_load_2d_pair(stage_w + (size_t)s * kStageW, &map_w, full, ks * kBlockK,
+                                     tile * kPairTile + (int)rank * kTileM, pol_w);
+                    tma_load_2d_pair(stage_x + (size_t)s * kStageX2, &map_x, full, ks * kBlockK,
+                                     row0 + (int)rank * 128, pol_x);
+                }
+            }
+            if (leader)  // the leader's barriers see both CTAs' loads
+                for (uint32_t j = (it > (uint32_t)kStages2 ? it - kStages2 : 0); j < it; ++j)
+                    mbar_drain(&bars->full[j % kStages2], (j / kStages2) & 1u);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            const uint32_t idesc = idesc_bf16(kPairTile, kGroup);
+            uint32_t it = 0, local = 0;
+            bool ok = true;
+            for (int tile = tile0; tile < n_tiles && ok; tile += step, ++local) {
+                const uint32_t buf = local & 1u;
+                if (!mbar_wait(&bars->tmem_empty[buf], ((local >> 1) & 1u) ^ 1u, a.err)) break;
+                tc_fence_after();
+                for (int ks = 0; ks < k_stages; ++ks, ++it) {
+                    const int s = it % kStages2;
+                    if (!mbar_wait(&bars->full[s], (it / kStages2) & 1u, a.err)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sw = smem_u32(stage_w + (size_t)s * kStageW);
+                    const uint32_t sx = smem_u32(stage_x + (size_t)s * kStageX2);
+#pragma unroll
+                    for (int kk = 0; kk < kBlockK / 16; ++kk)
+                        mma_bf16_pair(tmem_base + buf * 256u, smem_desc_sw128(sw + kk * 32),
+                                      smem_desc_sw128(sx + kk * 32), idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit_pair(&bars->empty[s]);
+                }
+                if (ok) mma_commit_pair(&bars->tmem_full[buf]);
+            }
+            mma_commit_pair(&bars->mma_done);
+            mbar_drain(&bars->mma_done, 0u);
+        }
+    } else {
+        const int quarter = warp & 3;
+        Epilogue<kGroup / 32> ep;
+        ep.begin(a, row0, trans + quarter * (kTransBytes / 4));
+        const uint32_t empty0 = map_to_rank(smem_u32(&bars->tmem_empty[0]), 0);
+        const uint32_t empty1 = map_to_rank(smem_u32(&bars->tmem_empty[1]), 0);
+        uint32_t local = 0;
+        for (int tile = tile0; tile < n_tiles; tile += step, ++local) {
+            const uint32_t buf = local & 1u;
+            if (!mbar_wait(&bars->tmem_full[buf], (local >> 1) & 1u, a.err)) break;
+            tc_fence_after();
+            const int v0 = tile * kPairTile + (int)rank * kTileM + quarter * 32;
+#pragma unroll
+            for (int g = 0; g < kGroup / 32; ++g) {
+                float v[32];
+                tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * 256u + g * 32u, v);
+                if (g + 1 == kGroup / 32) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(buf ? empty1 : empty0);
+                }
+                if (v0 < a.V && row0 + g * 32 < a.R) ep.block(a, g, row0, v0, v);
+            }
+        }
+        ep.leave();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // no CTA leaves while its peer may still signal or read it
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols)
+                     : "memory");
+    }
+    publish(a, trans, tile0 * 2 + (int)rank, row0, min(kGroup, a.R - row0));
+}
+
+// ---------------------------------------------------------------------------
+// One CTA per hidden row: join the statistics, pick the alternatives.
+
+constexpr int kThreadsF = 256;
+constexpr int kWarpsF = kThreadsF / 32;
+
+struct FinishArgs {
+    int Rp, V, n_parts, segs, top_n;
+    const int32_t* tokens;
+    const float* tok_score;
+    const float4* part;
+    const float* seg_max;
+    const float* scores;
+    float *logprob, *entropy, *lse;
+    int32_t* top_ids;
+    float* top_logprobs;
+};
+
+__global__ void __launch_bounds__(kThreadsF) k_head_logprobs_finish(const FinishArgs a) {
+    __shared__ unsigned long long s_top[kWarpsF][32];
+    rows_launch_dependents();
+    rows_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x;
+    RowStat rs{};
+    if (warp == 0) {
+        Stat st = stat_none();
+        for (int i = lane; i < a.n_parts; i += 32) {
+            const float4 p = a.part[(size_t)i * a.Rp + row];
+            st = stat_join(st, Stat{p.x, p.y, p.z});
+        }
+        rs = stat_finish(stat_warp(st));
+        if (lane == 0) {
+            const int tok = a.tokens != nullptr ? a.tokens[row] : -1;
+            if (a.logprob != nullptr)
+                a.logprob[row] = (tok >= 0 && tok < a.V) ? stat_logprob(rs, a.tok_score[row]) : 0.f;
+            if (a.entropy != nullptr) a.entropy[row] = rs.entropy;
+            if (a.lse != nullptr) a.lse[row] = rs.lse;
+        }
+    }
+    if (a.top_n == 0) return;
+    const int n = a.top_n;
+    unsigned long long top = 0ull;
+    for (int g = warp * 32; g < a.segs; g += kThreadsF) {
+        const int gg = g + lane;
+        top_insert(top, gg < a.segs ? make_key(a.seg_max[(size_t)gg * a.Rp + row], (uint32_t)gg) : 0ull, n);
+    }
+    s_top[warp][lane] = top;
+    __syncthreads();
+    unsigned long long best = s_top[0][lane];
+#pragma unroll
+    for (int w = 1; w < kWarpsF; ++w) top_merge(best, s_top[w][lane]);
+    __syncthreads();
+    top = 0ull;
+    for (int i = warp; i < n; i += kWarpsF) {
+        const unsigned long long kseg = __shfl_sync(0xFFFFFFFFu, best, i);
+        if (kseg == 0ull) break;
+        const uint32_t g = key_gid(kseg);
+        const long long v = (long long)g * kSeg + lane;
+        const float x = a.scores[((size_t)g * a.Rp + row) * kSeg + lane];
+        top_insert(top, v < a.V ? make_key(x, (uint32_t)v) : 0ull, n);
+    }
+    s_top[warp][lane] = top;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < kWarpsF; ++w) top_merge(top, s_top[w][lane]);
+    if (lane < n) {
+        const size_t o = (size_t)row * n + lane;
+        a.top_ids[o] = top != 0ull ? (int32_t)key_gid(top) : -1;
+        a.top_logprobs[o] = top != 0ull ? stat_logprob(rs, key_score(top)) : neg_inf();
+    }
+}
+
+// ---------------------------------------------------------------------------
+
+struct Layout {
+    int Rp, segs;
+    size_t tok, part, seg_max, scores, total;
+};
+static Layout layout(int R, int V, int top_n) {
+    Layout l;
+    l.Rp = (std::min(R, kPassRows) + 31) / 32 * 32;
+    l.segs = (int)(((long long)V + kSeg - 1) / kSeg);
+    l.tok = kWsHeaderBytes;
+    l.part = l.tok + (size_t)l.Rp * 4;
+    l.seg_max = l.part + (size_t)kMaxParts * l.Rp * 16;
+    l.scores = l.seg_max + (top_n > 0 ? (size_t)l.segs * l.Rp * 4 : 0);
+    l.total = l.scores + (top_n > 0 ? (size_t)l.segs * l.Rp * kSeg * 4 : 0);
+    return l;
+}
+
+template <typename K>
+static cudaError_t launch_tc(K kernel, int grid, size_t smem, int cluster, cudaStream_t s, const CUtensorMap& mw,
+                             const CUtensorMap& mx, const Args& a) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreadsH);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    if (cluster > 1) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    } else {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, mw, mx, a);
+}
+
+// CTA pairs that are resident at once, per device.
+static int resident_pairs() {
+    static std::atomic<int> cache[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    int n = cache[dev & 63].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    const size_t smem = smem_bytes(kStages2, 128);
+    if (cudaFuncSetAttribute(k_head_logprobs_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
+    cfg.blockDim = dim3(kThreadsH);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, k_head_logprobs_pair, &cfg) != cudaSuccess) return 0;
+    cache[dev & 63].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// One pass over the head for nr <= kPassRows hidden rows.
+static cudaError_t pass(const HeadLogprobArgs& h, int r0, int nr, cudaStream_t s) {
+    const Layout l = layout(h.R, h.V, h.top_n);
+    uint8_t* base = static_cast<uint8_t*>(h.ws);
+    Args a{};
+    a.R = nr;
+    a.Rp = l.Rp;
+    a.H = h.H;
+    a.V = h.V;
+    a.tokens = h.tokens ? h.tokens + r0 : nullptr;
+    a.tok_score = reinterpret_cast<float*>(base + l.tok);
+    a.part = reinterpret_cast<float4*>(base + l.part);
+    a.seg_max = h.top_n > 0 ? reinterpret_cast<float*>(base + l.seg_max) : nullptr;
+    a.scores = reinterpret_cast<float*>(base + l.scores);
+    a.err = reinterpret_cast<unsigned int*>(base + kWsErrorOffset);
+    const uint16_t* x = h.x + (size_t)r0 * h.H;
+    alignas(64) CUtensorMap mw, mx;
+    if (!make_map(&mw, h.W, h.V, h.H, kTileM)) return cudaErrorNotSupported;
+    int n_parts;
+    cudaError_t e;
+    if (nr <= kOneCtaRows) {
+        a.N = (nr + 15) / 16 * 16;
+        if (!make_map(&mx, x, nr, h.H, a.N)) return cudaErrorNotSupported;
+        n_parts = std::min({sm_count(), (int)(((long long)h.V + kTileM - 1) / kTileM), kMaxParts});
+        e = a.N <= 64 ? launch_tc(k_head_logprobs<8, 64>, n_parts, smem_bytes(8, 64), 1, s, mw, mx, a)
+                      : launch_tc(k_head_logprobs<6, 128>, n_parts, smem_bytes(6, 128), 1, s, mw, mx, a);
+    } else {
+        a.groups = (nr + kGroup - 1) / kGroup;
+        if (!make_map(&mx, x, nr, h.H, 128)) return cudaErrorNotSupported;
+        const int pairs = resident_pairs();
+        const int tiles = (int)(((long long)h.V + kPairTile - 1) / kPairTile);
+        const int per = std::min({pairs / a.groups, tiles, kMaxParts / 2});  // pairs of one row group
+        if (per < 1) return cudaErrorNotSupported;
+        n_parts = 2 * per;
+        e = launch_tc(k_head_logprobs_pair, 2 * per * a.groups, smem_bytes(kStages2, 128), 2, s, mw, mx, a);
+    }
+    if (e != cudaSuccess) return e;
+    FinishArgs f{};
+    f.Rp = l.Rp;
+    f.V = h.V;
+    f.n_parts = n_parts;
+    f.segs = l.segs;
+    f.top_n = h.top_n;
+    f.tokens = a.tokens;
+    f.tok_score = a.tok_score;
+    f.part = a.part;
+    f.seg_max = a.seg_max;
+    f.scores = a.scores;
+    f.logprob = h.logprob ? h.logprob + r0 : nullptr;
+    f.entropy = h.entropy ? h.entropy + r0 : nullptr;
+    f.lse = h.lse ? h.lse + r0 : nullptr;
+    f.top_ids = h.top_ids ? h.top_ids + (size_t)r0 * h.top_n : nullptr;
+    f.top_logprobs = h.top_logprobs ? h.top_logprobs + (size_t)r0 * h.top_n : nullptr;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)nr);
+    cfg.blockDim = dim3(kThreadsF);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_head_logprobs_finish, f);
+}
+
+}  // namespace hlp
+
+size_t head_logprobs_ws_bytes(int R, int V, int top_n) { return hlp::layout(R, V, top_n).total; }
+
+cudaError_t launch_head_logprobs(const HeadLogprobArgs& a, cudaStream_t s) {
+    for (int r0 = 0; r0 < a.R; r0 += hlp::kPassRows) {
+        const cudaError_t e = hlp::pass(a, r0, std::min(hlp::kPassRows, a.R - r0), s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace vh
