@@ -434,12 +434,20 @@ def spec_verify_greedy_nvfp4_packed(hidden, packed, tensor_scale, draft_ids, B: 
 # Norm and log probabilities.
 
 _dtypes = {}  # torch dtype -> vh_dtype
+_f32 = _i32 = None  # torch.float32, torch.int32
+_current_device = None  # torch's query of the current device
+
+
+def _setup():
+    """Fills the names above on the first call (torch is imported no earlier than it is needed)."""
+    global _f32, _i32, _current_device
+    torch = _torch()
+    _dtypes.update({torch.float32: VH_F32, torch.bfloat16: VH_BF16, torch.float16: VH_F16})
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _f32, _i32 = torch.float32, torch.int32
 
 
 def _dtype(t, name):
-    if not _dtypes:
-        torch = _torch()
-        _dtypes.update({torch.float32: VH_F32, torch.bfloat16: VH_BF16, torch.float16: VH_F16})
     d = _dtypes.get(t.dtype)
     if d is None:
         raise ValueError(f"{name}: float32, bfloat16 or float16 wanted, not {t.dtype}")
@@ -448,12 +456,19 @@ def _dtype(t, name):
 
 def _device(t):
     """Device index of a call's first tensor, which must be the current device (the launch goes there)."""
+    if _f32 is None:
+        _setup()
     d = t.get_device()
     if d < 0:
         raise ValueError("verify_head_gb300 takes CUDA tensors only")
-    if d != _torch().cuda.current_device():
+    if d != _current_device():
         raise ValueError(f"the tensors are on device {d}, not on the current device")
     return d
+
+
+def _stream_on(stream, dev):
+    """cudaStream_t of `stream`, or of torch's current stream on device `dev`."""
+    return _raw_stream(dev) if stream is None and _raw_stream else _stream_ptr(stream)
 
 
 def _place(t, name, dev):
@@ -461,28 +476,32 @@ def _place(t, name, dev):
         raise ValueError(f"{name}: a CUDA tensor on device {dev} wanted")
 
 
-def _rows(t, name, dev, shape=None, dtype=None):
-    """Checks a 2-D CUDA tensor whose rows are contiguous; returns the elements between rows."""
+def _rows(t, name, dev, shape, dtype):
+    """Checks a 2-D CUDA tensor of that shape and type whose rows are contiguous; returns the elements between rows."""
+    # the usual case in as few queries as possible: the checks are most of a small call's time on the host
+    if t.is_contiguous() and t.dtype is dtype and t.shape == shape and t.get_device() == dev and len(shape) == 2:
+        return shape[1] or 1
     _place(t, name, dev)
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
+    if t.dim() != 2 or t.shape != shape:
         raise ValueError(f"{name}: shape mismatch")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise ValueError(f"{name}: {dtype} wanted, not {t.dtype}")
-    rows, width = t.shape
+    rows, width = shape
     if width > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
     return t.stride(0) if rows > 1 else max(width, 1)
 
 
 def _vector(t, name, dev, n, dtype):
-    """Checks a contiguous CUDA tensor of n elements (None passes)."""
+    """Checks a contiguous CUDA tensor of n elements and returns its address (None passes)."""
     if t is None:
-        return
+        return None
+    if t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
     _place(t, name, dev)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: {n} contiguous elements wanted")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: {dtype} wanted, not {t.dtype}")
+    raise ValueError(f"{name}: {dtype} wanted, not {t.dtype}")
 
 
 def _workspace(ws, dev):
@@ -498,31 +517,31 @@ def _allocating(stream):
     return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
 
 
-def _norm_weight(weight, x, dev):
-    """(pointer, whether it is fp32) of a norm's weight."""
+def _norm_weight(weight, H, dtype, dev):
+    """(address, whether it is fp32) of a norm's weight."""
     if weight is None:
         return None, 0
-    f32 = _torch().float32
-    _vector(weight, "weight", dev, x.shape[1], f32 if weight.dtype == f32 else x.dtype)
-    return weight.data_ptr(), int(weight.dtype == f32)
+    f32 = weight.dtype is _f32
+    return _vector(weight, "weight", dev, H, _f32 if f32 else dtype), int(f32)
 
 
 def _empty_rows(x):
     return _torch().empty(x.shape, dtype=x.dtype, device=x.device)
 
 
-def _add_rmsnorm(where, x, residual, weight, eps, weight_offset, y, kind, h, scales, stream):
+def _add_rmsnorm(where, x, residual, weight, eps, weight_offset, y, out_dtype, kind, h, scales, stream):
     dev = _device(x)
     dt = _dtype(x, "x")
-    xs = _rows(x, "x", dev)
-    T, H = x.shape
-    rs = _rows(residual, "residual", dev, x.shape, x.dtype) if residual is not None else 0
-    hs = _rows(h, "h", dev, x.shape, x.dtype) if h is not None else 0
-    ys = _rows(y, "y", dev, x.shape)
-    _vector(scales, "scales", dev, T, _torch().float32)
-    w, w32 = _norm_weight(weight, x, dev)
-    st = lib().vh_add_rmsnorm(_ptr(x), _ptr(residual), w, dt, w32, T, H, xs, rs, eps, weight_offset, _ptr(y), ys, kind,
-                              _ptr(h), hs, _ptr(scales), _stream_ptr(stream))
+    shape, dtype = x.shape, x.dtype
+    xs = _rows(x, "x", dev, shape, dtype)
+    T, H = shape
+    rp, rs = (residual.data_ptr(), _rows(residual, "residual", dev, shape, dtype)) if residual is not None else (None, 0)
+    hp, hs = (h.data_ptr(), _rows(h, "h", dev, shape, dtype)) if h is not None else (None, 0)
+    ys = _rows(y, "q" if kind else "y", dev, shape, out_dtype)
+    w, w32 = _norm_weight(weight, H, dtype, dev)
+    st = lib().vh_add_rmsnorm(
+        x.data_ptr(), rp, w, dt, w32, T, H, xs, rs, eps, weight_offset, y.data_ptr(), ys, kind, hp, hs,
+        _vector(scales, "scales", dev, T, _f32), _stream_on(stream, dev))
     _check(st, where)
 
 
@@ -536,9 +555,7 @@ def add_rmsnorm(x, residual=None, weight=None, eps: float = 1e-6, weight_offset:
         with _allocating(stream):
             y = _empty_rows(x) if y is None else y
             h = _empty_rows(x) if residual is not None and h is None else h
-    if y.dtype != x.dtype:
-        raise ValueError(f"y: {x.dtype} wanted, not {y.dtype}")
-    _add_rmsnorm("add_rmsnorm", x, residual, weight, eps, weight_offset, y, VH_NORM_SAME, h, None, stream)
+    _add_rmsnorm("add_rmsnorm", x, residual, weight, eps, weight_offset, y, x.dtype, VH_NORM_SAME, h, None, stream)
     return y, (x if h is None else h)
 
 
@@ -557,7 +574,7 @@ def add_rmsnorm_q8(x, residual=None, weight=None, eps: float = 1e-6, weight_offs
     kind = {torch.int8: VH_NORM_INT8, torch.float8_e4m3fn: VH_NORM_E4M3}.get(q.dtype)
     if kind is None:
         raise ValueError(f"q: int8 or float8_e4m3fn wanted, not {q.dtype}")
-    _add_rmsnorm("add_rmsnorm_q8", x, residual, weight, eps, weight_offset, q, kind, h, scales, stream)
+    _add_rmsnorm("add_rmsnorm_q8", x, residual, weight, eps, weight_offset, q, q.dtype, kind, h, scales, stream)
     return q, scales, (x if h is None else h)
 
 
@@ -573,11 +590,12 @@ def add_rmsnorm_grad(dy, h, weight=None, eps: float = 1e-6, weight_offset: float
     torch = _torch()
     dev = _device(h)
     dt = _dtype(h, "h")
-    hs = _rows(h, "h", dev)
-    T, H = h.shape
-    dys = _rows(dy, "dy", dev, h.shape, h.dtype)
-    dhs = _rows(dh, "dh", dev, h.shape, h.dtype) if dh is not None else 0
-    w, w32 = _norm_weight(weight, h, dev)
+    shape, dtype = h.shape, h.dtype
+    hs = _rows(h, "h", dev, shape, dtype)
+    T, H = shape
+    dys = _rows(dy, "dy", dev, shape, dtype)
+    ep, es = (dh.data_ptr(), _rows(dh, "dh", dev, shape, dtype)) if dh is not None else (None, 0)
+    w, w32 = _norm_weight(weight, H, dtype, dev)
     if weight is None and dweight is not None:
         raise ValueError("dweight without a weight")
     if dx is None or (weight is not None and (dweight is None or ws is None)):
@@ -586,37 +604,37 @@ def add_rmsnorm_grad(dy, h, weight=None, eps: float = 1e-6, weight_offset: float
             if weight is not None:
                 dweight = torch.empty(H, dtype=torch.float32, device=h.device) if dweight is None else dweight
                 ws = add_rmsnorm_grad_workspace(T, H, h.device) if ws is None else ws
-    dxs = _rows(dx, "dx", dev, h.shape, h.dtype)
-    _vector(dweight, "dweight", dev, H, torch.float32)
-    st = lib().vh_add_rmsnorm_grad(_ptr(dy), _ptr(h), w, _ptr(dh), dt, w32, T, H, dys, hs, dhs, eps, weight_offset,
-                                   _ptr(dx), dxs, _ptr(dweight), _ptr(ws), 0 if ws is None else _workspace(ws, dev),
-                                   _stream_ptr(stream))
+    dxs = _rows(dx, "dx", dev, shape, dtype)
+    st = lib().vh_add_rmsnorm_grad(dy.data_ptr(), h.data_ptr(), w, ep, dt, w32, T, H, dys, hs, es, eps, weight_offset,
+                                   dx.data_ptr(), dxs, _vector(dweight, "dweight", dev, H, _f32), _ptr(ws),
+                                   0 if ws is None else _workspace(ws, dev), _stream_on(stream, dev))
     _check(st, "add_rmsnorm_grad")
     return dx, dweight
 
 
-def _logprob_outputs(R, top_n, like, dev, stream, given, make_ws):
-    """The five outputs and the workspace, those not given newly made; then checked."""
-    torch = _torch()
-    f32, i32 = torch.float32, torch.int32
-    if any(g is None for g in given):
+def _logprob_outputs(R, top_n, like, dev, stream, tokens, outs, make_ws):
+    """The five outputs and the workspace, those not given newly made -> (outputs, their addresses and the
+    workspace's, its size)."""
+    logprob, entropy, lse, top_ids, top_logprobs, ws = outs
+    if logprob is None or entropy is None or lse is None or top_ids is None or top_logprobs is None or ws is None:
+        torch = _torch()
         with _allocating(stream):
             shapes = ((R,), (R,), (R,), (R, top_n), (R, top_n))
-            outs = [torch.empty(s, dtype=i32 if i == 3 else f32, device=like.device) if g is None else g
-                    for i, (s, g) in enumerate(zip(shapes, given))]
-            ws = make_ws() if given[5] is None else given[5]
-    else:
-        outs, ws = given[:5], given[5]
-    _vector(outs[0], "logprob", dev, R, f32)
-    _vector(outs[1], "entropy", dev, R, f32)
-    _vector(outs[2], "lse", dev, R, f32)
-    _vector(outs[3], "top_ids", dev, R * top_n, i32)
-    _vector(outs[4], "top_logprobs", dev, R * top_n, f32)
-    return (*outs, ws)
+            outs = [torch.empty(s, dtype=_i32 if i == 3 else _f32, device=like.device) if g is None else g
+                    for i, (s, g) in enumerate(zip(shapes, outs[:5]))] + [make_ws() if ws is None else ws]
+        logprob, entropy, lse, top_ids, top_logprobs, ws = outs
+    at = [_vector(logprob, "logprob", dev, R, _f32), _vector(entropy, "entropy", dev, R, _f32),
+          _vector(lse, "lse", dev, R, _f32), None, None, ws.data_ptr(), _workspace(ws, dev)]
+    if top_n > 0:
+        at[3] = _vector(top_ids, "top_ids", dev, R * top_n, _i32)
+        at[4] = _vector(top_logprobs, "top_logprobs", dev, R * top_n, _f32)
+    if tokens is None:
+        at[0] = None
+    return outs, at
 
 
 def _logprob_results(outs, tokens):
-    return tuple(outs) if tokens is not None else (None, *outs[1:])
+    return tuple(outs[:5]) if tokens is not None else (None, *outs[1:5])
 
 
 def logits_logprobs_workspace(R: int, V: int, top_n: int = 0, device=None):
@@ -630,18 +648,16 @@ def logits_logprobs(logits, tokens, top_n: int = 0, logprob=None, entropy=None, 
                     top_logprobs=None, ws=None, stream=None):
     """logits [R,V] fp32 / bf16 / fp16 (rows may be strided), tokens [R] int32 (outside [0,V): no token, logprob 0;
     None: logprob is None)  -> (logprob [R], entropy [R], lse [R], top_ids [R,top_n] int32, top_logprobs [R,top_n])."""
-    torch = _torch()
     dev = _device(logits)
-    stride = _rows(logits, "logits", dev)
-    R, V = logits.shape
     dt = _dtype(logits, "logits")
-    _vector(tokens, "tokens", dev, R, torch.int32)
-    *outs, ws = _logprob_outputs(R, top_n, logits, dev, stream, (logprob, entropy, lse, top_ids, top_logprobs, ws),
-                                 lambda: logits_logprobs_workspace(R, V, top_n, logits.device))
-    st = lib().vh_logits_logprobs(_ptr(logits), dt, R, V, stride, _ptr(tokens), top_n,
-                                  _ptr(outs[0]) if tokens is not None else None, _ptr(outs[1]),
-                                  _ptr(outs[2]), _ptr(outs[3]) if top_n else None, _ptr(outs[4]) if top_n else None,
-                                  _ptr(ws), _workspace(ws, dev), _stream_ptr(stream))
+    shape = logits.shape
+    stride = _rows(logits, "logits", dev, shape, logits.dtype)
+    R, V = shape
+    tp = _vector(tokens, "tokens", dev, R, _i32)
+    outs, at = _logprob_outputs(R, top_n, logits, dev, stream, tokens,
+                                (logprob, entropy, lse, top_ids, top_logprobs, ws),
+                                lambda: logits_logprobs_workspace(R, V, top_n, logits.device))
+    st = lib().vh_logits_logprobs(logits.data_ptr(), dt, R, V, stride, tp, top_n, *at, _stream_on(stream, dev))
     _check(st, "logits_logprobs")
     return _logprob_results(outs, tokens)
 
@@ -649,20 +665,19 @@ def logits_logprobs(logits, tokens, top_n: int = 0, logprob=None, entropy=None, 
 def logits_logprobs_grad(logits, tokens, lse, entropy=None, g_logprob=None, g_entropy=None, dlogits=None, stream=None):
     """Gradient of logits_logprobs' logprob and entropy (their gradients [R] fp32, either may be None) with respect to
     the logits, from the lse and entropy it returned; dlogits may be `logits` itself.  -> dlogits [R,V]"""
-    torch = _torch()
     dev = _device(logits)
-    stride = _rows(logits, "logits", dev)
-    R, V = logits.shape
     dt = _dtype(logits, "logits")
-    _vector(tokens, "tokens", dev, R, torch.int32)
-    for t, name in ((lse, "lse"), (entropy, "entropy"), (g_logprob, "g_logprob"), (g_entropy, "g_entropy")):
-        _vector(t, name, dev, R, torch.float32)
+    shape, dtype = logits.shape, logits.dtype
+    stride = _rows(logits, "logits", dev, shape, dtype)
+    R, V = shape
     if dlogits is None:
         with _allocating(stream):
             dlogits = _empty_rows(logits)
-    ds = _rows(dlogits, "dlogits", dev, logits.shape, logits.dtype)
-    st = lib().vh_logits_logprobs_grad(_ptr(logits), dt, R, V, stride, _ptr(tokens), _ptr(lse), _ptr(entropy),
-                                       _ptr(g_logprob), _ptr(g_entropy), _ptr(dlogits), ds, _stream_ptr(stream))
+    ds = _rows(dlogits, "dlogits", dev, shape, dtype)
+    st = lib().vh_logits_logprobs_grad(
+        logits.data_ptr(), dt, R, V, stride, _vector(tokens, "tokens", dev, R, _i32), _vector(lse, "lse", dev, R, _f32),
+        _vector(entropy, "entropy", dev, R, _f32), _vector(g_logprob, "g_logprob", dev, R, _f32),
+        _vector(g_entropy, "g_entropy", dev, R, _f32), dlogits.data_ptr(), ds, _stream_on(stream, dev))
     _check(st, "logits_logprobs_grad")
     return dlogits
 
@@ -671,7 +686,7 @@ def head_logprobs_workspace(R: int, V: int, top_n: int = 0, device=None):
     """A workspace for head_logprobs calls of this R, V and top_n (about 4 V bytes per row with alternatives)."""
     torch = _torch()
     ws = torch.empty(int(lib().vh_head_logprobs_workspace_bytes(R, V, top_n)), dtype=torch.uint8, device=device or "cuda")
-    ws[:16].zero_()
+    ws[:8192].zero_()
     return ws
 
 
@@ -679,19 +694,18 @@ def head_logprobs(hidden, W_full, tokens, top_n: int = 0, logprob=None, entropy=
                   top_logprobs=None, ws=None, stream=None):
     """logits_logprobs of the scores hidden @ W_full.T, which are not returned: hidden [R,H] bf16, W_full [V,H] bf16,
     tokens [R] int32 -> (logprob [R], entropy [R], lse [R], top_ids [R,top_n] int32, top_logprobs [R,top_n])."""
-    torch = _torch()
     dev = _device(hidden)
     _place(W_full, "W_full", dev)
     _require_cuda(hidden, W_full)
+    bf16 = _torch().bfloat16
     R, H = hidden.shape
     V = W_full.shape[0]
-    if W_full.shape[1] != H or hidden.dtype != torch.bfloat16 or W_full.dtype != torch.bfloat16:
+    if W_full.shape[1] != H or hidden.dtype != bf16 or W_full.dtype != bf16:
         raise ValueError("shape/dtype mismatch")
-    _vector(tokens, "tokens", dev, R, torch.int32)
-    *outs, ws = _logprob_outputs(R, top_n, hidden, dev, stream, (logprob, entropy, lse, top_ids, top_logprobs, ws),
-                                 lambda: head_logprobs_workspace(R, V, top_n, hidden.device))
-    st = lib().vh_head_logprobs(_ptr(hidden), _ptr(W_full), _ptr(tokens), R, H, V, top_n,
-                                _ptr(outs[0]) if tokens is not None else None, _ptr(outs[1]), _ptr(outs[2]), _ptr(outs[3]) if top_n else None, _ptr(outs[4]) if top_n else None,
-                                _ptr(ws), _workspace(ws, dev), _stream_ptr(stream))
+    tp = _vector(tokens, "tokens", dev, R, _i32)
+    outs, at = _logprob_outputs(R, top_n, hidden, dev, stream, tokens,
+                                (logprob, entropy, lse, top_ids, top_logprobs, ws),
+                                lambda: head_logprobs_workspace(R, V, top_n, hidden.device))
+    st = lib().vh_head_logprobs(hidden.data_ptr(), W_full.data_ptr(), tp, R, H, V, top_n, *at, _stream_on(stream, dev))
     _check(st, "head_logprobs")
     return _logprob_results(outs, tokens)

@@ -21,10 +21,10 @@
 // instructions per score and thread, under a tenth of the MMA time at H = 2048.
 //
 // Alternatives.  Where they are wanted each block of 32 head rows (a segment)
-// leaves its maximum and its 32 scores per hidden row in the workspace.  The
-// n largest scores of a row lie in the n segments with the largest maxima (see
-// the logits' kernel), so the finishing kernel reads the maxima and n blocks
-// of 128 bytes per row.
+// leaves its maximum per hidden row in the workspace, and its 32 scores unless
+// n larger ones are known.  The n largest scores of a row lie in the n segments
+// with the largest maxima (select_top), so the finishing kernel reads the
+// maxima and about n blocks of 128 bytes per row.
 //
 // Every wait is bounded; on expiry the workspace error word is set and the
 // CTA drains its copies, frees TMEM and returns.
@@ -53,7 +53,8 @@ constexpr int kGroup = 256;             // hidden rows per row group (MMA N)
 constexpr int kMaxGroups = 4;           // row groups per pass over the head
 constexpr int kPassRows = kGroup * kMaxGroups;
 constexpr int kOneCtaRows = 128;
-constexpr int kThreadsH = 192;
+constexpr int kThreadsH = 224;
+constexpr int kBoundWarp = 6;
 constexpr int kMaxStages = 8;
 constexpr int kStageW = kTileM * kBlockK * 2;  // 16 KiB
 constexpr int kTmemCols = 512;
@@ -70,7 +71,8 @@ struct alignas(8) Bars {
     unsigned long long tmem_empty[2];
     unsigned long long mma_done;
     unsigned int tmem_base;
-    unsigned int pad;
+    uint32_t done;             // an epilogue warp has finished its last tile
+    uint32_t bounds[kGroup];   // of the row group's rows: see find_bounds
 };
 
 struct Args {
@@ -82,13 +84,91 @@ struct Args {
     const int32_t* tokens;
     float* tok_score;  // [Rp]
     float4* part;      // [CTA of the row group][Rp]: c, s, t
-    float* seg_max;    // [segment][Rp], null: no alternatives
+    float* seg_max;    // [Rp][segments], null: no alternatives
     float* scores;     // [segment][Rp][32]
+    int segs, top_n;
+    uint32_t* bound;   // [Rp]: see Bound, zero between calls
+    uint32_t* seen;    // [kMaxGroups]: epilogue warps that have left their first tile's maxima
     unsigned int* err;
 };
 
 __host__ __device__ constexpr size_t smem_bytes(int stages, int nmax) {
     return 1024 + (size_t)stages * (kStageW + (size_t)nmax * kBlockK * 2) + sizeof(Bars) + 4 * kTransBytes + 64;
+}
+
+// ---------------------------------------------------------------------------
+// Which blocks of scores are kept for the alternatives.  Each epilogue warp
+// counts itself in `seen` once the maxima of its first tile are written.  A
+// warp of its own in every CTA looks at the count; when all have counted, the
+// CTAs of the row group share out the hidden rows, and each finds a
+// value that n of a row's first maxima reach: blocks whose maximum is below it need not be written any more.  At 248,320 head rows that
+// leaves about a sixth of the scores to write.  The epilogue never waits for a
+// bound: it reads what the CTA has so far from shared memory (0 = none).  In a
+// warp of the epilogue itself the same search cost the 64-row call 8 us.
+// The bound is rounded down to 16 bits of the ordered float.
+
+constexpr int kFirstSegs = 1024;
+constexpr int kMinFirstSegs = 64;   // so that each of the 64 groups below has one
+constexpr int kTries = 256;         // looks at the count, and at the bounds
+constexpr unsigned int kTryNs = 500;
+
+// A value that n <= 32 of the m <= kFirstSegs values p[0..m) reach, by one warp, as ord_f32 rounded down: the n-th
+// largest maximum of 64 groups of them (two per lane).
+__device__ __forceinline__ uint32_t nth_largest(const float* p, int m, int n) {
+    const int lane = threadIdx.x & 31;
+    float x[kFirstSegs / 32];
+#pragma unroll
+    for (int i = 0; i < kFirstSegs / 32; ++i) x[i] = i * 32 + lane < m ? __ldcg(p + i * 32 + lane) : quiet_nan();
+    float lo = x[0], hi = x[1];
+#pragma unroll
+    for (int i = 2; i < kFirstSegs / 32; i += 2) {
+        lo = fmaxf(lo, x[i]);
+        hi = fmaxf(hi, x[i + 1]);
+    }
+    const uint32_t a = lo == lo ? ord_f32(lo) >> 16 : 0u, b = hi == hi ? ord_f32(hi) >> 16 : 0u;  // NaN: no value
+    uint32_t t = 0u;
+#pragma unroll
+    for (int bit = 15; bit >= 0; --bit) {
+        const uint32_t u = t | (1u << bit);
+        const int c = __popc(__ballot_sync(0xFFFFFFFFu, a >= u)) + __popc(__ballot_sync(0xFFFFFFFFu, b >= u));
+        t = c >= n ? u : t;
+    }
+    return t << 16;
+}
+
+// The bounds of a row group, by one warp of each of its n_cta CTAs; `first_segs`: the segments of their first tiles.
+// bounds: the CTA's copy (shared, zero at the start); *done: the CTA's epilogue has finished.
+__device__ __forceinline__ void find_bounds(const Args& a, int row0, int cta, int n_cta, int first_segs,
+                                            volatile uint32_t* bounds, volatile uint32_t* done) {
+    first_segs = min(first_segs, kFirstSegs);
+    // no later tiles (this CTA's, at least), or too few maxima
+    if (a.seg_max == nullptr || first_segs >= a.segs || first_segs < kMinFirstSegs) return;
+    const int lane = threadIdx.x & 31;
+    const int rows = min(kGroup, a.R - row0);
+    volatile uint32_t* seen = a.seen + row0 / kGroup;
+    volatile uint32_t* shared = a.bound + row0;
+    bool all = false;
+    for (int i = 0; i < kTries && !all && *done == 0u; ++i) {
+        if (i > 0) __nanosleep(kTryNs);
+        all = __shfl_sync(0xFFFFFFFFu, lane == 0 ? *seen : 0u, 0) == 4u * (uint32_t)n_cta;
+    }
+    if (!all) return;
+    __threadfence();
+    for (int r = cta; r < rows; r += n_cta) {
+        const uint32_t b = nth_largest(a.seg_max + (size_t)(row0 + r) * a.segs, first_segs, a.top_n);
+        if (lane == 0) shared[r] = b;
+    }
+    all = false;
+    for (int i = 0; i < kTries && !all && *done == 0u; ++i) {
+        if (i > 0) __nanosleep(kTryNs);
+        bool have = true;
+        for (int r = lane; r < rows; r += 32) {
+            const uint32_t b = shared[r];
+            bounds[r] = b;
+            have = have && b != 0u;
+        }
+        all = __all_sync(0xFFFFFFFFu, have);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -99,9 +179,11 @@ struct Epilogue {
     Stat st[NG];
     int tok[NG];
     float* tr;
+    volatile uint32_t* bounds;  // of the row group's rows
 
-    __device__ __forceinline__ void begin(const Args& a, int row0, float* tr_) {
+    __device__ __forceinline__ void begin(const Args& a, int row0, float* tr_, volatile uint32_t* bounds_) {
         tr = tr_;
+        bounds = bounds_;
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -109,6 +191,14 @@ struct Epilogue {
             st[g] = stat_none();
             tok[g] = (a.tokens != nullptr && row < a.R) ? a.tokens[row] : -1;
         }
+    }
+
+    // After the warp's first tile: its maxima are there (see find_bounds).
+    __device__ __forceinline__ void first_done(const Args& a, int row0) {
+        if (a.seg_max == nullptr) return;
+        __threadfence();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) atomicAdd(a.seen + row0 / kGroup, 1u);
     }
 
     // v[j]: the score of head row v0 + lane for column j of group g.
@@ -139,18 +229,26 @@ struct Epilogue {
         float m = neg_inf();
 #pragma unroll
         for (int i = 0; i < 32; ++i) m = fmaxf(m, x[i]);
-        if (a.seg_max != nullptr && row < a.R) {
-            const size_t o = (size_t)(v0 / kSeg) * a.Rp + row;
-            a.seg_max[o] = m;
-            float4* p = reinterpret_cast<float4*>(a.scores + o * kSeg);
+        if (a.seg_max != nullptr) {
+            const int seg = v0 / kSeg;
+            if (row < a.R) a.seg_max[(size_t)row * a.segs + seg] = m;
+            // rows whose scores are kept: 128 bytes each, lane = head row again
+            const uint32_t keep = __ballot_sync(0xFFFFFFFFu, row < a.R && ord_f32(m) >= bounds[g * 32 + lane]);
+            float* p = a.scores + ((size_t)seg * a.Rp + row0 + g * 32) * kSeg + lane;
+            if (keep != 0u) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                for (int j = 0; j < 32; ++j)
+                    if ((keep >> j) & 1u) p[j * kSeg] = v[j];
+            }
         }
-        if (m > st[g].c) stat_shift(st[g], m);
-        if (st[g].c != neg_inf()) {
+        Stat2 run{st[g].c, f2(st[g].s, 0.f), f2(st[g].t, 0.f)};
+        run.raise(m);
+        if (run.c != neg_inf()) {
+            const F2 mc = f2(-run.c, -run.c);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) stat_add(st[g], x[i]);
+            for (int i = 0; i < 32; i += 2) run.add(x[i], x[i + 1], mc);
         }
+        st[g] = run.get();
     }
 
     // The warp's statistics of every hidden row, for the CTA to join.
@@ -192,12 +290,15 @@ __device__ __forceinline__ void init_bars(Bars* b, int stages, int empty_arrival
         }
         mbar_init(&b->mma_done, 1);
         ptx::fence_barrier_init();
+        b->done = 0u;
     }
+    for (int i = threadIdx.x; i < kGroup; i += blockDim.x) b->bounds[i] = 0u;
 }
 
 // ---------------------------------------------------------------------------
 // Up to 128 hidden rows: one CTA per tile.  Warp 0 = TMA producer, warp 1 =
-// TMEM owner and MMA issuer, warps 2..5 = epilogue (TMEM lane quarter = warp % 4).
+// TMEM owner and MMA issuer, warps 2..5 = epilogue (TMEM lane quarter = warp % 4),
+// warp 6 = the alternatives' bounds.
 
 template <int STAGES, int NMAX>
 __global__ void __launch_bounds__(kThreadsH, 1)
@@ -283,11 +384,14 @@ __global__ void __launch_bounds__(kThreadsH, 1)
             mma_commit(&bars->mma_done);
             mbar_drain(&bars->mma_done, 0u);
         }
+    } else if (warp == kBoundWarp) {
+        rows_wait();
+        find_bounds(a, 0, blockIdx.x, gridDim.x, (int)gridDim.x * (kTileM / kSeg), bars->bounds, &bars->done);
     } else {
         rows_wait();
         const int quarter = warp & 3;
         Epilogue<NG> ep;
-        ep.begin(a, 0, trans + quarter * (kTransBytes / 4));
+        ep.begin(a, 0, trans + quarter * (kTransBytes / 4), bars->bounds);
         const int ngroups = (a.N + 31) / 32;
         uint32_t local = 0;
         for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x, ++local) {
@@ -308,8 +412,10 @@ __global__ void __launch_bounds__(kThreadsH, 1)
                     if (v0 < a.V) ep.block(a, g, 0, v0, v);
                 }
             }
+            if (local == 0) ep.first_done(a, 0);
         }
         ep.leave();
+        *const_cast<volatile uint32_t*>(&bars->done) = 1u;
     }
     tc_fence_before();
     __syncthreads();
@@ -360,24 +466,37 @@ __global__ void __launch_bounds__(kThreadsH, 1)
     cluster_sync();  // both CTAs' barriers are initialised before any remote use
     tc_fence_after();
     const uint32_t tmem_base = bars->tmem_base;
+    rows_launch_dependents();
 
     if (warp == 0) {
         if (lane == 0) {
             const unsigned long long pol_w = policy_evict_first(), pol_x = policy_evict_last();
             uint32_t it = 0;
-            bool ok = true;
+            bool ok = true, waited = false;
+            auto load_x = [&](uint32_t j) {
+                const int s = j % kStages2;
+                tma_load_2d_pair(stage_x + (size_t)s * kStageX2, &map_x, map_to_rank(smem_u32(&bars->full[s]), 0),
+                                 (int)(j % k_stages) * kBlockK, row0 + (int)rank * 128, pol_x);
+            };
+            auto release_first_ring = [&](uint32_t n) {
+                rows_wait();
+                for (uint32_t j = 0; j < n; ++j) load_x(j);
+                waited = true;
+            };
             for (int tile = tile0; tile < n_tiles && ok; tile += step) {
                 for (int ks = 0; ks < k_stages; ++ks, ++it) {
                     const int s = it % kStages2;
                     if (!mbar_wait(&bars->empty[s], ((it / kStages2) & 1u) ^ 1u, a.err)) { ok = false; break; }
-                    const uint32_t full = map_to_rank(smem_u32(&bars->full[s]), 0);
                     if (leader) mbar_arrive_expect_tx(&bars->full[s], 2u * (uint32_t)(kStageW + kStageX2));
-                    tma_load_2d_pair(stage_w + (size_t)s * kStageW, &map_w, full, ks * kBlockK,
-                                     tile * kPairTile + (int)rank * kTileM, pol_w);
-                    tma_load_2d_pair(stage_x + (size_t)s * kStageX2, &map_x, full, ks * kBlockK,
-                                     row0 + (int)rank * 128, pol_x);
+                    tma_load_2d_pair(stage_w + (size_t)s * kStageW, &map_w, map_to_rank(smem_u32(&bars->full[s]), 0),
+                                     ks * kBlockK, tile * kPairTile + (int)rank * kTileM, pol_w);
+                    if (waited)
+                        load_x(it);
+                    else if (it + 1 == (uint32_t)kStages2)
+                        release_first_ring(it + 1);
                 }
             }
+            if (!waited) release_first_ring(it);
             if (leader)  // the leader's barriers see both CTAs' loads
                 for (uint32_t j = (it > (uint32_t)kStages2 ? it - kStages2 : 0); j < it; ++j)
                     mbar_drain(&bars->full[j % kStages2], (j / kStages2) & 1u);
@@ -408,10 +527,14 @@ __global__ void __launch_bounds__(kThreadsH, 1)
             mma_commit_pair(&bars->mma_done);
             mbar_drain(&bars->mma_done, 0u);
         }
+    } else if (warp == kBoundWarp) {
+        rows_wait();
+        find_bounds(a, row0, tile0 * 2 + (int)rank, step * 2, step * (kPairTile / kSeg), bars->bounds, &bars->done);
     } else {
+        rows_wait();
         const int quarter = warp & 3;
         Epilogue<kGroup / 32> ep;
-        ep.begin(a, row0, trans + quarter * (kTransBytes / 4));
+        ep.begin(a, row0, trans + quarter * (kTransBytes / 4), bars->bounds);
         const uint32_t empty0 = map_to_rank(smem_u32(&bars->tmem_empty[0]), 0);
         const uint32_t empty1 = map_to_rank(smem_u32(&bars->tmem_empty[1]), 0);
         uint32_t local = 0;
@@ -431,8 +554,10 @@ __global__ void __launch_bounds__(kThreadsH, 1)
                 }
                 if (v0 < a.V && row0 + g * 32 < a.R) ep.block(a, g, row0, v0, v);
             }
+            if (local == 0) ep.first_done(a, row0);
         }
         ep.leave();
+        *const_cast<volatile uint32_t*>(&bars->done) = 1u;
     }
     tc_fence_before();
     __syncthreads();
@@ -442,14 +567,14 @@ __global__ void __launch_bounds__(kThreadsH, 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols)
                      : "memory");
     }
+    rows_wait();
     publish(a, trans, tile0 * 2 + (int)rank, row0, min(kGroup, a.R - row0));
 }
 
 // ---------------------------------------------------------------------------
 // One CTA per hidden row: join the statistics, pick the alternatives.
 
-constexpr int kThreadsF = 256;
-constexpr int kWarpsF = kThreadsF / 32;
+constexpr int kThreadsF = kSelThreads;
 
 struct FinishArgs {
     int Rp, V, n_parts, segs, top_n;
@@ -458,64 +583,78 @@ struct FinishArgs {
     const float4* part;
     const float* seg_max;
     const float* scores;
+    uint32_t* bound;
+    uint32_t* seen;
     float *logprob, *entropy, *lse;
     int32_t* top_ids;
     float* top_logprobs;
 };
 
+// A row's blocks of scores for select_top.
+struct Blocks {
+    using Item = float;
+    const FinishArgs& a;
+    int row;
+    __device__ __forceinline__ float max(int g) const { return a.seg_max[(size_t)row * a.segs + g]; }
+    __device__ __forceinline__ float load(int g) const {
+        return a.scores[((size_t)g * a.Rp + row) * kSeg + (threadIdx.x & 31)];
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(float x, int g, F take) const {
+        const long long v = (long long)g * kSeg + (threadIdx.x & 31);
+        take(v < a.V ? make_key(x, (uint32_t)v) : 0ull);
+    }
+};
+
 __global__ void __launch_bounds__(kThreadsF) k_head_logprobs_finish(const FinishArgs a) {
-    __shared__ unsigned long long s_top[kWarpsF][32];
+    constexpr int kHeld = 5;  // shares of the statistics a lane of warp 0 loads at once (152 CTAs)
+    __shared__ SelectSmem s_sel;
+    __shared__ RowStat s_rs;
     rows_launch_dependents();
     rows_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x;
-    RowStat rs{};
+    float4 p[kHeld];
+    const int tok = a.tokens != nullptr ? a.tokens[row] : -1;
+    const bool given = tok >= 0 && tok < a.V;
+    const float tok_score = given ? a.tok_score[row] : 0.f;
     if (warp == 0) {
-        Stat st = stat_none();
-        for (int i = lane; i < a.n_parts; i += 32) {
-            const float4 p = a.part[(size_t)i * a.Rp + row];
-            st = stat_join(st, Stat{p.x, p.y, p.z});
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int q = i * 32 + lane;
+            p[i] = q < a.n_parts ? a.part[(size_t)q * a.Rp + row] : make_float4(neg_inf(), 0.f, 0.f, 0.f);
         }
-        rs = stat_finish(stat_warp(st));
+    }
+    auto join = [&] {
+        if (warp != 0) return;
+        Stat st = stat_none();
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) st = stat_join(st, Stat{p[i].x, p[i].y, p[i].z});
+        for (int q = kHeld * 32 + lane; q < a.n_parts; q += 32) {
+            const float4 o = a.part[(size_t)q * a.Rp + row];
+            st = stat_join(st, Stat{o.x, o.y, o.z});
+        }
+        const RowStat rs = stat_finish(stat_warp(st));
         if (lane == 0) {
-            const int tok = a.tokens != nullptr ? a.tokens[row] : -1;
-            if (a.logprob != nullptr)
-                a.logprob[row] = (tok >= 0 && tok < a.V) ? stat_logprob(rs, a.tok_score[row]) : 0.f;
+            s_rs = rs;
+            if (a.logprob != nullptr) a.logprob[row] = given ? stat_logprob(rs, tok_score) : 0.f;
             if (a.entropy != nullptr) a.entropy[row] = rs.entropy;
             if (a.lse != nullptr) a.lse[row] = rs.lse;
         }
+    };
+    if (a.top_n == 0) {
+        join();
+        return;
     }
-    if (a.top_n == 0) return;
-    const int n = a.top_n;
-    unsigned long long top = 0ull;
-    for (int g = warp * 32; g < a.segs; g += kThreadsF) {
-        const int gg = g + lane;
-        top_insert(top, gg < a.segs ? make_key(a.seg_max[(size_t)gg * a.Rp + row], (uint32_t)gg) : 0ull, n);
-    }
-    s_top[warp][lane] = top;
-    __syncthreads();
-    unsigned long long best = s_top[0][lane];
-#pragma unroll
-    for (int w = 1; w < kWarpsF; ++w) top_merge(best, s_top[w][lane]);
-    __syncthreads();
-    top = 0ull;
-    for (int i = warp; i < n; i += kWarpsF) {
-        const unsigned long long kseg = __shfl_sync(0xFFFFFFFFu, best, i);
-        if (kseg == 0ull) break;
-        const uint32_t g = key_gid(kseg);
-        const long long v = (long long)g * kSeg + lane;
-        const float x = a.scores[((size_t)g * a.Rp + row) * kSeg + lane];
-        top_insert(top, v < a.V ? make_key(x, (uint32_t)v) : 0ull, n);
-    }
-    s_top[warp][lane] = top;
-    __syncthreads();
-    if (warp != 0) return;
-#pragma unroll
-    for (int w = 1; w < kWarpsF; ++w) top_merge(top, s_top[w][lane]);
-    if (lane < n) {
-        const size_t o = (size_t)row * n + lane;
-        a.top_ids[o] = top != 0ull ? (int32_t)key_gid(top) : -1;
-        a.top_logprobs[o] = top != 0ull ? stat_logprob(rs, key_score(top)) : neg_inf();
+    const uint32_t floor = a.bound[row];
+    select_top(s_sel, a.segs, a.top_n, floor, Blocks{a, row}, join, [&](int i, unsigned long long k) {
+        const size_t o = (size_t)row * a.top_n + i;
+        a.top_ids[o] = k != 0ull ? (int32_t)key_gid(k) : -1;
+        a.top_logprobs[o] = k != 0ull ? stat_logprob(s_rs, key_score(k)) : neg_inf();
+    });
+    if (threadIdx.x == 0) {  // for the next call
+        a.bound[row] = 0u;
+        if (row < kMaxGroups) a.seen[row] = 0u;
     }
 }
 
@@ -525,11 +664,15 @@ struct Layout {
     int Rp, segs;
     size_t tok, part, seg_max, scores, total;
 };
+// Bounds and counts at a fixed place, so that a workspace serves calls of any size.
+constexpr size_t kBoundAt = kWsHeaderBytes + kMaxGroups * 4;
+constexpr size_t kZeroed = 8192;
+static_assert(kBoundAt + (size_t)kPassRows * 4 <= kZeroed, "zeroed part of the workspace");
 static Layout layout(int R, int V, int top_n) {
     Layout l;
     l.Rp = (std::min(R, kPassRows) + 31) / 32 * 32;
     l.segs = (int)(((long long)V + kSeg - 1) / kSeg);
-    l.tok = kWsHeaderBytes;
+    l.tok = kZeroed;
     l.part = l.tok + (size_t)l.Rp * 4;
     l.seg_max = l.part + (size_t)kMaxParts * l.Rp * 16;
     l.scores = l.seg_max + (top_n > 0 ? (size_t)l.segs * l.Rp * 4 : 0);
@@ -547,17 +690,14 @@ static cudaError_t launch_tc(K kernel, int grid, size_t smem, int cluster, cudaS
     cfg.blockDim = dim3(kThreadsH);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    if (cluster > 1) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)cluster;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    } else {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-    }
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, mw, mx, a);
 }
 
@@ -600,6 +740,10 @@ static cudaError_t pass(const HeadLogprobArgs& h, int r0, int nr, cudaStream_t s
     a.part = reinterpret_cast<float4*>(base + l.part);
     a.seg_max = h.top_n > 0 ? reinterpret_cast<float*>(base + l.seg_max) : nullptr;
     a.scores = reinterpret_cast<float*>(base + l.scores);
+    a.segs = l.segs;
+    a.top_n = h.top_n;
+    a.seen = reinterpret_cast<uint32_t*>(base + kWsHeaderBytes);
+    a.bound = reinterpret_cast<uint32_t*>(base + kBoundAt);
     a.err = reinterpret_cast<unsigned int*>(base + kWsErrorOffset);
     const uint16_t* x = h.x + (size_t)r0 * h.H;
     alignas(64) CUtensorMap mw, mx;
@@ -634,6 +778,8 @@ static cudaError_t pass(const HeadLogprobArgs& h, int r0, int nr, cudaStream_t s
     f.part = a.part;
     f.seg_max = a.seg_max;
     f.scores = a.scores;
+    f.seen = a.seen;
+    f.bound = a.bound;
     f.logprob = h.logprob ? h.logprob + r0 : nullptr;
     f.entropy = h.entropy ? h.entropy + r0 : nullptr;
     f.lse = h.lse ? h.lse + r0 : nullptr;

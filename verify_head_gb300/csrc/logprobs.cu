@@ -7,12 +7,9 @@
 // Forward: one pass over the logits.  A row is cut into slots of 16 aligned
 // bytes and segments of 32 slots (one warp load).  Each thread keeps a running
 // maximum and the two sums of Stat; where alternatives are wanted the warp
-// also writes each segment's maximum.  The n largest elements of a row lie in
-// the n segments with the largest maxima (equal maxima: the lower segment
-// first, since a segment is a range of ids): any element of another segment
-// is preceded by n others.  So the row's last CTA picks those segments from
-// the maxima, reads them again (n x 512 bytes) and sorts their elements; no
-// threshold search, and no input makes it slower.
+// also writes each segment's maximum, and the row's last CTA picks the
+// alternatives from the segments with the largest maxima (select_top), reading
+// about n segments of 512 bytes again.
 //
 // A row is split over several CTAs when there are few rows; their statistics
 // meet in the workspace and the last CTA of a row (a ticket per row, left
@@ -27,7 +24,7 @@
 namespace vh {
 namespace lp {
 
-constexpr int kThreadsL = 256;
+constexpr int kThreadsL = kSelThreads;
 constexpr int kWarpsL = kThreadsL / 32;
 constexpr int kUnroll = 4;            // segments in flight per warp
 constexpr int kTargetCtas = 608;      // CTAs wanted on the GPU at once (four per SM)
@@ -63,6 +60,29 @@ struct Row {
     }
 };
 
+// A row's segments for select_top.
+template <typename T>
+struct Segments {
+    struct Item {
+        float f[kVecOf<T>];
+    };
+    const Row<T>& x;
+    const float* maxima;
+    __device__ __forceinline__ float max(int g) const { return __ldcg(maxima + g); }
+    __device__ __forceinline__ Item load(int g) const {
+        Item it;
+        x.load(g * 32 + (threadIdx.x & 31), it.f);
+        return it;
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(const Item& it, int g, F take) const {
+        const long long e0 = x.first(g * 32 + (threadIdx.x & 31));
+#pragma unroll
+        for (int j = 0; j < kVecOf<T>; ++j)
+            take(e0 + j >= 0 && e0 + j < x.V ? make_key(it.f[j], (uint32_t)(e0 + j)) : 0ull);
+    }
+};
+
 // Upper bound of the segments of a row of V elements of `size` bytes, whatever its alignment.
 __host__ __device__ inline int max_segs(int V, int size) {
     const long long per = 512 / size;
@@ -92,7 +112,8 @@ template <typename T>
 __global__ void __launch_bounds__(kThreadsL, 4) k_logprobs(const LogprobArgs a, const Ws ws, const Plan pl) {
     constexpr int VEC = kVecOf<T>;
     __shared__ float4 s_part[kWarpsL];
-    __shared__ unsigned long long s_top[kWarpsL][32];
+    __shared__ SelectSmem s_sel;
+    __shared__ RowStat s_rs;
     __shared__ int s_last;
     rows_launch_dependents();
     rows_wait();
@@ -103,42 +124,60 @@ __global__ void __launch_bounds__(kThreadsL, 4) k_logprobs(const LogprobArgs a, 
     const int g0 = (int)((long long)segs * blockIdx.x / gridDim.x), g1 = (int)((long long)segs * (blockIdx.x + 1) / gridDim.x);
     float* seg_max = ws.seg_max + (size_t)row * pl.segs;
 
-    Stat st = stat_none();
+    // Segments [in0, in1) hold whole slots only.
+    const int in0 = x.shift != 0 ? 1 : 0;
+    const int in1 = (int)(((long long)a.V + x.shift) / (32 * VEC));
+    Stat2 run;
+    run.clear();
+    auto add = [&](const RawVec<T, VEC>& r) {
+        const F2 mc = f2(-run.c, -run.c);
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) run.add(r.get(i), r.get(i + 1), mc);
+    };
+    auto keep_max = [&](int g, float m) {
+        if (a.top_n > 0) {
+            float w;
+            asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(w) : "f"(m));
+            if (lane == 0) seg_max[g] = w;
+        }
+    };
     for (int g = g0 + warp; g < g1; g += kWarpsL * kUnroll) {
-        float f[kUnroll][VEC];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int gg = g + u * kWarpsL;
-            if (gg < g1) {
-                x.load(gg * 32 + lane, f[u]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) f[u][i] = neg_inf();
-            }
-        }
-        float m = neg_inf();
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            float mu = f[u][0];
-#pragma unroll
-            for (int i = 1; i < VEC; ++i) mu = fmaxf(mu, f[u][i]);
-            mu = fmaxf(mu, neg_inf());  // a slot of NaNs
-            m = fmaxf(m, mu);
-            const int gg = g + u * kWarpsL;
-            if (a.top_n > 0 && gg < g1) {
-                float w;
-                asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(w) : "f"(mu));
-                if (lane == 0) seg_max[gg] = w;
-            }
-        }
-        if (m > st.c) stat_shift(st, m);
-        if (st.c != neg_inf()) {
+        const int last = g + (kUnroll - 1) * kWarpsL;
+        if (g >= in0 && last < min(g1, in1)) {
+            RawVec<T, VEC> r[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u)
+                r[u].load(reinterpret_cast<const T*>(x.base + ((size_t)(g + u * kWarpsL) * 32 + lane) * 16));
+            float m = neg_inf();
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) stat_add(st, f[u][i]);
+            for (int u = 0; u < kUnroll; ++u) {
+                const float mu = r[u].max();
+                m = fmaxf(m, mu);
+                keep_max(g + u * kWarpsL, mu);
+            }
+            run.raise(m);
+            if (run.c != neg_inf()) {
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) add(r[u]);
+            }
+        } else {  // a row's ends
+            for (int gg = g; gg < g1 && gg <= last; gg += kWarpsL) {
+                float f[VEC];
+                x.load(gg * 32 + lane, f);
+                float m = neg_inf();
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) m = fmaxf(m, f[i]);
+                keep_max(gg, m);
+                run.raise(m);
+                if (run.c != neg_inf()) {
+                    const F2 mc = f2(-run.c, -run.c);
+#pragma unroll
+                    for (int i = 0; i < VEC; i += 2) run.add(f[i], f[i + 1], mc);
+                }
+            }
         }
     }
+    Stat st = run.get();
     st = stat_warp(st);
     if (lane == 0) s_part[warp] = make_float4(st.c, st.s, st.t, 0.f);
     __syncthreads();
@@ -179,46 +218,14 @@ __global__ void __launch_bounds__(kThreadsL, 4) k_logprobs(const LogprobArgs a, 
         }
     }
     if (a.top_n == 0) return;
-
-    // The top_n segments with the largest maxima: each warp sorts its share, warp 0 joins the lists.
-    const int n = a.top_n;
-    unsigned long long top = 0ull;
-    for (int g = warp * 32; g < segs; g += kThreadsL) {
-        const int gg = g + lane;
-        const unsigned long long k = gg < segs ? make_key(__ldcg(seg_max + gg), (uint32_t)gg) : 0ull;
-        top_insert(top, k, n);
-    }
-    s_top[warp][lane] = top;
-    __syncthreads();
-    unsigned long long best = s_top[0][lane];
-#pragma unroll
-    for (int w = 1; w < kWarpsL; ++w) top_merge(best, s_top[w][lane]);
-    __syncthreads();
-    // Their elements, a segment per warp at a time.
-    top = 0ull;
-    for (int i = warp; i < n; i += kWarpsL) {
-        const unsigned long long kseg = __shfl_sync(0xFFFFFFFFu, best, i);
-        if (kseg == 0ull) break;
-        const int slot = (int)key_gid(kseg) * 32 + lane;
-        float f[VEC];
-        x.load(slot, f);
-        const long long e0 = x.first(slot);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const bool in = e0 + j >= 0 && e0 + j < a.V;
-            top_insert(top, in ? make_key(f[j], (uint32_t)(e0 + j)) : 0ull, n);
-        }
-    }
-    s_top[warp][lane] = top;
-    __syncthreads();
-    if (warp != 0) return;
-#pragma unroll
-    for (int w = 1; w < kWarpsL; ++w) top_merge(top, s_top[w][lane]);
-    if (lane < n) {
-        const size_t o = (size_t)row * n + lane;
-        a.top_ids[o] = top != 0ull ? (int32_t)key_gid(top) : -1;
-        a.top_logprobs[o] = top != 0ull ? stat_logprob(rs, key_score(top)) : neg_inf();
-    }
+    if (threadIdx.x == 0) s_rs = rs;  // select_top has barriers before it emits
+    select_top(
+        s_sel, segs, a.top_n, 0u, Segments<T>{x, seg_max}, [] {},
+        [&](int i, unsigned long long k) {
+            const size_t o = (size_t)row * a.top_n + i;
+            a.top_ids[o] = k != 0ull ? (int32_t)key_gid(k) : -1;
+            a.top_logprobs[o] = k != 0ull ? stat_logprob(s_rs, key_score(k)) : neg_inf();
+        });
 }
 
 // ---------------------------------------------------------------------------

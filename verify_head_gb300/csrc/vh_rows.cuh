@@ -72,6 +72,18 @@ struct RawVec {
         }
     }
     __device__ __forceinline__ void load(const T* p) { q = *reinterpret_cast<const uint4*>(p); }
+    // The largest element, NaN left out (-inf if there is nothing else).
+    __device__ __forceinline__ float max() const {
+        if constexpr (sizeof(T) == 4) {
+            const float m = fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3)));
+            return fmaxf(m, -__int_as_float(0x7f800000));
+        } else {
+            using P = typename std::conditional<std::is_same<T, __nv_bfloat16>::value, __nv_bfloat162, __half2>::type;
+            const P* p = reinterpret_cast<const P*>(u);
+            const P m = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+            return fmaxf(fmaxf(to_f32(m.x), to_f32(m.y)), -__int_as_float(0x7f800000));
+        }
+    }
     __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = q; }
 };
 
@@ -138,12 +150,66 @@ __device__ __forceinline__ Stat stat_join(Stat a, Stat b) {
     return Stat{c, a.s + b.s, a.t + b.t};
 }
 
-__device__ __forceinline__ void stat_add(Stat& a, float x) {  // a.c >= x, not -inf
-    const float y = fmaxf((x - a.c) * kLog2e, kFloorY);
-    const float e = ex2(y);
-    a.s += e;
-    a.t = fmaf(e, y, a.t);
+// Two floats in one register pair: the packed fp32 instructions issue once for both.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
 }
+__device__ __forceinline__ float2 f2_get(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// The same statistics with the sums in two halves, for long runs of scores.
+struct Stat2 {
+    float c;
+    F2 s, t;
+    __device__ __forceinline__ void clear() {
+        c = neg_inf();
+        s = t = f2(0.f, 0.f);
+    }
+    __device__ __forceinline__ Stat get() const {
+        const float2 a = f2_get(s), b = f2_get(t);
+        return Stat{c, a.x + a.y, b.x + b.y};
+    }
+    __device__ __forceinline__ void raise(float m) {  // a new maximum
+        if (m > c) {
+            Stat a = get();
+            stat_shift(a, m);
+            c = m;
+            s = f2(a.s, 0.f);
+            t = f2(a.t, 0.f);
+        }
+    }
+    // Two scores; c is their maximum or more, not -inf.  minus_c = (-c, -c).
+    __device__ __forceinline__ void add(float x0, float x1, F2 minus_c) {
+        const float2 y = f2_get(f2_mul(f2_add(f2(x0, x1), minus_c), f2(kLog2e, kLog2e)));
+        const float y0 = fmaxf(y.x, kFloorY), y1 = fmaxf(y.y, kFloorY);
+        const F2 e = f2(ex2(y0), ex2(y1));
+        s = f2_add(s, e);
+        t = f2_fma(e, f2(y0, y1), t);
+    }
+};
 
 __device__ __forceinline__ Stat stat_warp(Stat a) {
 #pragma unroll
@@ -229,6 +295,161 @@ __device__ __forceinline__ void top_merge(unsigned long long& top, unsigned long
 __device__ __forceinline__ void top_insert(unsigned long long& top, unsigned long long key, int n) {
     const unsigned long long floor = __shfl_sync(0xFFFFFFFFu, top, n - 1);
     if (__any_sync(0xFFFFFFFFu, key > floor)) top_merge(top, top_sort(key));
+}
+
+// ---------------------------------------------------------------------------
+// The n <= kMaxTop largest elements of a row from its segments' maxima, by a
+// CTA of kSelThreads threads.  The n largest elements lie in the n segments
+// with the largest maxima (equal maxima: the lower segment first, since a
+// segment is a range of ids): any element elsewhere is preceded by n others.
+//
+// Usual way, a few dependent steps in all: 64 groups of segments give a bound
+// (the n-th largest of their maxima: n elements at least reach it, and about
+// 1.2 n segments do); the segments that reach the bound are listed, then their
+// elements that do; an element's place is the number of listed keys above its
+// own.  Where a list overflows (many elements equal to the bound, as in a row
+// that is masked to fewer than n places) the CTA sorts instead: each warp
+// keeps the 32 largest keys of its share, first of the maxima, then of the
+// elements of the n best segments, and the lists are merged.
+
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelGroups = 64;
+constexpr int kSelSegs = 128;   // listed segments
+constexpr int kSelElems = 256;  // listed elements
+
+struct SelectSmem {
+    uint32_t group[kSelGroups];
+    uint32_t seg[kSelSegs];
+    unsigned long long elem[kSelElems];
+    unsigned long long sorted[kSelWarps][32];
+    uint32_t bound;
+    int n_seg, n_elem;
+};
+
+// Segs: float max(int g), the maximum of segment g < segs (NaN left out);
+//   Item load(int g), this lane's elements of segment g (the warp loads it together);
+//   void each(const Item&, int g, f): f(key) with the argmax key of each of them, 0 for a place outside the row.
+// meanwhile(): called once, after the maxima are requested and before they are used.
+// emit(i, key): key of the i-th largest element, i < n (0 = the row has fewer).
+// floor: ord_f32 of a value that n elements are known to reach, 0 = none.
+// All threads call it; sm.n_seg, sm.n_elem and sm.bound need not be set.
+template <typename Segs, typename Meanwhile, typename Emit>
+__device__ __forceinline__ void select_top(SelectSmem& sm, int segs, int n, uint32_t floor, const Segs& sg,
+                                           Meanwhile meanwhile, Emit emit) {
+    constexpr int kHeld = 32;    // maxima a thread holds in registers
+    constexpr int kAtOnce = 4;   // segments a warp loads at once
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float held[kHeld];
+    auto hold = [&](int base) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int g = base + i * kSelThreads + tid;
+            held[i] = g < segs ? sg.max(g) : neg_inf();
+        }
+    };
+    hold(0);
+    meanwhile();
+    float m = held[0];
+#pragma unroll
+    for (int i = 1; i < kHeld; ++i) m = fmaxf(m, held[i]);
+    for (int base = kHeld * kSelThreads; base < segs; base += kHeld * kSelThreads) {
+        hold(base);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) m = fmaxf(m, held[i]);
+    }
+    const uint32_t mine = tid < segs ? ord_f32(m) : 0u;
+    uint32_t grp = max(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1));
+    grp = max(grp, __shfl_xor_sync(0xFFFFFFFFu, grp, 2));
+    if ((lane & 3) == 0) sm.group[tid >> 2] = grp;
+    if (tid == 0) sm.n_seg = sm.n_elem = 0;
+    __syncthreads();
+    if (tid < kSelGroups) {
+        const uint32_t me = sm.group[tid];
+        int above = 0;
+#pragma unroll
+        for (int j = 0; j < kSelGroups; j += 4) {
+            const uint4 o = *reinterpret_cast<const uint4*>(sm.group + j);
+            above += (o.x > me || (o.x == me && j < tid)) + (o.y > me || (o.y == me && j + 1 < tid)) +
+                     (o.z > me || (o.z == me && j + 2 < tid)) + (o.w > me || (o.w == me && j + 3 < tid));
+        }
+        if (above == n - 1) sm.bound = max(me, floor);
+    }
+    __syncthreads();
+    const uint32_t bound = sm.bound;
+    if (mine >= bound && mine != 0u) {
+        for (int base = 0; base < segs; base += kHeld * kSelThreads) {
+            if (segs > kHeld * kSelThreads) hold(base);
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                const int g = base + i * kSelThreads + tid;
+                if (g < segs && ord_f32(held[i]) >= bound) {
+                    const int e = atomicAdd(&sm.n_seg, 1);
+                    if (e < kSelSegs) sm.seg[e] = (uint32_t)g;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const int n_seg = sm.n_seg;
+    if (n_seg <= kSelSegs) {
+        for (int i0 = warp; i0 < n_seg; i0 += kSelWarps * kAtOnce) {
+            typename Segs::Item it[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int i = i0 + u * kSelWarps;
+                if (i < n_seg) it[u] = sg.load((int)sm.seg[i]);
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int i = i0 + u * kSelWarps;
+                if (i < n_seg)
+                    sg.each(it[u], (int)sm.seg[i], [&](unsigned long long k) {
+                        if ((uint32_t)(k >> 32) >= bound && k != 0ull) {
+                            const int e = atomicAdd(&sm.n_elem, 1);
+                            if (e < kSelElems) sm.elem[e] = k;
+                        }
+                    });
+            }
+        }
+        __syncthreads();
+        const int m2 = sm.n_elem;
+        if (m2 <= kSelElems) {
+            if (tid < m2) {
+                const unsigned long long k = sm.elem[tid];
+                int above = 0;
+                for (int j = 0; j < m2; ++j) above += sm.elem[j] > k;
+                if (above < n) emit(above, k);
+            } else if (tid < n) {
+                emit(tid, 0ull);  // fewer elements than n
+            }
+            return;
+        }
+    }
+    // Sorted lists.
+    unsigned long long top = 0ull;
+    for (int g = warp * 32; g < segs; g += kSelThreads) {
+        const int gg = g + lane;
+        top_insert(top, gg < segs ? make_key(sg.max(gg), (uint32_t)gg) : 0ull, n);
+    }
+    sm.sorted[warp][lane] = top;
+    __syncthreads();
+    unsigned long long best = sm.sorted[0][lane];
+#pragma unroll
+    for (int w = 1; w < kSelWarps; ++w) top_merge(best, sm.sorted[w][lane]);
+    __syncthreads();
+    top = 0ull;
+    for (int i = warp; i < n; i += kSelWarps) {
+        const unsigned long long kseg = __shfl_sync(0xFFFFFFFFu, best, i);
+        if (kseg == 0ull) break;
+        sg.each(sg.load((int)key_gid(kseg)), (int)key_gid(kseg), [&](unsigned long long k) { top_insert(top, k, n); });
+    }
+    sm.sorted[warp][lane] = top;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < kSelWarps; ++w) top_merge(top, sm.sorted[w][lane]);
+    if (lane < n) emit(lane, top);
 }
 
 }  // namespace vh
