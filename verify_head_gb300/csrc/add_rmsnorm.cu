@@ -27,32 +27,37 @@ namespace norm {
 constexpr int kMaxThreads = 512;  // register-resident rows: up to 128 registers a thread
 constexpr int kWideThreads = 512;
 
-// Sums of two values over the warps of one row (threadIdx.y) of the CTA.
-// `max_second`: the second value is a maximum instead of a sum.  All threads
-// of the CTA call it; `slot` alternates between calls.
+// Sums of two values over the threads of one row (threadIdx.y) of the CTA.
+// MAX_SECOND: the second value is a maximum instead of a sum.  All threads of
+// the CTA call it; `slot` alternates between calls.  The lower half of a warp
+// goes on with the first value and the upper half with the second, so both
+// take one chain of shuffles.
 template <bool MAX_SECOND>
 __device__ __forceinline__ float2 reduce_row(float a, float b, float2 (*red)[32], int slot) {
+    const int lane = threadIdx.x & 31;
+    const bool second = lane >= 16;
+    auto join = [&](float v, float o) { return MAX_SECOND && second ? fmaxf(v, o) : v + o; };
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, second ? a : b, 16);
+    float v = join(second ? b : a, other);
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) {
-        a += __shfl_xor_sync(0xFFFFFFFFu, a, m);
-        const float o = __shfl_xor_sync(0xFFFFFFFFu, b, m);
-        b = MAX_SECOND ? fmaxf(b, o) : b + o;
-    }
+    for (int m = 8; m >= 1; m >>= 1) v = join(v, __shfl_xor_sync(0xFFFFFFFFu, v, m));
     const int wpr = blockDim.x >> 5;
-    if (wpr == 1) return make_float2(a, b);
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    if (wpr == 1) return make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
     float2* row = red[slot] + threadIdx.y * wpr;
-    if (lane == 0) row[w] = make_float2(a, b);
+    if ((lane & 15) == 0) reinterpret_cast<float*>(row + (threadIdx.x >> 5))[lane >> 4] = v;
     __syncthreads();
-    float2 v = lane < wpr ? row[lane] : make_float2(0.f, 0.f);
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) {
-        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, m);
-        const float o = __shfl_xor_sync(0xFFFFFFFFu, v.y, m);
-        v.y = MAX_SECOND ? fmaxf(v.y, o) : v.y + o;
+    float2 t = row[0];
+#pragma unroll 4
+    for (int w = 1; w < wpr; ++w) {
+        const float2 o = row[w];
+        t.x += o.x;
+        t.y = MAX_SECOND ? fmaxf(t.y, o.y) : t.y + o.y;
     }
-    return v;
+    return t;
 }
+
+// 1 / sqrt(sum / H + eps).
+__device__ __forceinline__ float row_rstd(float sum, float inv_h, float eps) { return rsqrtf(fmaf(sum, inv_h, eps)); }
 
 template <typename T, int VEC>
 __device__ __forceinline__ void load_weight(const void* w, int w32, size_t i, float off, float (&f)[VEC]) {
@@ -93,22 +98,39 @@ __device__ __forceinline__ Quant make_quant(float amax, float q) {
     return z;
 }
 
+// Codes of VEC elements.  |u inv| is at most Q up to a few roundings, so rounding cannot leave the codes' range.
+// int8: added to 1.5 * 2^23 a float's low byte is the nearest integer (ties to even) in two's complement; the
+// float-to-integer conversion runs at an eighth of that addition's rate.
 template <int VEC>
 __device__ __forceinline__ void store_codes(uint8_t* p, const float (&u)[VEC], const Quant& z, int out) {
-    uint32_t b[VEC];
+    constexpr float kRound = 12582912.0f;
+    float v[VEC];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-        const float v = (u[k] * z.pre) * z.inv;
-        b[k] = out == VH_NORM_INT8 ? (uint32_t)(max(-127, min(127, __float2int_rn(v))) & 0xFF)
-                                   : (uint32_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+    for (int k = 0; k < VEC; ++k) v[k] = __fmul_rn(u[k], z.inv);  // rounded before the addition below, not fused with it
+    if (z.pre != 1.0f) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[k] = __fmul_rn(u[k] * z.pre, z.inv);
     }
     if constexpr (VEC == 1) {
-        p[0] = (uint8_t)b[0];
+        p[0] = out == VH_NORM_INT8 ? (uint8_t)__float_as_uint(v[0] + kRound)
+                                   : (uint8_t)__nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
     } else {
         uint32_t w[VEC / 4];
+        if (out == VH_NORM_INT8) {
 #pragma unroll
-        for (int k = 0; k < VEC / 4; ++k)
-            w[k] = b[4 * k] | (b[4 * k + 1] << 8) | (b[4 * k + 2] << 16) | (b[4 * k + 3] << 24);
+            for (int k = 0; k < VEC; k += 4) {
+                const uint32_t lo = __byte_perm(__float_as_uint(v[k] + kRound), __float_as_uint(v[k + 1] + kRound), 0x0040);
+                const uint32_t hi = __byte_perm(__float_as_uint(v[k + 2] + kRound), __float_as_uint(v[k + 3] + kRound), 0x0040);
+                w[k / 4] = __byte_perm(lo, hi, 0x5410);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < VEC; k += 4) {
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[k], v[k + 1]), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[k + 2], v[k + 3]), __NV_SATFINITE, __NV_E4M3);
+                w[k / 4] = lo | (hi << 16);
+            }
+        }
         if constexpr (VEC == 8)
             *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
         else
@@ -161,7 +183,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a) {
         }
     }
     const float2 tot = reduce_row<true>(ss, amax, red, 0);
-    const float rstd = 1.0f / sqrtf(tot.x / (float)a.H + a.eps);
+    const float rstd = row_rstd(tot.x, a.inv_h, a.eps);
     if (!live) return;
     if (a.out == VH_NORM_SAME) {
         T* y = static_cast<T*>(a.y) + row * a.y_stride;
@@ -221,7 +243,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(const NormArgs a) {
         }
     }
     const float2 tot = reduce_row<true>(ss, amax, red, 0);
-    const float rstd = 1.0f / sqrtf(tot.x / (float)a.H + a.eps);
+    const float rstd = row_rstd(tot.x, a.inv_h, a.eps);
     const float q = a.out == VH_NORM_INT8 ? 127.0f : 448.0f;
     const Quant z = make_quant(tot.y, q);
     for (int v = threadIdx.x; v < nvec; v += kWideThreads) {
@@ -264,27 +286,42 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_grad(const NormGradArgs a)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) dw[j][k] = 0.f;
     int slot = 0;
-    for (long long row = blockIdx.x; row < a.T; row += gridDim.x, slot ^= 1) {
+    // a token's loads are issued while the one before it is reduced and written
+    RawVec<T, VEC> hv[NV], yv[NV], ev[NV], hn[NV], yn[NV], en[NV];
+    auto load = [&](long long row) {
         const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
         const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
         const T* dh = static_cast<const T*>(a.dh) + row * a.dh_stride;
-        RawVec<T, VEC> hv[NV], yv[NV], ev[NV];
-        float w[NV][VEC];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            if (v < nvec) {
+                hn[j].load(h + (size_t)v * VEC);
+                yn[j].load(dy + (size_t)v * VEC);
+                if (a.dh != nullptr) en[j].load(dh + (size_t)v * VEC);
+            }
+        }
+    };
+    float w[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        if (v < nvec) load_weight<T, VEC>(a.w, a.w32, (size_t)v * VEC, a.w_offset, w[j]);
+    }
+    if (blockIdx.x < a.T) load(blockIdx.x);
+    for (long long row = blockIdx.x; row < a.T; row += gridDim.x, slot ^= 1) {
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
-            if (v < nvec) {
-                hv[j].load(h + (size_t)v * VEC);
-                yv[j].load(dy + (size_t)v * VEC);
-                if (a.dh != nullptr) ev[j].load(dh + (size_t)v * VEC);
-            }
+            hv[j] = hn[j];
+            yv[j] = yn[j];
+            ev[j] = en[j];
         }
+        if (row + gridDim.x < a.T) load(row + gridDim.x);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int v = threadIdx.x + j * blockDim.x;
             if (v < nvec) {
-                load_weight<T, VEC>(a.w, a.w32, (size_t)v * VEC, a.w_offset, w[j]);
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) {
                     const float f = hv[j].get(k);
@@ -294,8 +331,8 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_grad(const NormGradArgs a)
             }
         }
         const float2 tot = reduce_row<false>(ss, dot, red, slot);
-        const float rstd = 1.0f / sqrtf(tot.x / (float)a.H + a.eps);
-        const float mean = tot.y * rstd / (float)a.H;  // mean(g n)
+        const float rstd = row_rstd(tot.x, a.inv_h, a.eps);
+        const float mean = tot.y * rstd * a.inv_h;  // mean(g n)
         T* dx = static_cast<T*>(a.dx) + row * a.dx_stride;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -356,8 +393,8 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_grad_wide(const NormGradA
             }
         }
         const float2 tot = reduce_row<false>(ss, dot, red, slot);
-        const float rstd = 1.0f / sqrtf(tot.x / (float)a.H + a.eps);
-        const float mean = tot.y * rstd / (float)a.H;
+        const float rstd = row_rstd(tot.x, a.inv_h, a.eps);
+        const float mean = tot.y * rstd * a.inv_h;
         for (int v = threadIdx.x; v < nvec; v += kWideThreads) {
             RawVec<T, VEC> hv, yv, ev;
             float w[VEC], f[VEC];
@@ -381,16 +418,26 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_grad_wide(const NormGradA
     }
 }
 
-// dweight[c] = sum of part[0..n)[c], in order: 32 columns x 16 row groups per CTA.
-constexpr int kSumGroups = 16;
+// dweight[c] = sum of part[0..n)[c], in order: 32 columns x 32 row groups per CTA, loads in batches.
+constexpr int kSumGroups = 32;
 __global__ void __launch_bounds__(32 * kSumGroups) k_sum_parts(const float* part, int n, int H, float* out) {
+    constexpr int kBatch = 10;
     __shared__ float s[kSumGroups][33];
     rows_launch_dependents();
     rows_wait();
     const int c = blockIdx.x * 32 + threadIdx.x;
     float v = 0.f;
     if (c < H)
-        for (int r = threadIdx.y; r < n; r += kSumGroups) v += part[(size_t)r * H + c];
+        for (int r0 = threadIdx.y; r0 < n; r0 += kSumGroups * kBatch) {
+            float x[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int r = r0 + i * kSumGroups;
+                x[i] = r < n ? part[(size_t)r * H + c] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) v += x[i];
+        }
     s[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
     if (threadIdx.y == 0 && c < H) {
@@ -430,7 +477,9 @@ static cudaError_t norm_vec(const NormArgs& a, cudaStream_t s) {
         const int ty = std::max(1, 128 / tx);
         return launch(kernel, dim3((unsigned)((a.T + ty - 1) / ty)), dim3(tx, ty), s, a);
     };
-    if (nvec <= kMaxThreads) return go(k_norm<T, VEC, 1>, 1);
+    // Two vectors a thread: 16384 x 2048 bf16 36.8 us to int8, 40.4 us to bf16, against 42.4 / 41.2 us with one, 37.2 /
+    // 41.1 us with four and 41.3 / 43.5 us with eight (a warp per row).  One where that leaves less than two warps.
+    if (nvec <= 64) return go(k_norm<T, VEC, 1>, 1);
     if (nvec <= kMaxThreads * 2) return go(k_norm<T, VEC, 2>, 2);
     if (nvec <= kMaxThreads * 4) return go(k_norm<T, VEC, 4>, 4);
     return launch(k_norm_wide<T, VEC>, dim3((unsigned)a.T), dim3(kWideThreads), s, a);

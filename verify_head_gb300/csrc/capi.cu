@@ -474,6 +474,7 @@ vh_status vh_add_rmsnorm(const void* x, const void* residual, const void* weight
     a.out = out;
     a.eps = eps;
     a.w_offset = weight_offset;
+    a.inv_h = 1.0f / (float)H;
     return launch_status(vh::launch_add_rmsnorm(a, dtype, static_cast<cudaStream_t>(stream)));
 }
 
@@ -513,6 +514,7 @@ vh_status vh_add_rmsnorm_grad(const void* dy, const void* h, const void* weight,
     a.w32 = weight_f32 != 0 || dtype == VH_F32;
     a.eps = eps;
     a.w_offset = weight_offset;
+    a.inv_h = 1.0f / (float)H;
     return launch_status(vh::launch_add_rmsnorm_grad(a, dtype, dweight, static_cast<cudaStream_t>(stream)));
 }
 

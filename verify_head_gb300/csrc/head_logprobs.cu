@@ -243,10 +243,13 @@ struct Epilogue {
         }
         Stat2 run{st[g].c, f2(st[g].s, 0.f), f2(st[g].t, 0.f)};
         run.raise(m);
-        if (run.c != neg_inf()) {
-            const F2 mc = f2(-run.c, -run.c);
+        if (run.c > kLiftFrom && run.c < kNearLimit) {
+            const F2 mcl = run.minus_cl();
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) run.add(x[i], x[i + 1], mc);
+            for (int i = 0; i < 32; i += 2) run.add_plain(fmaxf(x[i], kLift), fmaxf(x[i + 1], kLift), mcl);
+        } else if (run.c != neg_inf()) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) run.add(x[i], x[i + 1]);
         }
         st[g] = run.get();
     }
@@ -599,10 +602,16 @@ struct Blocks {
     __device__ __forceinline__ float load(int g) const {
         return a.scores[((size_t)g * a.Rp + row) * kSeg + (threadIdx.x & 31)];
     }
+    __device__ __forceinline__ float peak(float x) const { return fmaxf(x, neg_inf()); }
     template <typename F>
-    __device__ __forceinline__ void each(float x, int g, F take) const {
+    __device__ __forceinline__ void each(float x, int g, float b, F take) const {
         const long long v = (long long)g * kSeg + (threadIdx.x & 31);
-        take(v < a.V ? make_key(x, (uint32_t)v) : 0ull);
+        if (!(x < b) && v < a.V) take(make_key(x, (uint32_t)v));
+    }
+    static constexpr int kBatches = 1;
+    __device__ __forceinline__ unsigned long long key(int g, int) const {
+        const long long v = (long long)g * kSeg + (threadIdx.x & 31);
+        return v < a.V ? make_key(load(g), (uint32_t)v) : 0ull;
     }
 };
 
@@ -647,7 +656,7 @@ __global__ void __launch_bounds__(kThreadsF) k_head_logprobs_finish(const Finish
         return;
     }
     const uint32_t floor = a.bound[row];
-    select_top(s_sel, a.segs, a.top_n, floor, Blocks{a, row}, join, [&](int i, unsigned long long k) {
+    select_top<32>(s_sel, a.segs, a.top_n, floor, Blocks{a, row}, join, [&](int i, unsigned long long k) {
         const size_t o = (size_t)row * a.top_n + i;
         a.top_ids[o] = k != 0ull ? (int32_t)key_gid(k) : -1;
         a.top_logprobs[o] = k != 0ull ? stat_logprob(s_rs, key_score(k)) : neg_inf();

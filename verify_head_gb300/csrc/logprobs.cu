@@ -4,16 +4,16 @@
 //     lse = log sum_v e^x_v      logprob = x_token - lse      entropy = lse - sum_v p_v x_v
 //     dx_v = g_lp ([v = token] - p_v) - g_ent p_v (log p_v + entropy)
 //
-// Forward: one pass over the logits.  A row is cut into slots of 16 aligned
-// bytes and segments of 32 slots (one warp load).  Each thread keeps a running
-// maximum and the two sums of Stat; where alternatives are wanted the warp
-// also writes each segment's maximum, and the row's last CTA picks the
-// alternatives from the segments with the largest maxima (select_top), reading
-// about n segments of 512 bytes again.
+// Forward: one pass over the logits.  A row is cut into slots of 32 aligned
+// bytes and segments of 32 slots (one warp load of 1 KiB).  Each thread keeps
+// a running maximum and the two sums of Stat; where alternatives are wanted
+// the warp also writes each segment's maximum, and a second kernel, one CTA
+// per row, picks the alternatives from the segments with the largest maxima
+// (select_top), reading about n segments again.
 //
-// A row is split over several CTAs when there are few rows; their statistics
-// meet in the workspace and the last CTA of a row (a ticket per row, left
-// zero again) finishes it.
+// All rows' segments are shared out evenly over one resident wave of CTAs; a
+// row that several CTAs hold pieces of meets in the workspace, where the last
+// of them (a ticket, left zero again), or the second kernel, finishes it.
 //
 // Bound: memory (the logits once; the gradient also writes them once).
 #include <algorithm>
@@ -26,36 +26,40 @@ namespace lp {
 
 constexpr int kThreadsL = kSelThreads;
 constexpr int kWarpsL = kThreadsL / 32;
-constexpr int kUnroll = 4;            // segments in flight per warp
-constexpr int kTargetCtas = 608;      // CTAs wanted on the GPU at once (four per SM)
-constexpr int kMinSegs = 2 * kWarpsL;  // segments per CTA below which a row is not cut further
+constexpr int kUnroll = 2;             // segments in flight per warp (and two more requested)
+// CTAs per SM.  Four for statistics alone (2048 x 65536 bf16: 45.2 against 47.4 us with three); with alternatives
+// the rows are few and three, with more registers each, are faster (129 x 40001 fp16: 18.4 against 19.2 us).
+constexpr int kPerSm = 4, kPerSmTop = 3;
+constexpr int kTargetCtas = 152 * kPerSm;
+constexpr int kMinSegs = 2 * kWarpsL;  // segments per CTA below which the work is not cut further
 
-// A row as aligned 16-byte slots: slot v holds elements [v * VEC - shift, +VEC).
+// A row as aligned 32-byte slots: slot v holds elements [v * kSlot - shift, +kSlot).
+constexpr int kSlotBytes = 32;
+template <typename T>
+constexpr int kSlot = kSlotBytes / (int)sizeof(T);
 template <typename T>
 struct Row {
-    const uint8_t* base;  // row address rounded down to 16 bytes
+    const uint8_t* base;  // row address rounded down to 32 bytes
     int shift;            // elements before the row's first one in slot 0
     int V;
     __device__ __forceinline__ Row(const T* p, int V_) : V(V_) {
         const uintptr_t u = reinterpret_cast<uintptr_t>(p);
-        base = reinterpret_cast<const uint8_t*>(u & ~uintptr_t(15));
-        shift = (int)((u & 15) / sizeof(T));
+        base = reinterpret_cast<const uint8_t*>(u & ~uintptr_t(kSlotBytes - 1));
+        shift = (int)((u & (kSlotBytes - 1)) / sizeof(T));
     }
-    __device__ __forceinline__ int slots() const { return (int)(((long long)V + shift + kVecOf<T> - 1) / kVecOf<T>); }
-    __device__ __forceinline__ long long first(int slot) const { return (long long)slot * kVecOf<T> - shift; }
+    __device__ __forceinline__ int slots() const { return (int)(((long long)V + shift + kSlot<T> - 1) / kSlot<T>); }
+    __device__ __forceinline__ long long first(int slot) const { return (long long)slot * kSlot<T> - shift; }
     // Elements of a slot; places outside the row (and whole slots past the end) read as -inf.
-    __device__ __forceinline__ void load(int slot, float (&f)[kVecOf<T>]) const {
-        constexpr int VEC = kVecOf<T>;
+    __device__ __forceinline__ void load(int slot, RawVec<T, kSlot<T>>& r) const {
         const long long e0 = first(slot);
-        if (e0 >= 0 && e0 + VEC <= V) {
-            RawVec<T, VEC> r;
-            r.load(reinterpret_cast<const T*>(base + (size_t)slot * 16));
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) f[i] = r.get(i);
+        if (e0 >= 0 && e0 + kSlot<T> <= V) {
+            r.load(reinterpret_cast<const T*>(base + (size_t)slot * kSlotBytes));
         } else {
-            const T* p = reinterpret_cast<const T*>(base) + (long long)slot * VEC;
+            const T* p = reinterpret_cast<const T*>(base) + (long long)slot * kSlot<T>;
+            r.fill_lowest();
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) f[i] = (e0 + i >= 0 && e0 + i < V) ? to_f32(p[i]) : neg_inf();
+            for (int i = 0; i < kSlot<T>; ++i)
+                if (e0 + i >= 0 && e0 + i < V) r.put(i, p[i]);
         }
     }
 };
@@ -63,164 +67,283 @@ struct Row {
 // A row's segments for select_top.
 template <typename T>
 struct Segments {
-    struct Item {
-        float f[kVecOf<T>];
-    };
+    using Item = RawVec<T, kSlot<T>>;
     const Row<T>& x;
     const float* maxima;
     __device__ __forceinline__ float max(int g) const { return __ldcg(maxima + g); }
     __device__ __forceinline__ Item load(int g) const {
         Item it;
-        x.load(g * 32 + (threadIdx.x & 31), it.f);
+        x.load(g * 32 + (threadIdx.x & 31), it);
         return it;
     }
+    __device__ __forceinline__ float peak(const Item& it) const { return it.max(); }
     template <typename F>
-    __device__ __forceinline__ void each(const Item& it, int g, F take) const {
+    __device__ __forceinline__ void each(const Item& it, int g, float b, F take) const {
         const long long e0 = x.first(g * 32 + (threadIdx.x & 31));
 #pragma unroll
-        for (int j = 0; j < kVecOf<T>; ++j)
-            take(e0 + j >= 0 && e0 + j < x.V ? make_key(it.f[j], (uint32_t)(e0 + j)) : 0ull);
+        for (int j = 0; j < kSlot<T>; ++j)
+            if (!(it.get(j) < b) && e0 + j >= 0 && e0 + j < x.V) take(make_key(it.get(j), (uint32_t)(e0 + j)));
+    }
+    static constexpr int kBatches = kSlot<T>;
+    __device__ __forceinline__ unsigned long long key(int g, int i) const {
+        const long long e = x.first(g * 32) + i * 32 + (threadIdx.x & 31);
+        if (e < 0 || e >= x.V) return 0ull;
+        return make_key(to_f32((reinterpret_cast<const T*>(x.base) + x.shift)[e]), (uint32_t)e);
     }
 };
 
 // Upper bound of the segments of a row of V elements of `size` bytes, whatever its alignment.
 __host__ __device__ inline int max_segs(int V, int size) {
-    const long long per = 512 / size;
-    return (int)(((long long)V + 16 / size - 1 + per - 1) / per);
+    const long long per = 32 * kSlotBytes / size;
+    return (int)(((long long)V + kSlotBytes / size - 1 + per - 1) / per);
 }
 
+// The call's units are the R x segs segments, cut into one range per CTA: every CTA has the same work to within a
+// segment, whatever R and V.  A range holds whole rows and, at its ends, pieces of rows that other CTAs share.
 struct Ws {
-    unsigned int* ticket;  // [kTargetCtas]: rows that are split
-    float4* part;          // [R][splits]: c, s, t
-    float* seg_max;        // [R][segs]
+    unsigned int* ticket;  // [kTargetCtas], zero between calls: by the first CTA of a shared row
+    float4* part;          // [kTargetCtas][2]: c, s, t of the CTA's first piece of a row begun before it, and of its last
+    float* seg_max;        // [R][segs], alternatives only
+    float4* row;           // [R]: c, s, t of rows that are not shared, alternatives only
 };
-struct Plan {
-    int segs, splits;
-};
-inline Plan plan(int R, int V, int size) {
-    Plan p;
-    p.segs = max_segs(V, size);
-    const int by_rows = std::max(1, (kTargetCtas + R - 1) / R);
-    p.splits = std::max(1, std::min(by_rows, p.segs / kMinSegs));
-    return p;
-}
-// Only calls of fewer than kTargetCtas rows split rows, so the tickets take a fixed place and a
-// workspace serves calls of any size up to its own.
 constexpr size_t kTicketEnd = kWsHeaderBytes + (size_t)kTargetCtas * 4;
+constexpr size_t kPartEnd = kTicketEnd + (size_t)kTargetCtas * 2 * 16;
 
+inline int ctas(long long units, int per_sm) {
+    return (int)std::max(1LL, std::min(152LL * per_sm, units / kMinSegs));
+}
+
+// A range of segments of one row.
 template <typename T>
-__global__ void __launch_bounds__(kThreadsL, 4) k_logprobs(const LogprobArgs a, const Ws ws, const Plan pl) {
-    constexpr int VEC = kVecOf<T>;
-    __shared__ float4 s_part[kWarpsL];
-    __shared__ SelectSmem s_sel;
-    __shared__ RowStat s_rs;
-    __shared__ int s_last;
-    rows_launch_dependents();
-    rows_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = blockIdx.y;
-    const Row<T> x(static_cast<const T*>(a.logits) + (long long)row * a.stride, a.V);
-    const int segs = (x.slots() + 31) / 32;
-    const int g0 = (int)((long long)segs * blockIdx.x / gridDim.x), g1 = (int)((long long)segs * (blockIdx.x + 1) / gridDim.x);
-    float* seg_max = ws.seg_max + (size_t)row * pl.segs;
+struct Piece {
+    Row<T> x;
+    int row, g0, g1;   // segments [g0, g1) of the row, of row_segs
+    int segs;          // segments that the row has
+    int in0, in1;      // those of the range that hold whole slots only
+    const T* p;        // this thread's slot of segment in0 + warp
+    __device__ __forceinline__ Piece(const LogprobArgs& a, int row_, int g0_, int g1_)
+        : x(static_cast<const T*>(a.logits) + (long long)row_ * a.stride, a.V), row(row_), g0(g0_), g1(g1_) {
+        segs = (x.slots() + 31) / 32;
+        in0 = max(g0, x.shift != 0 ? 1 : 0);
+        in1 = min(g1, (int)(((long long)x.V + x.shift) / (32 * kSlot<T>)));
+        p = reinterpret_cast<const T*>(x.base + ((size_t)in0 * 32 + threadIdx.x) * kSlotBytes);
+    }
+    __device__ __forceinline__ int first() const { return in0 + (threadIdx.x >> 5); }  // this warp's first whole segment
+};
 
-    // Segments [in0, in1) hold whole slots only.
-    const int in0 = x.shift != 0 ? 1 : 0;
-    const int in1 = (int)(((long long)a.V + x.shift) / (32 * VEC));
+// kUnroll segments of a piece per warp, from segment g on; places past the piece read as -inf.
+template <typename T>
+struct Block {
+    RawVec<T, kSlot<T>> r[kUnroll];
+    __device__ __forceinline__ void request(const Piece<T>& pc, int g) {
+        if (g >= pc.in1) return;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (g + u * kWarpsL < pc.in1)
+                r[u].load(pc.p + (size_t)(g - pc.first() + u * kWarpsL) * (32 * kSlot<T>));
+            else
+                r[u].fill_lowest();
+        }
+    }
+};
+
+// Statistics of a piece by one thread, and the maxima of its segments.  `next` holds the piece's first block;
+// request_after() puts the first block of the next piece there: loads are in flight while a block, or a row, is
+// summed up.
+template <typename T, bool TOP, typename F>
+__device__ __forceinline__ Stat scan(const Piece<T>& pc, Block<T>& next, float* seg_max, F request_after) {
+    constexpr int VEC = kSlot<T>;
+    constexpr bool kHalf = std::is_same<T, __half>::value;
+    constexpr float lift = kHalf ? kLiftHalf : kLift, lift_from = kHalf ? kLiftFromHalf : kLiftFrom;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Stat2 run;
     run.clear();
-    auto add = [&](const RawVec<T, VEC>& r) {
-        const F2 mc = f2(-run.c, -run.c);
-#pragma unroll
-        for (int i = 0; i < VEC; i += 2) run.add(r.get(i), r.get(i + 1), mc);
-    };
     auto keep_max = [&](int g, float m) {
-        if (a.top_n > 0) {
+        if (TOP) {
             float w;
             asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(w) : "f"(m));
             if (lane == 0) seg_max[g] = w;
         }
     };
-    for (int g = g0 + warp; g < g1; g += kWarpsL * kUnroll) {
-        const int last = g + (kUnroll - 1) * kWarpsL;
-        if (g >= in0 && last < min(g1, in1)) {
-            RawVec<T, VEC> r[kUnroll];
+    // The row's ends, element by element: the first segment by warp 0, the last by warp 1.
+    const int g1 = min(pc.g1, pc.segs);
+    const int end = warp == 0 ? (pc.g0 < pc.in0 ? pc.g0 : -1) : warp == 1 ? (g1 > pc.in1 && g1 > pc.in0 ? g1 - 1 : -1) : -1;
+    if (end >= 0) {
+        RawVec<T, VEC> f;
+        pc.x.load(end * 32 + lane, f);
+        const float m = f.max();
+        keep_max(end, m);
+        run.raise(m);
+        if (run.c != neg_inf()) {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                r[u].load(reinterpret_cast<const T*>(x.base + ((size_t)(g + u * kWarpsL) * 32 + lane) * 16));
-            float m = neg_inf();
+            for (int i = 0; i < VEC; i += 2) run.add(f.get(i), f.get(i + 1));
+        }
+    }
+    int g = pc.first();
+    if (g >= pc.in1) request_after();
+    for (; g < pc.in1; g += kWarpsL * kUnroll) {
+        Block<T> b = next;
+        if (g + kWarpsL * kUnroll < pc.in1)
+            next.request(pc, g + kWarpsL * kUnroll);
+        else
+            request_after();
+        float m = neg_inf();
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const float mu = b.r[u].max();
+            m = fmaxf(m, mu);
+            if (g + u * kWarpsL < pc.in1) keep_max(g + u * kWarpsL, mu);
+        }
+        run.raise(m);
+        if (run.c > lift_from && run.c < kNearLimit) {
+            const F2 mcl = run.minus_cl();
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const float mu = r[u].max();
-                m = fmaxf(m, mu);
-                keep_max(g + u * kWarpsL, mu);
-            }
-            run.raise(m);
-            if (run.c != neg_inf()) {
+                b.r[u].lift(lift);
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) add(r[u]);
+                for (int i = 0; i < VEC; i += 2) run.add_plain(b.r[u].get(i), b.r[u].get(i + 1), mcl);
             }
-        } else {  // a row's ends
-            for (int gg = g; gg < g1 && gg <= last; gg += kWarpsL) {
-                float f[VEC];
-                x.load(gg * 32 + lane, f);
-                float m = neg_inf();
+        } else if (run.c != neg_inf()) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) m = fmaxf(m, f[i]);
-                keep_max(gg, m);
-                run.raise(m);
-                if (run.c != neg_inf()) {
-                    const F2 mc = f2(-run.c, -run.c);
-#pragma unroll
-                    for (int i = 0; i < VEC; i += 2) run.add(f[i], f[i + 1], mc);
-                }
-            }
+            for (int u = 0; u < kUnroll; ++u)
+                for (int i = 0; i < VEC; i += 2) run.add(b.r[u].get(i), b.r[u].get(i + 1));
         }
     }
-    Stat st = run.get();
-    st = stat_warp(st);
-    if (lane == 0) s_part[warp] = make_float4(st.c, st.s, st.t, 0.f);
-    __syncthreads();
-    if (warp == 0) {
-        st = stat_none();
-        if (lane < kWarpsL) st = Stat{s_part[lane].x, s_part[lane].y, s_part[lane].z};
-        st = stat_warp(st);
+    return run.get();
+}
+
+// a / b for a, b >= 0; the 64-bit division takes several times as long.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// How the units are cut into ranges of n CTAs: `per` units each, the first `more` CTAs one more.
+struct Split {
+    long long per, more;
+    __device__ __forceinline__ Split(long long units, int n) {
+        per = quotient(units, n);
+        more = units - per * n;
     }
-    if (gridDim.x > 1) {
-        if (threadIdx.x == 0) ws.part[(size_t)row * pl.splits + blockIdx.x] = make_float4(st.c, st.s, st.t, 0.f);
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0) s_last = atomicAdd(ws.ticket + row, 1u) == gridDim.x - 1;
-        __syncthreads();
-        if (!s_last) return;
-        __threadfence();
-        if (threadIdx.x == 0) atomicExch(ws.ticket + row, 0u);
-        if (warp == 0) {
-            st = stat_none();
-            for (int i = lane; i < (int)gridDim.x; i += 32) {
-                const float4 p = __ldcg(ws.part + (size_t)row * pl.splits + i);
-                st = stat_join(st, Stat{p.x, p.y, p.z});
-            }
-            st = stat_warp(st);
+    __device__ __forceinline__ long long begin(int c) const { return c * per + min((long long)c, more); }
+    __device__ __forceinline__ int cta_of(long long u) const {  // whose range holds unit u
+        const long long big = more * (per + 1);
+        return (int)(u < big ? quotient(u, per + 1) : more + quotient(u - big, per));
+    }
+};
+
+__device__ __forceinline__ float4 pack(const Stat& st) { return make_float4(st.c, st.s, st.t, 0.f); }
+__device__ __forceinline__ Stat unpack(float4 v) { return Stat{v.x, v.y, v.z}; }
+
+// The pieces of a row that CTAs first .. last share, by one warp.
+__device__ __forceinline__ Stat join_pieces(const Ws& ws, int first, int last) {
+    Stat st = stat_none();
+    for (int c = first + (threadIdx.x & 31); c <= last; c += 32)
+        st = stat_join(st, unpack(__ldcg(ws.part + c * 2 + (c == first))));
+    return stat_warp(st);
+}
+
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int row, const RowStat& rs, bool given, float tok_score) {
+    if (a.logprob != nullptr) a.logprob[row] = given ? stat_logprob(rs, tok_score) : 0.f;
+    if (a.entropy != nullptr) a.entropy[row] = rs.entropy;
+    if (a.lse != nullptr) a.lse[row] = rs.lse;
+}
+
+// Everything after a row's scan is warp 0's; the other warps go on with the next row.  With alternatives (TOP) the
+// second kernel joins the pieces and writes the results; without, the last CTA of a row does.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprobs(const LogprobArgs a, const Ws ws, const int row_segs) {
+    __shared__ float4 s_part[2][kWarpsL];
+    rows_launch_dependents();
+    rows_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Split split((long long)a.R * row_segs, gridDim.x);
+    const long long u0 = split.begin(blockIdx.x), u1 = split.begin(blockIdx.x + 1);
+    const int row0 = (int)quotient(u0, row_segs), first_g = (int)(u0 - (long long)row0 * row_segs);
+    long long left = u1 - u0;  // units from the current piece on
+    int row = row0, g0 = first_g;
+    Block<T> next;
+    {
+        const Piece<T> pc(a, row, g0, (int)min((long long)row_segs, g0 + left));
+        next.request(pc, pc.first());
+    }
+    for (int buf = 0; left > 0; buf ^= 1, ++row, g0 = 0) {
+        const int g1 = (int)min((long long)row_segs, g0 + left);
+        left -= g1 - g0;
+        const T* p = static_cast<const T*>(a.logits) + (long long)row * a.stride;
+        float* seg_max = TOP ? ws.seg_max + (size_t)row * row_segs : nullptr;
+        float tok_score = 0.f;  // requested before the scan, used after it
+        bool given = false;
+        if (!TOP && threadIdx.x == 0 && a.logprob != nullptr) {
+            const int tok = a.tokens[row];
+            given = tok >= 0 && tok < a.V;
+            if (given) tok_score = to_f32(p[tok]);
         }
-    }
-    RowStat rs{};
-    if (warp == 0) {
-        rs = stat_finish(st);
+        Stat st = stat_warp(scan<T, TOP>(Piece<T>(a, row, g0, g1), next, seg_max, [&] {
+            if (left > 0) {
+                const Piece<T> after(a, row + 1, 0, (int)min((long long)row_segs, left));
+                next.request(after, after.first());
+            }
+        }));
+        if (lane == 0) s_part[buf][warp] = pack(st);
+        __syncthreads();
+        if (warp != 0) continue;
+        st = stat_warp(lane < kWarpsL ? unpack(s_part[buf][lane]) : stat_none());
+        if (g1 - g0 < row_segs) {
+            const int first = split.cta_of((long long)row * row_segs);
+            float4* part = ws.part + blockIdx.x * 2 + ((int)blockIdx.x == first);
+            if (TOP) {
+                if (lane == 0) *part = pack(st);
+                continue;
+            }
+            // the last of the row's CTAs to get here joins the pieces
+            const int last = split.cta_of((long long)(row + 1) * row_segs - 1);
+            int done = 0;
+            if (lane == 0) {
+                __stcg(part, pack(st));
+                __threadfence();
+                done = atomicAdd(ws.ticket + first, 1u) == (unsigned)(last - first);
+                if (done) atomicExch(ws.ticket + first, 0u);
+                __threadfence();
+            }
+            if (__shfl_sync(0xFFFFFFFFu, done, 0) == 0) continue;
+            st = join_pieces(ws, first, last);
+        }
         if (lane == 0) {
-            if (a.logprob != nullptr) {
-                const int tok = a.tokens != nullptr ? a.tokens[row] : -1;
-                const T* p = static_cast<const T*>(a.logits) + (long long)row * a.stride;
-                a.logprob[row] = (tok >= 0 && tok < a.V) ? stat_logprob(rs, to_f32(p[tok])) : 0.f;
-            }
-            if (a.entropy != nullptr) a.entropy[row] = rs.entropy;
-            if (a.lse != nullptr) a.lse[row] = rs.lse;
+            if (TOP)
+                ws.row[row] = pack(st);
+            else
+                write_row(a, row, stat_finish(st), given, tok_score);
         }
     }
-    if (a.top_n == 0) return;
-    if (threadIdx.x == 0) s_rs = rs;  // select_top has barriers before it emits
-    select_top(
-        s_sel, segs, a.top_n, 0u, Segments<T>{x, seg_max}, [] {},
+}
+
+// One row per CTA: its statistics and its alternatives, after k_logprobs<T, true> of n_scan CTAs.
+template <typename T>
+__global__ void __launch_bounds__(kSelThreads, 4) k_logprobs_top(const LogprobArgs a, const Ws ws, const int row_segs,
+                                                                 const int n_scan) {
+    constexpr int kHeld = 4;
+    __shared__ SelectSmem s_sel;
+    __shared__ RowStat s_rs;
+    rows_launch_dependents();
+    rows_wait();
+    const int row = blockIdx.x;
+    const T* p = static_cast<const T*>(a.logits) + (long long)row * a.stride;
+    const Row<T> x(p, a.V);
+    auto finish = [&] {
+        if (threadIdx.x >= 32) return;
+        const Split split((long long)a.R * row_segs, n_scan);
+        const int tok = a.logprob != nullptr ? a.tokens[row] : -1;
+        const bool given = tok >= 0 && tok < a.V;
+        const float tok_score = given ? to_f32(p[tok]) : 0.f;
+        const int first = split.cta_of((long long)row * row_segs), last = split.cta_of((long long)(row + 1) * row_segs - 1);
+        const RowStat rs = stat_finish(first == last ? unpack(ws.row[row]) : join_pieces(ws, first, last));
+        if (threadIdx.x == 0) {
+            s_rs = rs;
+            write_row(a, row, rs, given, tok_score);
+        }
+    };
+    select_top<kHeld>(
+        s_sel, (x.slots() + 31) / 32, a.top_n, 0u, Segments<T>{x, ws.seg_max + (size_t)row * row_segs}, finish,
         [&](int i, unsigned long long k) {
             const size_t o = (size_t)row * a.top_n + i;
             a.top_ids[o] = k != 0ull ? (int32_t)key_gid(k) : -1;
@@ -299,31 +422,18 @@ static cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, cudaStrea
 
 template <typename T>
 static cudaError_t forward(const LogprobArgs& a, cudaStream_t s) {
-    const Plan pl = plan(a.R, a.V, (int)sizeof(T));
+    const int segs = max_segs(a.V, (int)sizeof(T));
     Ws ws;
     uint8_t* p = static_cast<uint8_t*>(a.ws);
     ws.ticket = reinterpret_cast<unsigned int*>(p + kWsHeaderBytes);
     ws.part = reinterpret_cast<float4*>(p + kTicketEnd);
-    ws.seg_max = reinterpret_cast<float*>(ws.part + (size_t)a.R * pl.splits);
-    for (int r0 = 0; r0 < a.R; r0 += 65535) {  // the grid's second dimension holds 65,535 rows
-        LogprobArgs b = a;
-        Ws w = ws;
-        const int nr = std::min(65535, a.R - r0);
-        b.logits = static_cast<const T*>(a.logits) + (long long)r0 * a.stride;
-        b.tokens = a.tokens ? a.tokens + r0 : nullptr;
-        b.logprob = a.logprob ? a.logprob + r0 : nullptr;
-        b.entropy = a.entropy ? a.entropy + r0 : nullptr;
-        b.lse = a.lse ? a.lse + r0 : nullptr;
-        if (a.top_n > 0) {
-            b.top_ids += (size_t)r0 * a.top_n;
-            b.top_logprobs += (size_t)r0 * a.top_n;
-        }
-        w.part += (size_t)r0 * pl.splits;
-        w.seg_max += (size_t)r0 * pl.segs;
-        cudaError_t e = launch(k_logprobs<T>, dim3((unsigned)pl.splits, (unsigned)nr), dim3(kThreadsL), s, b, w, pl);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    ws.row = reinterpret_cast<float4*>(p + kPartEnd);
+    ws.seg_max = reinterpret_cast<float*>(p + kPartEnd + (size_t)a.R * 16);
+    const dim3 grid((unsigned)ctas((long long)a.R * segs, a.top_n > 0 ? kPerSmTop : kPerSm));
+    if (a.top_n == 0) return launch(k_logprobs<T, false>, grid, dim3(kThreadsL), s, a, ws, segs);
+    const cudaError_t e = launch(k_logprobs<T, true>, grid, dim3(kThreadsL), s, a, ws, segs);
+    if (e != cudaSuccess) return e;
+    return launch(k_logprobs_top<T>, dim3((unsigned)a.R), dim3(kSelThreads), s, a, ws, segs, (int)grid.x);
 }
 
 template <typename T, int VEC>
@@ -358,10 +468,8 @@ static cudaError_t grad(const LogprobGradArgs& a, cudaStream_t s) {
 }  // namespace lp
 
 size_t logits_logprobs_ws_bytes(int R, int V, int top_n) {
-    const lp::Plan p = lp::plan(R, V, 4);  // 32-bit logits have the most segments
-    const lp::Plan q = lp::plan(R, V, 2);
-    const size_t part = (size_t)R * std::max(p.splits, q.splits) * 16;
-    return lp::kTicketEnd + part + (top_n > 0 ? round16((size_t)R * p.segs * 4) : 0);
+    // 32-bit logits have the most segments
+    return lp::kPartEnd + (top_n > 0 ? (size_t)R * 16 + round16((size_t)R * lp::max_segs(V, 4) * 4) : 0);
 }
 
 cudaError_t launch_logits_logprobs(const LogprobArgs& a, int dtype, cudaStream_t s) {

@@ -128,7 +128,7 @@ struct NormArgs {
     int T, H;
     int w32;        // w is fp32 (else the rows' type)
     int out;        // vh_norm_out
-    float eps, w_offset;
+    float eps, w_offset, inv_h;
 };
 cudaError_t launch_add_rmsnorm(const NormArgs& a, int dtype, cudaStream_t s);
 
@@ -141,7 +141,7 @@ struct NormGradArgs {
     long long dy_stride, h_stride, dh_stride, dx_stride;
     int T, H;
     int w32;
-    float eps, w_offset;
+    float eps, w_offset, inv_h;
 };
 constexpr int kNormGradParts = 608;  // CTAs that share the tokens: four per SM
 int norm_grad_parts(int T);

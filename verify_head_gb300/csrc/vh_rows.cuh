@@ -47,11 +47,9 @@ struct RawVec<T, 1> {
 };
 template <typename T, int VEC>
 struct RawVec {
-    static_assert(VEC * sizeof(T) == 16, "one 16-byte vector");
-    union {
-        uint4 q;
-        uint32_t u[4];
-    };
+    static constexpr int N = VEC * (int)sizeof(T) / 4;  // 32-bit words
+    static_assert(N == 4 || N == 8, "one vector of 16 or 32 bytes");
+    uint32_t u[N];
     __device__ __forceinline__ float get(int i) const {
         if constexpr (sizeof(T) == 4) {
             return __uint_as_float(u[i]);
@@ -71,20 +69,67 @@ struct RawVec {
             u[i] = *reinterpret_cast<const uint32_t*>(&b);
         }
     }
-    __device__ __forceinline__ void load(const T* p) { q = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (N == 4) {
+            const uint4 q = *reinterpret_cast<const uint4*>(p);
+            u[0] = q.x;
+            u[1] = q.y;
+            u[2] = q.z;
+            u[3] = q.w;
+        } else {
+            const U32x8 q = ld_stream32(p);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = q.v[i];
+        }
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        static_assert(N == 4, "stores are of 16 bytes");
+        *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    __device__ __forceinline__ void put(int i, T v) {  // element i as it is
+        if constexpr (sizeof(T) == 4) {
+            u[i] = __float_as_uint(v);
+        } else {
+            const uint32_t h = *reinterpret_cast<const uint16_t*>(&v);
+            u[i >> 1] = (i & 1) ? (u[i >> 1] & 0xFFFFu) | (h << 16) : (u[i >> 1] & 0xFFFF0000u) | h;
+        }
+    }
+    __device__ __forceinline__ void fill_lowest() {  // -inf
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            u[i] = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __nv_bfloat16>::value ? 0xFF80FF80u : 0xFC00FC00u;
+    }
+    // Elements below `lo` and NaN become `lo`: two per instruction for the 16-bit types.
+    __device__ __forceinline__ void lift(float lo) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) u[i] = __float_as_uint(fmaxf(__uint_as_float(u[i]), lo));
+        } else {
+            using P = typename std::conditional<std::is_same<T, __nv_bfloat16>::value, __nv_bfloat162, __half2>::type;
+            P b;
+            b.x = b.y = from_f32<T>(lo);
+            P* p = reinterpret_cast<P*>(u);
+#pragma unroll
+            for (int i = 0; i < N; ++i) p[i] = __hmax2(p[i], b);
+        }
+    }
     // The largest element, NaN left out (-inf if there is nothing else).
     __device__ __forceinline__ float max() const {
+        const float lowest = -__int_as_float(0x7f800000);
         if constexpr (sizeof(T) == 4) {
-            const float m = fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3)));
-            return fmaxf(m, -__int_as_float(0x7f800000));
+            float m = lowest;
+#pragma unroll
+            for (int i = 0; i < N; ++i) m = fmaxf(m, get(i));
+            return m;
         } else {
             using P = typename std::conditional<std::is_same<T, __nv_bfloat16>::value, __nv_bfloat162, __half2>::type;
             const P* p = reinterpret_cast<const P*>(u);
-            const P m = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
-            return fmaxf(fmaxf(to_f32(m.x), to_f32(m.y)), -__int_as_float(0x7f800000));
+            P m = p[0];
+#pragma unroll
+            for (int i = 1; i < N; ++i) m = __hmax2(m, p[i]);
+            return fmaxf(fmaxf(to_f32(m.x), to_f32(m.y)), lowest);
         }
     }
-    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = q; }
 };
 
 template <typename T, int VEC>
@@ -101,17 +146,24 @@ __device__ __forceinline__ void pack_vec(RawVec<T, VEC>& r, const float (&f)[VEC
 }
 
 // ---------------------------------------------------------------------------
-// Softmax statistics relative to a running maximum c: s = sum e^(x - c),
-// t = sum e^(x - c) y with y = log2(e) (x - c) <= 0.  Then lse = c + ln s,
-// log p = (x - c) - ln s and entropy = ln2 (log2 s - t / s): the entropy's
-// terms are small where the row is peaked, so nothing cancels.  c = -inf:
-// nothing summed yet (s = t = 0).  A +inf score leaves c = +inf and the row's
-// statistics are NaN.  x - c is taken before the factor log2(e): the type's
-// lowest value times that factor would be -inf, and a row that holds nothing
-// else would be lost.
+// Softmax statistics relative to a running maximum c: s = sum 2^y, t = sum
+// 2^y y with y = log2(e) (x - c) <= 0.  Then lse = c + ln s, log p = (x - c)
+// - ln s and entropy = ln2 (log2 s - t / s): the entropy's terms are small
+// where the row is peaked, so nothing cancels.  c = -inf: nothing summed yet
+// (s = t = 0).  A +inf score leaves c = +inf and the row's statistics are NaN.
+//
+// y is taken as fma(x, log2e, -round(c log2e)); every use of c rounds that
+// product the same way, and what the rounding took is given back at the end.
+// Where |c| is near the type's limits the product would be infinite (a row
+// that holds the lowest value and nothing else) and y is (x - c) log2e.
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNearLimit = 1e38f;
+// Scores below kLift carry no probability beside a maximum above kLiftFrom and may be lifted to it.  A type whose
+// lowest value is above kLift is lifted to that value, beside a maximum that is well above it.
+constexpr float kLift = -1e30f, kLiftFrom = -1e29f;
+constexpr float kLiftHalf = -65504.f, kLiftFromHalf = -60000.f;
 // y below this is lifted to it: 2^y is 0 in either case and y * 2^y must not
 // become -inf * 0 at masked places (NaN scores land here too: they count as -inf).
 constexpr float kFloorY = -2000.0f;
@@ -132,10 +184,19 @@ struct Stat {
 
 __device__ __forceinline__ Stat stat_none() { return Stat{neg_inf(), 0.f, 0.f}; }
 
-// Move statistics to a larger shift.
+// y of a score or of an older maximum.
+__device__ __forceinline__ float stat_y(float x, float c) {
+    const float y = fabsf(c) < kNearLimit ? fmaf(x, kLog2e, -(c * kLog2e)) : (x - c) * kLog2e;
+    return fmaxf(y, kFloorY);
+}
+
+// Move statistics to a larger maximum.
 __device__ __forceinline__ void stat_shift(Stat& a, float c) {
     if (a.s != 0.f) {
-        const float d = fmaxf((a.c - c) * kLog2e, kFloorY);
+        // both maxima's products rounded alike (no fma)
+        const float d = fabsf(a.c) < kNearLimit && fabsf(c) < kNearLimit
+                            ? fmaxf(__fmul_rn(a.c, kLog2e) - __fmul_rn(c, kLog2e), kFloorY)
+                            : fmaxf((a.c - c) * kLog2e, kFloorY);
         const float f = ex2(d);
         a.t = f * fmaf(d, a.s, a.t);
         a.s *= f;
@@ -201,36 +262,48 @@ struct Stat2 {
             t = f2(a.t, 0.f);
         }
     }
-    // Two scores; c is their maximum or more, not -inf.  minus_c = (-c, -c).
-    __device__ __forceinline__ void add(float x0, float x1, F2 minus_c) {
-        const float2 y = f2_get(f2_mul(f2_add(f2(x0, x1), minus_c), f2(kLog2e, kLog2e)));
-        const float y0 = fmaxf(y.x, kFloorY), y1 = fmaxf(y.y, kFloorY);
-        const F2 e = f2(ex2(y0), ex2(y1));
+    // Two scores; c is their maximum or more, not -inf.
+    __device__ __forceinline__ void add(float x0, float x1) { add_y(stat_y(x0, c), stat_y(x1, c)); }
+    // Two scores of which none is -inf or NaN, where |c| < kNearLimit: minus_cl = -c log2e twice.
+    __device__ __forceinline__ void add_plain(float x0, float x1, F2 minus_cl) {
+        const F2 y = f2_fma(f2(x0, x1), f2(kLog2e, kLog2e), minus_cl);
+        const float2 v = f2_get(y);
+        const F2 e = f2(ex2(v.x), ex2(v.y));
         s = f2_add(s, e);
-        t = f2_fma(e, f2(y0, y1), t);
+        t = f2_fma(e, y, t);
+    }
+    __device__ __forceinline__ F2 minus_cl() const { return f2(-(c * kLog2e), -(c * kLog2e)); }
+
+private:
+    __device__ __forceinline__ void add_y(float y0, float y1) {
+        const F2 y = f2(y0, y1), e = f2(ex2(y0), ex2(y1));
+        s = f2_add(s, e);
+        t = f2_fma(e, y, t);
     }
 };
 
 __device__ __forceinline__ Stat stat_warp(Stat a) {
+    float c;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(c) : "f"(a.c));
+    stat_shift(a, c);
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) {
-        Stat b;
-        b.c = __shfl_xor_sync(0xFFFFFFFFu, a.c, m);
-        b.s = __shfl_xor_sync(0xFFFFFFFFu, a.s, m);
-        b.t = __shfl_xor_sync(0xFFFFFFFFu, a.t, m);
-        a = stat_join(a, b);
+        a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, m);
+        a.t += __shfl_xor_sync(0xFFFFFFFFu, a.t, m);
     }
     return a;
 }
 
 // A finished row.
 struct RowStat {
-    float c, log2_s, lse, entropy;
+    float c, log2_s, lse, entropy;  // log2_s: of the sum relative to c log2e itself, not to its rounding
 };
 __device__ __forceinline__ RowStat stat_finish(const Stat& a) {
     RowStat r;
     r.c = a.c;
-    r.log2_s = log2f(a.s);
+    const float l = log2f(a.s);
+    const float rest = fabsf(a.c) < kNearLimit ? fmaf(a.c, kLog2e, -(a.c * kLog2e)) : 0.f;
+    r.log2_s = l - rest;
     if (a.c == neg_inf()) {  // nothing but -inf (or NaN)
         r.lse = neg_inf();
         r.entropy = 0.f;
@@ -238,7 +311,7 @@ __device__ __forceinline__ RowStat stat_finish(const Stat& a) {
         r.lse = r.entropy = quiet_nan();
     } else {
         r.lse = fmaf(r.log2_s, kLn2, a.c);
-        r.entropy = fmaxf((r.log2_s - a.t / a.s) * kLn2, 0.f);
+        r.entropy = fmaxf((l - a.t / a.s) * kLn2, 0.f);
     }
     return r;
 }
@@ -273,9 +346,9 @@ __device__ __forceinline__ unsigned long long top_clean(unsigned long long k) {
 // Any 32 keys -> descending (bitonic sort).
 __device__ __forceinline__ unsigned long long top_sort(unsigned long long k) {
     const int lane = threadIdx.x & 31;
-#pragma unroll
+#pragma unroll 1
     for (int size = 2; size <= 32; size <<= 1) {
-#pragma unroll
+#pragma unroll 1
         for (int m = size >> 1; m >= 1; m >>= 1) {
             const unsigned long long o = shfl_key(k, m);
             const bool keep_max = ((lane & m) == 0) == ((lane & size) == 0);
@@ -329,34 +402,40 @@ struct SelectSmem {
 
 // Segs: float max(int g), the maximum of segment g < segs (NaN left out);
 //   Item load(int g), this lane's elements of segment g (the warp loads it together);
-//   void each(const Item&, int g, f): f(key) with the argmax key of each of them, 0 for a place outside the row.
+//   float peak(const Item&), the largest of them (NaN left out);
+//   void each(const Item&, int g, float b, f): f(key) with the argmax key of those that are not below b;
+//   kBatches, key(int g, int i): the lane's key in batch i < kBatches of the segment's elements, 0 outside the row.
 // meanwhile(): called once, after the maxima are requested and before they are used.
 // emit(i, key): key of the i-th largest element, i < n (0 = the row has fewer).
 // floor: ord_f32 of a value that n elements are known to reach, 0 = none.
 // All threads call it; sm.n_seg, sm.n_elem and sm.bound need not be set.
-template <typename Segs, typename Meanwhile, typename Emit>
+// HELD: maxima a thread holds in registers; up to HELD * kSelThreads segments are read once, more are read twice.
+template <int HELD, typename Segs, typename Meanwhile, typename Emit>
 __device__ __forceinline__ void select_top(SelectSmem& sm, int segs, int n, uint32_t floor, const Segs& sg,
                                            Meanwhile meanwhile, Emit emit) {
-    constexpr int kHeld = 32;    // maxima a thread holds in registers
-    constexpr int kAtOnce = 4;   // segments a warp loads at once
+    constexpr int kHeld = HELD;
+    constexpr int kAtOnce = 3;   // segments a warp loads at once
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float held[kHeld];
     auto hold = [&](int base) {
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
             const int g = base + i * kSelThreads + tid;
-            held[i] = g < segs ? sg.max(g) : neg_inf();
+            if (base + i * kSelThreads < segs) held[i] = g < segs ? sg.max(g) : neg_inf();
         }
+    };
+    auto held_max = [&](int base, float m) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (base + i * kSelThreads < segs) m = fmaxf(m, held[i]);
+        return m;
     };
     hold(0);
     meanwhile();
-    float m = held[0];
-#pragma unroll
-    for (int i = 1; i < kHeld; ++i) m = fmaxf(m, held[i]);
+    float m = held_max(0, neg_inf());
     for (int base = kHeld * kSelThreads; base < segs; base += kHeld * kSelThreads) {
         hold(base);
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) m = fmaxf(m, held[i]);
+        m = held_max(base, m);
     }
     const uint32_t mine = tid < segs ? ord_f32(m) : 0u;
     uint32_t grp = max(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1));
@@ -377,13 +456,14 @@ __device__ __forceinline__ void select_top(SelectSmem& sm, int segs, int n, uint
     }
     __syncthreads();
     const uint32_t bound = sm.bound;
+    const float least = unord_f32(bound);  // may be NaN, which nothing is below
     if (mine >= bound && mine != 0u) {
         for (int base = 0; base < segs; base += kHeld * kSelThreads) {
             if (segs > kHeld * kSelThreads) hold(base);
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
                 const int g = base + i * kSelThreads + tid;
-                if (g < segs && ord_f32(held[i]) >= bound) {
+                if (base + i * kSelThreads < segs && g < segs && ord_f32(held[i]) >= bound) {
                     const int e = atomicAdd(&sm.n_seg, 1);
                     if (e < kSelSegs) sm.seg[e] = (uint32_t)g;
                 }
@@ -403,9 +483,9 @@ __device__ __forceinline__ void select_top(SelectSmem& sm, int segs, int n, uint
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
                 const int i = i0 + u * kSelWarps;
-                if (i < n_seg)
-                    sg.each(it[u], (int)sm.seg[i], [&](unsigned long long k) {
-                        if ((uint32_t)(k >> 32) >= bound && k != 0ull) {
+                if (i < n_seg && ord_f32(sg.peak(it[u])) >= bound)
+                    sg.each(it[u], (int)sm.seg[i], least, [&](unsigned long long k) {
+                        if ((uint32_t)(k >> 32) >= bound) {
                             const int e = atomicAdd(&sm.n_elem, 1);
                             if (e < kSelElems) sm.elem[e] = k;
                         }
@@ -418,6 +498,7 @@ __device__ __forceinline__ void select_top(SelectSmem& sm, int segs, int n, uint
             if (tid < m2) {
                 const unsigned long long k = sm.elem[tid];
                 int above = 0;
+#pragma unroll 8
                 for (int j = 0; j < m2; ++j) above += sm.elem[j] > k;
                 if (above < n) emit(above, k);
             } else if (tid < n) {
@@ -435,19 +516,20 @@ __device__ __forceinline__ void select_top(SelectSmem& sm, int segs, int n, uint
     sm.sorted[warp][lane] = top;
     __syncthreads();
     unsigned long long best = sm.sorted[0][lane];
-#pragma unroll
+#pragma unroll 1
     for (int w = 1; w < kSelWarps; ++w) top_merge(best, sm.sorted[w][lane]);
     __syncthreads();
     top = 0ull;
     for (int i = warp; i < n; i += kSelWarps) {
         const unsigned long long kseg = __shfl_sync(0xFFFFFFFFu, best, i);
         if (kseg == 0ull) break;
-        sg.each(sg.load((int)key_gid(kseg)), (int)key_gid(kseg), [&](unsigned long long k) { top_insert(top, k, n); });
+#pragma unroll 1
+        for (int j = 0; j < Segs::kBatches; ++j) top_insert(top, sg.key((int)key_gid(kseg), j), n);
     }
     sm.sorted[warp][lane] = top;
     __syncthreads();
     if (warp != 0) return;
-#pragma unroll
+#pragma unroll 1
     for (int w = 1; w < kSelWarps; ++w) top_merge(top, sm.sorted[w][lane]);
     if (lane < n) emit(lane, top);
 }
