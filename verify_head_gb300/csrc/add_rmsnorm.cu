@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "vh_kernels.h"
+#include "vh_ptx.cuh"
 #include "vh_rows.cuh"
 
 namespace vh {
@@ -26,6 +27,8 @@ namespace norm {
 
 constexpr int kMaxThreads = 512;  // register-resident rows: up to 128 registers a thread
 constexpr int kWideThreads = 512;
+constexpr int kMaxRing = 4;                // tokens in flight per CTA of the gradient
+constexpr size_t kRingBytes = 56 * 1024;   // of shared memory per CTA that its ring stays below (four CTAs per SM)
 
 // Sums of two values over the threads of one row (threadIdx.y) of the CTA.
 // MAX_SECOND: the second value is a maximum instead of a sum.  All threads of
@@ -274,80 +277,94 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(const NormArgs a) {
 // share of dw in registers and leaves it in part[c][H]; a second kernel adds
 // the shares in CTA order, so the sums do not change from call to call.
 
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(kMaxThreads) k_norm_grad(const NormGradArgs a) {
+// Whole 16-byte vectors: the rows come by bulk copies into a ring of `depth` tokens in shared memory, so that loads
+// are in flight whatever the registers hold (8192 x 2048 bf16: 28.7 against 30.2 us with the next token's vectors in
+// registers, where 64 registers a thread left no room for a second token).  Token i is summed, reduced (one barrier)
+// and written; behind that barrier every thread is done with token i - 1, whose place is refilled.
+// A wait is for copies that the CTA itself has issued; should it expire (it is bounded) the token's results are NaN.
+template <typename T, int NV>
+__global__ void __launch_bounds__(kMaxThreads) k_norm_grad_ring(const NormGradArgs a, const int depth) {
+    constexpr int VEC = kVecOf<T>;
+    extern __shared__ __align__(128) uint8_t ring[];  // [depth][h, dy, dh][H]
     __shared__ float2 red[2][32];
+    __shared__ unsigned long long full[kMaxRing];
+    const int nvec = a.H / VEC;
+    const uint32_t row_bytes = (uint32_t)(a.H * sizeof(T));
+    const int streams = a.dh != nullptr ? 3 : 2;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < depth; ++i) ptx::mbar_init(&full[i], 1);
+        ptx::fence_barrier_init();
+    }
+    __syncthreads();
     rows_launch_dependents();
     rows_wait();
-    const int nvec = a.H / VEC;
-    float dw[NV][VEC];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) dw[j][k] = 0.f;
-    int slot = 0;
-    // a token's loads are issued while the one before it is reduced and written
-    RawVec<T, VEC> hv[NV], yv[NV], ev[NV], hn[NV], yn[NV], en[NV];
-    auto load = [&](long long row) {
-        const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
-        const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
-        const T* dh = static_cast<const T*>(a.dh) + row * a.dh_stride;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
-            if (v < nvec) {
-                hn[j].load(h + (size_t)v * VEC);
-                yn[j].load(dy + (size_t)v * VEC);
-                if (a.dh != nullptr) en[j].load(dh + (size_t)v * VEC);
-            }
-        }
+    const long long step = gridDim.x;
+    const int n = (int)((a.T - blockIdx.x + step - 1) / step);  // tokens of this CTA
+    auto fill = [&](int i) {                                    // by thread 0
+        const long long row = blockIdx.x + i * step;
+        const int s = i % depth;
+        uint8_t* to = ring + (size_t)s * 3 * row_bytes;
+        ptx::mbar_arrive_expect_tx(&full[s], streams * row_bytes);
+        ptx::bulk_copy(to, static_cast<const T*>(a.h) + row * a.h_stride, row_bytes, &full[s]);
+        ptx::bulk_copy(to + row_bytes, static_cast<const T*>(a.dy) + row * a.dy_stride, row_bytes, &full[s]);
+        if (a.dh != nullptr)
+            ptx::bulk_copy(to + 2 * row_bytes, static_cast<const T*>(a.dh) + row * a.dh_stride, row_bytes, &full[s]);
     };
-    float w[NV][VEC];
+    if (threadIdx.x == 0)
+        for (int i = 0; i < min(depth, n); ++i) fill(i);
+    float w[NV][VEC], dw[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int v = threadIdx.x + j * blockDim.x;
         if (v < nvec) load_weight<T, VEC>(a.w, a.w32, (size_t)v * VEC, a.w_offset, w[j]);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) dw[j][k] = 0.f;
     }
-    if (blockIdx.x < a.T) load(blockIdx.x);
-    for (long long row = blockIdx.x; row < a.T; row += gridDim.x, slot ^= 1) {
+    T* dx = static_cast<T*>(a.dx) + blockIdx.x * a.dx_stride;
+    for (int i = 0; i < n; ++i, dx += step * a.dx_stride) {
+        const int s = i % depth;
+        const T* hs = reinterpret_cast<const T*>(ring + (size_t)s * 3 * row_bytes);
+        const T* ys = reinterpret_cast<const T*>(ring + ((size_t)s * 3 + 1) * row_bytes);
+        const T* es = reinterpret_cast<const T*>(ring + ((size_t)s * 3 + 2) * row_bytes);
+        const bool there = ptx::mbar_drain(&full[s], (i / depth) & 1u);
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            hv[j] = hn[j];
-            yv[j] = yn[j];
-            ev[j] = en[j];
-        }
-        if (row + gridDim.x < a.T) load(row + gridDim.x);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
             const int v = threadIdx.x + j * blockDim.x;
             if (v < nvec) {
+                RawVec<T, VEC> hv, yv;
+                hv.load(hs + v * VEC);
+                yv.load(ys + v * VEC);
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) {
-                    const float f = hv[j].get(k);
+                    const float f = hv.get(k);
                     ss = fmaf(f, f, ss);
-                    dot = fmaf(yv[j].get(k) * w[j][k], f, dot);
+                    dot = fmaf(yv.get(k) * w[j][k], f, dot);
                 }
             }
         }
-        const float2 tot = reduce_row<false>(ss, dot, red, slot);
-        const float rstd = row_rstd(tot.x, a.inv_h, a.eps);
-        const float mean = tot.y * rstd * a.inv_h;  // mean(g n)
-        T* dx = static_cast<T*>(a.dx) + row * a.dx_stride;
+        const float2 tot = reduce_row<false>(ss, dot, red, i & 1);
+        if (threadIdx.x == 0 && i > 0 && i - 1 + depth < n) fill(i - 1 + depth);
+        const float rstd = there ? row_rstd(tot.x, a.inv_h, a.eps) : quiet_nan();
+        const float back = -tot.y * rstd * rstd * rstd * a.inv_h;  // dx = rstd g + back h + dh
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int v = threadIdx.x + j * blockDim.x;
             if (v < nvec) {
-                float f[VEC];
+                RawVec<T, VEC> hv, yv, ev;
+                hv.load(hs + v * VEC);
+                yv.load(ys + v * VEC);
+                if (a.dh != nullptr) ev.load(es + v * VEC);
+                float o[VEC];
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) {
-                    const float n = hv[j].get(k) * rstd, d = yv[j].get(k);
-                    dw[j][k] = fmaf(d, n, dw[j][k]);
-                    f[k] = fmaf(rstd, fmaf(-n, mean, d * w[j][k]), a.dh != nullptr ? ev[j].get(k) : 0.f);
+                    const float f = hv.get(k), d = yv.get(k) * rstd;
+                    dw[j][k] = fmaf(d, f, dw[j][k]);
+                    o[k] = fmaf(d, w[j][k], fmaf(back, f, a.dh != nullptr ? ev.get(k) : 0.f));
                 }
-                RawVec<T, VEC> o;
-                pack_vec<T, VEC>(o, f);
-                o.store(dx + (size_t)v * VEC);
+                RawVec<T, VEC> p;
+                pack_vec<T, VEC>(p, o);
+                p.store(dx + (size_t)v * VEC);
             }
         }
     }
@@ -358,7 +375,80 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_grad(const NormGradArgs a)
         const int v = threadIdx.x + j * blockDim.x;
         if (v < nvec)
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) p[(size_t)v * VEC + k] = dw[j][k];
+            for (int k = 0; k < VEC; k += 4)
+                *reinterpret_cast<float4*>(p + (size_t)v * VEC + k) =
+                    make_float4(dw[j][k], dw[j][k + 1], dw[j][k + 2], dw[j][k + 3]);
+    }
+}
+
+// Any other alignment or width: NE elements a thread, the next token's in registers while one is reduced and written.
+template <typename T, int NE>
+__global__ void __launch_bounds__(kMaxThreads) k_norm_grad(const NormGradArgs a) {
+    __shared__ float2 red[2][32];
+    rows_launch_dependents();
+    rows_wait();
+    T hn[NE], yn[NE], en[NE];
+    auto request = [&](long long row) {
+        const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
+        const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
+        const T* dh = static_cast<const T*>(a.dh) + row * a.dh_stride;
+#pragma unroll
+        for (int j = 0; j < NE; ++j) {
+            const int c = threadIdx.x + j * blockDim.x;
+            if (c < a.H) {
+                hn[j] = h[c];
+                yn[j] = dy[c];
+                if (a.dh != nullptr) en[j] = dh[c];
+            }
+        }
+    };
+    if (blockIdx.x < a.T) request(blockIdx.x);
+    float w[NE], dw[NE];
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+        const int c = threadIdx.x + j * blockDim.x;
+        float f[1] = {0.f};
+        if (c < a.H) load_weight<T, 1>(a.w, a.w32, c, a.w_offset, f);
+        w[j] = f[0];
+        dw[j] = 0.f;
+    }
+    int slot = 0;
+    for (long long row = blockIdx.x; row < a.T; row += gridDim.x, slot ^= 1) {
+        T hv[NE], yv[NE], ev[NE];
+#pragma unroll
+        for (int j = 0; j < NE; ++j) {
+            hv[j] = hn[j];
+            yv[j] = yn[j];
+            ev[j] = en[j];
+        }
+        if (row + gridDim.x < a.T) request(row + gridDim.x);
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < NE; ++j)
+            if (threadIdx.x + j * blockDim.x < a.H) {
+                const float f = to_f32(hv[j]);
+                ss = fmaf(f, f, ss);
+                dot = fmaf(to_f32(yv[j]) * w[j], f, dot);
+            }
+        const float2 tot = reduce_row<false>(ss, dot, red, slot);
+        const float rstd = row_rstd(tot.x, a.inv_h, a.eps);
+        const float mean = tot.y * rstd * a.inv_h;  // mean(g n)
+        T* dx = static_cast<T*>(a.dx) + row * a.dx_stride;
+#pragma unroll
+        for (int j = 0; j < NE; ++j) {
+            const int c = threadIdx.x + j * blockDim.x;
+            if (c < a.H) {
+                const float n = to_f32(hv[j]) * rstd, d = to_f32(yv[j]);
+                dw[j] = fmaf(d, n, dw[j]);
+                dx[c] = from_f32<T>(fmaf(rstd, fmaf(-n, mean, d * w[j]), a.dh != nullptr ? to_f32(ev[j]) : 0.f));
+            }
+        }
+    }
+    if (a.part == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+        const int c = threadIdx.x + j * blockDim.x;
+        if (c < a.H) a.part[(size_t)blockIdx.x * a.H + c] = dw[j];
     }
 }
 
@@ -449,10 +539,11 @@ __global__ void __launch_bounds__(32 * kSumGroups) k_sum_parts(const float* part
 }
 
 template <typename... P, typename... A>
-static cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+static cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -475,14 +566,14 @@ static cudaError_t norm_vec(const NormArgs& a, cudaStream_t s) {
     auto go = [&](auto kernel, int nv) {
         const int tx = row_threads(nvec, nv);
         const int ty = std::max(1, 128 / tx);
-        return launch(kernel, dim3((unsigned)((a.T + ty - 1) / ty)), dim3(tx, ty), s, a);
+        return launch(kernel, dim3((unsigned)((a.T + ty - 1) / ty)), dim3(tx, ty), 0, s, a);
     };
     // Two vectors a thread: 16384 x 2048 bf16 36.8 us to int8, 40.4 us to bf16, against 42.4 / 41.2 us with one, 37.2 /
     // 41.1 us with four and 41.3 / 43.5 us with eight (a warp per row).  One where that leaves less than two warps.
     if (nvec <= 64) return go(k_norm<T, VEC, 1>, 1);
     if (nvec <= kMaxThreads * 2) return go(k_norm<T, VEC, 2>, 2);
     if (nvec <= kMaxThreads * 4) return go(k_norm<T, VEC, 4>, 4);
-    return launch(k_norm_wide<T, VEC>, dim3((unsigned)a.T), dim3(kWideThreads), s, a);
+    return launch(k_norm_wide<T, VEC>, dim3((unsigned)a.T), dim3(kWideThreads), 0, s, a);
 }
 
 template <typename T>
@@ -497,15 +588,6 @@ static cudaError_t norm_type(const NormArgs& a, cudaStream_t s) {
     return vec ? norm_vec<T, V>(a, s) : norm_vec<T, 1>(a, s);
 }
 
-template <typename T, int VEC>
-static cudaError_t grad_vec(const NormGradArgs& a, cudaStream_t s) {
-    const int nvec = a.H / VEC;
-    const dim3 grid((unsigned)norm_grad_parts(a.T));
-    if (nvec <= kMaxThreads) return launch(k_norm_grad<T, VEC, 1>, grid, dim3(row_threads(nvec, 1)), s, a);
-    if (nvec <= kMaxThreads * 2) return launch(k_norm_grad<T, VEC, 2>, grid, dim3(row_threads(nvec, 2)), s, a);
-    return launch(k_norm_grad_wide<T, VEC>, grid, dim3(kWideThreads), s, a);
-}
-
 template <typename T>
 static cudaError_t grad_type(const NormGradArgs& a, cudaStream_t s) {
     constexpr int V = kVecOf<T>;
@@ -513,7 +595,24 @@ static cudaError_t grad_type(const NormGradArgs& a, cudaStream_t s) {
     const bool vec = a.H % V == 0 && mult16(a.h, a.h_stride, size) && mult16(a.dy, a.dy_stride, size) &&
                      (!a.dh || mult16(a.dh, a.dh_stride, size)) && mult16(a.dx, a.dx_stride, size) &&
                      (!a.w || mult16(a.w, 0, size));
-    return vec ? grad_vec<T, V>(a, s) : grad_vec<T, 1>(a, s);
+    const dim3 grid((unsigned)norm_grad_parts(a.T));
+    if (!vec) {
+        if (a.H <= kMaxThreads) return launch(k_norm_grad<T, 1>, grid, dim3(row_threads(a.H, 1)), 0, s, a);
+        if (a.H <= kMaxThreads * 4) return launch(k_norm_grad<T, 4>, grid, dim3(row_threads(a.H, 4)), 0, s, a);
+        if (a.H <= kMaxThreads * 8) return launch(k_norm_grad<T, 8>, grid, dim3(row_threads(a.H, 8)), 0, s, a);
+        return launch(k_norm_grad_wide<T, 1>, grid, dim3(kWideThreads), 0, s, a);
+    }
+    const int nvec = a.H / V;
+    if (nvec > kMaxThreads * 2) return launch(k_norm_grad_wide<T, V>, grid, dim3(kWideThreads), 0, s, a);
+    const size_t token = 3 * (size_t)a.H * size;
+    const int depth = std::max(2, std::min(kMaxRing, (int)(kRingBytes / token)));
+    auto go = [&](auto kernel, int nv) -> cudaError_t {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(depth * token));
+        if (e != cudaSuccess) return e;
+        return launch(kernel, grid, dim3(row_threads(nvec, nv)), depth * token, s, a, depth);
+    };
+    // two vectors a thread halve what a thread spends on each token's reduction (8192 x 2048 bf16: 28.8 against 30.6 us)
+    return nvec <= 64 ? go(k_norm_grad_ring<T, 1>, 1) : go(k_norm_grad_ring<T, 2>, 2);
 }
 
 }  // namespace norm
@@ -531,7 +630,7 @@ cudaError_t launch_add_rmsnorm_grad(const NormGradArgs& a, int dtype, float* dwe
                     : dtype == VH_F16 ? norm::grad_type<__half>(a, s)
                                       : norm::grad_type<float>(a, s);
     if (e != cudaSuccess || dweight == nullptr) return e;
-    return norm::launch(norm::k_sum_parts, dim3((unsigned)((a.H + 31) / 32)), dim3(32, norm::kSumGroups), s,
+    return norm::launch(norm::k_sum_parts, dim3((unsigned)((a.H + 31) / 32)), dim3(32, norm::kSumGroups), 0, s,
                         (const float*)a.part, norm_grad_parts(a.T), a.H, dweight);
 }
 

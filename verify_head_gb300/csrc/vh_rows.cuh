@@ -42,6 +42,7 @@ struct RawVec<T, 1> {
     T v;
     __device__ __forceinline__ float get(int) const { return to_f32(v); }
     __device__ __forceinline__ void set(int, float f) { v = from_f32<T>(f); }
+    __device__ __forceinline__ void clear() { v = from_f32<T>(0.f); }
     __device__ __forceinline__ void load(const T* p) { v = *p; }
     __device__ __forceinline__ void store(T* p) const { *p = v; }
 };
@@ -94,6 +95,10 @@ struct RawVec {
             u[i >> 1] = (i & 1) ? (u[i >> 1] & 0xFFFFu) | (h << 16) : (u[i >> 1] & 0xFFFF0000u) | h;
         }
     }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < N; ++i) u[i] = 0u;
+    }
     __device__ __forceinline__ void fill_lowest() {  // -inf
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -143,6 +148,37 @@ __device__ __forceinline__ void pack_vec(RawVec<T, VEC>& r, const float (&f)[VEC
 #pragma unroll
         for (int i = 0; i < VEC / 2; ++i) r.set2(i, f[2 * i], f[2 * i + 1]);
     }
+}
+
+// ---------------------------------------------------------------------------
+// Two floats in one register pair: the packed fp32 instructions issue once for both.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 f2_get(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
 }
 
 // ---------------------------------------------------------------------------
@@ -209,36 +245,6 @@ __device__ __forceinline__ Stat stat_join(Stat a, Stat b) {
     stat_shift(a, c);
     stat_shift(b, c);
     return Stat{c, a.s + b.s, a.t + b.t};
-}
-
-// Two floats in one register pair: the packed fp32 instructions issue once for both.
-struct F2 {
-    unsigned long long v;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 f2_get(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
 }
 
 // The same statistics with the sums in two halves, for long runs of scores.
