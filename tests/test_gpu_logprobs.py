@@ -74,6 +74,21 @@ def test_strides_and_alignment(vh, V, pitch, offset, dtype):
     check(vh.logits_logprobs(x, tokens.cuda(), 4), x, tokens, 4)
 
 
+def test_rows_past_32_bits(vh):
+    """Rows more than 2^31 elements apart."""
+    V, pitch = 4000, 1_500_000_000
+    flat = torch.empty(2 * pitch + V, dtype=BF, device="cuda")
+    x = flat.as_strided((3, V), (pitch, 1))
+    x.copy_(torch.randn(3, V, generator=gen(1)).to(BF))
+    tokens = torch.tensor([1, 2, 3], dtype=torch.int32)
+    got = vh.logits_logprobs(x, tokens.cuda(), 5)
+    check(got, x, tokens, 5)
+    one = torch.ones(3, device="cuda")
+    want = vh.logits_logprobs_grad(x.contiguous(), tokens.cuda(), got[2], got[1], one, one)
+    vh.logits_logprobs_grad(x, tokens.cuda(), got[2], got[1], one, one, dlogits=x)
+    assert torch.equal(x, want)
+
+
 @pytest.mark.parametrize("dtype", [BF, HF, F32])
 @pytest.mark.parametrize("V", [5, 700, 9001, 100000])
 def test_masks_and_special_rows(vh, V, dtype):
@@ -187,15 +202,17 @@ def test_grad_matches_formula(vh, R, V, dtype, parts):
     close(d, want, U[dtype] * (1 + 2 ** -10) + 2.0 ** -22, size.double() * (sums(V) + 2.0 ** -18) + TINY[dtype])
 
 
-@pytest.mark.parametrize("V,pitch,offset", [(1000, 1000, 1), (999, 1003, 0)])
-def test_grad_strides_and_in_place(vh, V, pitch, offset):
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V,pitch,offset", [(1000, 1000, 1), (999, 1003, 0), (5, 7, 3), (9001, 9001, 5), (4096, 4104, 0)])
+def test_grad_strides_and_in_place(vh, V, pitch, offset, dtype):
+    """Rows that lie alike in their 16-byte slots (in place) and not (a new tensor), with the same results."""
     g = gen(V)
-    x = logits(g, 6, V, BF, pitch=pitch, offset=offset)
+    x = logits(g, 6, V, dtype, pitch=pitch, offset=offset)
     tokens = torch.randint(0, V, (6,), generator=g, dtype=torch.int32).cuda()
     gl = torch.randn(6, generator=g).cuda()
     _, ent, lse = vh.logits_logprobs(x, tokens)[:3]
-    d = vh.logits_logprobs_grad(x.contiguous(), tokens, lse, ent, gl, gl)
-    whole = torch.empty(0, dtype=BF, device="cuda").set_(x.untyped_storage())
+    d = vh.logits_logprobs_grad(x, tokens, lse, ent, gl, gl)
+    whole = torch.empty(0, dtype=dtype, device="cuda").set_(x.untyped_storage())
     before = whole.clone()
     same = vh.logits_logprobs_grad(x, tokens, lse, ent, gl, gl, dlogits=x)
     assert same is x and torch.equal(x, d)

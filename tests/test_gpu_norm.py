@@ -100,6 +100,24 @@ def test_strides_and_alignment(vh, dtype, H, pitch, offset):
     assert torch.equal(whole[mask], before[mask])  # nothing beside the rows was written
 
 
+def test_rows_past_32_bits(vh):
+    """Rows more than 2^31 elements apart."""
+    H, pitch = 2048, 1_500_000_000
+    flat = torch.empty(2 * pitch + H, dtype=BF, device="cuda")
+    x = flat.as_strided((3, H), (pitch, 1))
+    x.copy_(torch.randn(3, H, generator=gen(1)).to(BF))
+    w = torch.randn(H, generator=gen(2)).to(BF).cuda()
+    near = x.contiguous()
+    want = vh.add_rmsnorm(near, near, w)
+    q = vh.add_rmsnorm_q8(x, near, w)
+    dx, dw = vh.add_rmsnorm_grad(near, x, w, dh=x)
+    want_dx, want_dw = vh.add_rmsnorm_grad(near, near, w, dh=near)
+    assert torch.equal(dx, want_dx) and torch.equal(dw, want_dw)
+    assert torch.equal(q[0], vh.add_rmsnorm_q8(near, near, w)[0])
+    y, h = vh.add_rmsnorm(x, near, w, h=x)
+    assert torch.equal(y, want[0]) and torch.equal(x, want[1])
+
+
 @pytest.mark.parametrize("H", [2048, 20001])
 def test_output_on_an_input(vh, H):
     g = gen(H)

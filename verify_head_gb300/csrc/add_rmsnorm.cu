@@ -28,7 +28,8 @@ namespace norm {
 constexpr int kMaxThreads = 512;  // register-resident rows: up to 128 registers a thread
 constexpr int kWideThreads = 512;
 constexpr int kMaxRing = 4;                // tokens in flight per CTA of the gradient
-constexpr size_t kRingBytes = 56 * 1024;   // of shared memory per CTA that its ring stays below (four CTAs per SM)
+constexpr size_t kRingBytes = 56 * 1024;   // of shared memory per CTA that a ring of over two tokens stays below
+constexpr size_t kSmRingBytes = 220 * 1024;  // of shared memory per SM for rings
 
 // Sums of two values over the threads of one row (threadIdx.y) of the CTA.
 // MAX_SECOND: the second value is a maximum instead of a sum.  All threads of
@@ -70,11 +71,11 @@ __device__ __forceinline__ void load_weight(const void* w, int w32, size_t i, fl
     } else if (w32) {
         const float* p = static_cast<const float*>(w) + i;
         if constexpr (VEC == 1) {
-            f[0] = __ldg(p) + off;
+            f[0] = *p + off;
         } else {
 #pragma unroll
             for (int k = 0; k < VEC; k += 4) {
-                const float4 q = __ldg(reinterpret_cast<const float4*>(p + k));
+                const float4 q = *reinterpret_cast<const float4*>(p + k);
                 f[k] = q.x + off;
                 f[k + 1] = q.y + off;
                 f[k + 2] = q.z + off;
@@ -310,8 +311,10 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_grad_ring(const NormGradAr
         if (a.dh != nullptr)
             ptx::bulk_copy(to + 2 * row_bytes, static_cast<const T*>(a.dh) + row * a.dh_stride, row_bytes, &full[s]);
     };
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
+        rows_fence_async();
         for (int i = 0; i < min(depth, n); ++i) fill(i);
+    }
     float w[NV][VEC], dw[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -588,14 +591,15 @@ static cudaError_t norm_type(const NormArgs& a, cudaStream_t s) {
     return vec ? norm_vec<T, V>(a, s) : norm_vec<T, 1>(a, s);
 }
 
+// `parts`: the CTAs that share the tokens (in: at most).
 template <typename T>
-static cudaError_t grad_type(const NormGradArgs& a, cudaStream_t s) {
+static cudaError_t grad_type(const NormGradArgs& a, int& parts, cudaStream_t s) {
     constexpr int V = kVecOf<T>;
     const int size = (int)sizeof(T);
     const bool vec = a.H % V == 0 && mult16(a.h, a.h_stride, size) && mult16(a.dy, a.dy_stride, size) &&
                      (!a.dh || mult16(a.dh, a.dh_stride, size)) && mult16(a.dx, a.dx_stride, size) &&
                      (!a.w || mult16(a.w, 0, size));
-    const dim3 grid((unsigned)norm_grad_parts(a.T));
+    dim3 grid((unsigned)parts);
     if (!vec) {
         if (a.H <= kMaxThreads) return launch(k_norm_grad<T, 1>, grid, dim3(row_threads(a.H, 1)), 0, s, a);
         if (a.H <= kMaxThreads * 4) return launch(k_norm_grad<T, 4>, grid, dim3(row_threads(a.H, 4)), 0, s, a);
@@ -606,6 +610,8 @@ static cudaError_t grad_type(const NormGradArgs& a, cudaStream_t s) {
     if (nvec > kMaxThreads * 2) return launch(k_norm_grad_wide<T, V>, grid, dim3(kWideThreads), 0, s, a);
     const size_t token = 3 * (size_t)a.H * size;
     const int depth = std::max(2, std::min(kMaxRing, (int)(kRingBytes / token)));
+    parts = std::min(parts, 152 * std::min(4, (int)(kSmRingBytes / (depth * token))));  // one resident wave
+    grid.x = (unsigned)parts;
     auto go = [&](auto kernel, int nv) -> cudaError_t {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(depth * token));
         if (e != cudaSuccess) return e;
@@ -626,12 +632,13 @@ cudaError_t launch_add_rmsnorm(const NormArgs& a, int dtype, cudaStream_t s) {
 }
 
 cudaError_t launch_add_rmsnorm_grad(const NormGradArgs& a, int dtype, float* dweight, cudaStream_t s) {
-    cudaError_t e = dtype == VH_BF16  ? norm::grad_type<__nv_bfloat16>(a, s)
-                    : dtype == VH_F16 ? norm::grad_type<__half>(a, s)
-                                      : norm::grad_type<float>(a, s);
+    int parts = norm_grad_parts(a.T);
+    cudaError_t e = dtype == VH_BF16  ? norm::grad_type<__nv_bfloat16>(a, parts, s)
+                    : dtype == VH_F16 ? norm::grad_type<__half>(a, parts, s)
+                                      : norm::grad_type<float>(a, parts, s);
     if (e != cudaSuccess || dweight == nullptr) return e;
     return norm::launch(norm::k_sum_parts, dim3((unsigned)((a.H + 31) / 32)), dim3(32, norm::kSumGroups), 0, s,
-                        (const float*)a.part, norm_grad_parts(a.T), a.H, dweight);
+                        (const float*)a.part, parts, a.H, dweight);
 }
 
 }  // namespace vh

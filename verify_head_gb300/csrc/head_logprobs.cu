@@ -231,7 +231,7 @@ struct Epilogue {
         for (int i = 0; i < 32; ++i) m = fmaxf(m, x[i]);
         if (a.seg_max != nullptr) {
             const int seg = v0 / kSeg;
-            if (row < a.R) a.seg_max[(size_t)row * a.segs + seg] = m;
+            if (row < a.R && vh_guard(seg < a.segs, a.err)) a.seg_max[(size_t)row * a.segs + seg] = m;
             // rows whose scores are kept: 128 bytes each, lane = head row again
             const uint32_t keep = __ballot_sync(0xFFFFFFFFu, row < a.R && ord_f32(m) >= bounds[g * 32 + lane]);
             float* p = a.scores + ((size_t)seg * a.Rp + row0 + g * 32) * kSeg + lane;
@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(kThreadsH, 1)
             bool ok = true, waited = false;
             auto release_first_ring = [&](uint32_t n) {
                 rows_wait();
+                rows_fence_async();
                 for (uint32_t j = 0; j < n; ++j)
                     tma_load_2d(stage_x + (size_t)j * kStageX, &map_x, &bars->full[j], (int)(j % k_stages) * kBlockK, 0,
                                 pol_x);
@@ -483,6 +484,7 @@ __global__ void __launch_bounds__(kThreadsH, 1)
             };
             auto release_first_ring = [&](uint32_t n) {
                 rows_wait();
+                rows_fence_async();
                 for (uint32_t j = 0; j < n; ++j) load_x(j);
                 waited = true;
             };

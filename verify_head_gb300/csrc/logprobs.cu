@@ -352,10 +352,11 @@ __global__ void __launch_bounds__(kSelThreads, 4) k_logprobs_top(const LogprobAr
 }
 
 // ---------------------------------------------------------------------------
-// Gradient: every thread takes kGradUnroll vectors of its row.
+// Gradient: every thread takes kGradUnroll slots of its row.
 
 constexpr int kGradUnroll = 4;
 
+// VEC: elements of a 16-byte slot, as the forward pass cuts a row (both tensors' rows lie alike in their slots), or 1.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreadsL) k_logprobs_grad(const LogprobGradArgs a, int chunks) {
     rows_launch_dependents();
@@ -364,44 +365,48 @@ __global__ void __launch_bounds__(kThreadsL) k_logprobs_grad(const LogprobGradAr
     const int chunk = (int)(blockIdx.x % chunks);
     const T* x = static_cast<const T*>(a.logits) + (long long)row * a.stride;
     T* d = static_cast<T*>(a.dlogits) + (long long)row * a.d_stride;
-    const long long nvec = a.V / VEC;
+    const int shift = VEC == 1 ? 0 : (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    const long long e0 = ((long long)chunk * kThreadsL * kGradUnroll + threadIdx.x) * VEC - shift;
+    constexpr long long kStep = (long long)kThreadsL * VEC;
+    RawVec<T, VEC> r[kGradUnroll];
+#pragma unroll
+    for (int u = 0; u < kGradUnroll; ++u) {
+        const long long e = e0 + u * kStep;
+        if (e >= 0 && e + VEC <= a.V) r[u].load(x + e);
+    }
     const float lse = a.lse[row];
     const int tok = a.tokens != nullptr ? a.tokens[row] : -1;
     const bool given = tok >= 0 && tok < a.V;
     float gl = (given && a.g_logprob != nullptr) ? a.g_logprob[row] : 0.f;
-    float ge = a.g_entropy != nullptr ? a.g_entropy[row] : 0.f;
+    const float ge = a.g_entropy != nullptr ? a.g_entropy[row] : 0.f;
     const float ent = a.g_entropy != nullptr ? a.entropy[row] : 0.f;
     const bool empty = lse == neg_inf();
     // dx = p (k0 - ge2 y) with y = log2 p: -g_lp p - g_ent p (ln2 y + entropy)
     const float k0 = empty ? 0.f : (lse != lse ? quiet_nan() : -gl - ge * ent);
     const float ge2 = empty ? 0.f : ge * kLn2;
     if (empty) gl = 0.f;
-    const long long v0 = (long long)chunk * kThreadsL * kGradUnroll + threadIdx.x;
-    RawVec<T, VEC> r[kGradUnroll];
+    auto of = [&](float v) {
+        const float y = fmaxf((v - lse) * kLog2e, kFloorY);
+        return (empty ? 0.f : ex2(y)) * fmaf(-ge2, y, k0);
+    };
 #pragma unroll
     for (int u = 0; u < kGradUnroll; ++u) {
-        const long long v = v0 + u * kThreadsL;
-        if (v < nvec) r[u].load(x + v * VEC);
-    }
-#pragma unroll
-    for (int u = 0; u < kGradUnroll; ++u) {
-        const long long v = v0 + u * kThreadsL;
-        if (v < nvec) {
+        const long long e = e0 + u * kStep;
+        if (e >= 0 && e + VEC <= a.V) {
             float f[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float y = fmaxf((r[u].get(i) - lse) * kLog2e, kFloorY);
-                const float p = empty ? 0.f : ex2(y);
-                f[i] = p * fmaf(-ge2, y, k0);
-            }
-            const long long at = (long long)tok - v * VEC;
-            if (given && at >= 0 && at < VEC) {
+            for (int i = 0; i < VEC; ++i) f[i] = of(r[u].get(i));
+            if (given && tok >= e && tok < e + VEC) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) f[i] += i == at ? gl : 0.f;
+                for (int i = 0; i < VEC; ++i) f[i] += e + i == tok ? gl : 0.f;
             }
             RawVec<T, VEC> o;
             pack_vec<T, VEC>(o, f);
-            o.store(d + v * VEC);
+            o.store(d + e);
+        } else if (VEC > 1 && e < a.V && e + VEC > 0) {  // a row's ends
+            for (int i = 0; i < VEC; ++i)
+                if (e + i >= 0 && e + i < a.V)
+                    d[e + i] = from_f32<T>(of(to_f32(x[e + i])) + (given && e + i == tok ? gl : 0.f));
         }
     }
 }
@@ -439,7 +444,7 @@ static cudaError_t forward(const LogprobArgs& a, cudaStream_t s) {
 template <typename T, int VEC>
 static cudaError_t grad_vec(const LogprobGradArgs& a, cudaStream_t s) {
     const long long per = (long long)kThreadsL * kGradUnroll * VEC;
-    const long long chunks = (a.V + per - 1) / per;
+    const long long chunks = ((long long)a.V + VEC - 1 + per - 1) / per;  // up to VEC - 1 places before the first element
     const long long rows_max = std::max(1LL, 2147483647LL / chunks);
     for (long long r0 = 0; r0 < a.R; r0 += rows_max) {
         LogprobGradArgs b = a;
@@ -460,9 +465,9 @@ static cudaError_t grad_vec(const LogprobGradArgs& a, cudaStream_t s) {
 template <typename T>
 static cudaError_t grad(const LogprobGradArgs& a, cudaStream_t s) {
     constexpr int V = kVecOf<T>;
-    const bool vec = a.V % V == 0 && a.stride % V == 0 && a.d_stride % V == 0 &&
-                     ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits)) & 15) == 0;
-    return vec ? grad_vec<T, V>(a, s) : grad_vec<T, 1>(a, s);
+    const bool alike = ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.dlogits)) & 15) == 0 &&
+                       (a.stride - a.d_stride) % V == 0;
+    return alike ? grad_vec<T, V>(a, s) : grad_vec<T, 1>(a, s);
 }
 
 }  // namespace lp

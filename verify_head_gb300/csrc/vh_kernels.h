@@ -143,7 +143,7 @@ struct NormGradArgs {
     int w32;
     float eps, w_offset, inv_h;
 };
-constexpr int kNormGradParts = 608;  // CTAs that share the tokens: four per SM
+constexpr int kNormGradParts = 608;  // CTAs that share the tokens, at most: four per SM
 int norm_grad_parts(int T);
 cudaError_t launch_add_rmsnorm_grad(const NormGradArgs& a, int dtype, float* dweight, cudaStream_t s);
 

@@ -15,6 +15,8 @@ namespace vh {
 
 __device__ __forceinline__ void rows_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void rows_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Before bulk or tensor copies read what kernels before this one wrote.
+__device__ __forceinline__ void rows_fence_async() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
 // Element types and vectors of VEC elements (16 bytes, or one element).
@@ -78,9 +80,12 @@ struct RawVec {
             u[2] = q.z;
             u[3] = q.w;
         } else {
-            const U32x8 q = ld_stream32(p);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] = q.v[i];
+            // read once: no L1 allocation, first out of L2; not the read-only path, since a kernel of this library that
+            // let this one start early may have written the row
+            asm volatile(
+                "ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                : "l"(p));
         }
     }
     __device__ __forceinline__ void store(T* p) const {
