@@ -31,13 +31,12 @@ constexpr int kMaxRing = 4;                // tokens in flight per CTA of the gr
 constexpr size_t kRingBytes = 56 * 1024;   // of shared memory per CTA that a ring of over two tokens stays below
 constexpr size_t kSmRingBytes = 220 * 1024;  // of shared memory per SM for rings
 
-// Sums of two values over the threads of one row (threadIdx.y) of the CTA.
-// MAX_SECOND: the second value is a maximum instead of a sum.  All threads of
-// the CTA call it; `slot` alternates between calls.  The lower half of a warp
-// goes on with the first value and the upper half with the second, so both
-// take one chain of shuffles.
-template <bool MAX_SECOND>
-__device__ __forceinline__ float2 reduce_row(float a, float b, float2 (*red)[32], int slot) {
+// Sums of two values over the threads of one row: wpr warps, of which this is number w; `row`: the row's wpr slots in
+// shared memory.  MAX_SECOND: the second value is a maximum instead of a sum.  sync(): a barrier of all threads that
+// call this together (not called where a row has one warp).  The lower half of a warp goes on with the first value and
+// the upper half with the second, so both take one chain of shuffles.
+template <bool MAX_SECOND, typename Sync>
+__device__ __forceinline__ float2 reduce_row(float a, float b, float2* row, int w, int wpr, Sync sync) {
     const int lane = threadIdx.x & 31;
     const bool second = lane >= 16;
     auto join = [&](float v, float o) { return MAX_SECOND && second ? fmaxf(v, o) : v + o; };
@@ -45,19 +44,24 @@ __device__ __forceinline__ float2 reduce_row(float a, float b, float2 (*red)[32]
     float v = join(second ? b : a, other);
 #pragma unroll
     for (int m = 8; m >= 1; m >>= 1) v = join(v, __shfl_xor_sync(0xFFFFFFFFu, v, m));
-    const int wpr = blockDim.x >> 5;
     if (wpr == 1) return make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
-    float2* row = red[slot] + threadIdx.y * wpr;
-    if ((lane & 15) == 0) reinterpret_cast<float*>(row + (threadIdx.x >> 5))[lane >> 4] = v;
-    __syncthreads();
+    if ((lane & 15) == 0) reinterpret_cast<float*>(row + w)[lane >> 4] = v;
+    sync();
     float2 t = row[0];
 #pragma unroll 4
-    for (int w = 1; w < wpr; ++w) {
-        const float2 o = row[w];
+    for (int i = 1; i < wpr; ++i) {
+        const float2 o = row[i];
         t.x += o.x;
         t.y = MAX_SECOND ? fmaxf(t.y, o.y) : t.y + o.y;
     }
     return t;
+}
+
+// The same for a CTA of one row per threadIdx.y.
+template <bool MAX_SECOND>
+__device__ __forceinline__ float2 reduce_row(float a, float b, float2* red) {
+    const int wpr = blockDim.x >> 5;
+    return reduce_row<MAX_SECOND>(a, b, red + threadIdx.y * wpr, threadIdx.x >> 5, wpr, [] { __syncthreads(); });
 }
 
 // 1 / sqrt(sum / H + eps).
@@ -145,7 +149,7 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float (&u)[VEC], c
 // One row per threadIdx.y, NV vectors of VEC elements per thread, the row in registers.
 template <typename T, int VEC, int NV>
 __global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a) {
-    __shared__ float2 red[1][32];
+    __shared__ float2 red[32];
     rows_launch_dependents();
     rows_wait();
     const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a) {
             }
         }
     }
-    const float2 tot = reduce_row<true>(ss, amax, red, 0);
+    const float2 tot = reduce_row<true>(ss, amax, red);
     const float rstd = row_rstd(tot.x, a.inv_h, a.eps);
     if (!live) return;
     if (a.out == VH_NORM_SAME) {
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a) {
 // may lie on the inputs as in the kernel above.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kWideThreads) k_norm_wide(const NormArgs a) {
-    __shared__ float2 red[1][32];
+    __shared__ float2 red[32];
     rows_launch_dependents();
     rows_wait();
     const long long row = blockIdx.x;
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(const NormArgs a) {
             amax = fmaxf(amax, fabsf(hv[k] * w[k]));
         }
     }
-    const float2 tot = reduce_row<true>(ss, amax, red, 0);
+    const float2 tot = reduce_row<true>(ss, amax, red);
     const float rstd = row_rstd(tot.x, a.inv_h, a.eps);
     const float q = a.out == VH_NORM_INT8 ? 127.0f : 448.0f;
     const Quant z = make_quant(tot.y, q);
@@ -278,63 +282,140 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(const NormArgs a) {
 // share of dw in registers and leaves it in part[c][H]; a second kernel adds
 // the shares in CTA order, so the sums do not change from call to call.
 
-// Whole 16-byte vectors: the rows come by bulk copies into a ring of `depth` tokens in shared memory, so that loads
-// are in flight whatever the registers hold (8192 x 2048 bf16: 28.7 against 30.2 us with the next token's vectors in
-// registers, where 64 registers a thread left no room for a second token).  Token i is summed, reduced (one barrier)
-// and written; behind that barrier every thread is done with token i - 1, whose place is refilled.
-// A wait is for copies that the CTA itself has issued; should it expire (it is bounded) the token's results are NaN.
-template <typename T, int NV>
-__global__ void __launch_bounds__(kMaxThreads) k_norm_grad_ring(const NormGradArgs a, const int depth) {
-    constexpr int VEC = kVecOf<T>;
-    extern __shared__ __align__(128) uint8_t ring[];  // [depth][h, dy, dh][H]
+// The rows come by bulk copies into a ring of `depth` places in shared memory, so that loads are in flight whatever
+// the registers hold.  A place holds ty tokens, so that narrow rows fill a CTA.  tx * ty threads sum, reduce (one
+// barrier) and write a group of tokens; one thread of a further warp refills a place when they are done with it.
+//   8192 x 2048 bf16: 29.6 us, against 30.2 us with the next token's vectors in registers, where 64 registers a
+//   thread left no room for a second token, and 42.1 us with a thread of the summing warps refilling.
+//   16384 x 512: 18.9 us, against 46.0 us with one token at a time.
+// Waits are for copies that the CTA has issued and for its own warps; should one expire (they are bounded) the
+// group's results are NaN.
+//
+// VEC: elements per 16-byte vector where rows are whole aligned vectors, else 1: then a token's place holds the
+// 16-byte granules that its row touches.  What those hold beside the row is its neighbours' (or the gap between
+// rows); at the two ends of the tensor, where there is no neighbour, only whole granules are copied and the elements
+// outside them are stored one by one.  8191 x 2561 bf16: 63.4 us, against 98.9 us with loads of single elements.
+
+// The granules of a row of `bytes` that may be copied: [lo, hi).
+__device__ __forceinline__ void window(uintptr_t b, uint32_t bytes, bool first, bool last, uintptr_t& lo, uintptr_t& hi) {
+    lo = (first ? b + 15 : b) & ~uintptr_t(15);
+    hi = (last ? b + bytes : b + bytes + 15) & ~uintptr_t(15);
+    if (hi < lo) hi = lo;
+}
+
+// One row of elements into its place: the bytes that are copied (bar null: the ends of the first and last row are
+// stored, nothing is copied yet).
+template <typename T>
+__device__ __forceinline__ uint32_t fill_granules(uint8_t* to, const T* p, uint32_t bytes, bool first, bool last,
+                                                  unsigned long long* bar) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    uintptr_t lo, hi;
+    window(b, bytes, first, last, lo, hi);
+    if (bar != nullptr) {
+        if (hi > lo)
+            ptx::bulk_copy(to + (lo - (b & ~uintptr_t(15))), reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo), bar);
+    } else if (first || last) {
+        T* at = reinterpret_cast<T*>(to + (b & 15));
+        const int n = (int)(bytes / sizeof(T));
+        const int head = min(n, (int)((lo - b) / sizeof(T)));             // elements before the window
+        const int tail = hi > b ? min(n, (int)((hi - b) / sizeof(T))) : 0;  // the first one behind it
+        for (int i = 0; i < head; ++i) at[i] = p[i];
+        for (int i = max(head, tail); i < n; ++i) at[i] = p[i];
+    }
+    return (uint32_t)(hi - lo);
+}
+
+template <typename T, int VEC, int NV>
+__global__ void __launch_bounds__(kMaxThreads + 32) k_norm_grad(const NormGradArgs a, const int tx, const int ty,
+                                                                 const int depth, const uint32_t pitch) {
+    extern __shared__ __align__(128) uint8_t ring[];  // [depth][ty tokens][h, dy, dh][pitch]
     __shared__ float2 red[2][32];
-    __shared__ unsigned long long full[kMaxRing];
-    const int nvec = a.H / VEC;
-    const uint32_t row_bytes = (uint32_t)(a.H * sizeof(T));
-    const int streams = a.dh != nullptr ? 3 : 2;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < depth; ++i) ptx::mbar_init(&full[i], 1);
+    __shared__ unsigned long long full[kMaxRing], empty[kMaxRing];
+    const int nvec = a.H / VEC, workers = tx * ty;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const uint32_t place = (uint32_t)ty * 3 * pitch, row_bytes = (uint32_t)(a.H * sizeof(T));
+    if (tid == 0) {
+        for (int i = 0; i < depth; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], (uint32_t)workers / 32);
+        }
         ptx::fence_barrier_init();
     }
     __syncthreads();
-    rows_launch_dependents();
     rows_wait();
-    const long long step = gridDim.x;
-    const int n = (int)((a.T - blockIdx.x + step - 1) / step);  // tokens of this CTA
-    auto fill = [&](int i) {                                    // by thread 0
-        const long long row = blockIdx.x + i * step;
-        const int s = i % depth;
-        uint8_t* to = ring + (size_t)s * 3 * row_bytes;
-        ptx::mbar_arrive_expect_tx(&full[s], streams * row_bytes);
-        ptx::bulk_copy(to, static_cast<const T*>(a.h) + row * a.h_stride, row_bytes, &full[s]);
-        ptx::bulk_copy(to + row_bytes, static_cast<const T*>(a.dy) + row * a.dy_stride, row_bytes, &full[s]);
-        if (a.dh != nullptr)
-            ptx::bulk_copy(to + 2 * row_bytes, static_cast<const T*>(a.dh) + row * a.dh_stride, row_bytes, &full[s]);
-    };
-    if (threadIdx.x == 0) {
+    const long long groups = ((long long)a.T + ty - 1) / ty;
+    const int n = (int)((groups - blockIdx.x + gridDim.x - 1) / gridDim.x);  // of this CTA
+
+    if (tid >= workers) {
+        if (lane != 0) return;
         rows_fence_async();
-        for (int i = 0; i < min(depth, n); ++i) fill(i);
+        const T* h = static_cast<const T*>(a.h);
+        const T* dy = static_cast<const T*>(a.dy);
+        const T* dh = static_cast<const T*>(a.dh);
+        for (int i = 0, s = 0, ph = 1; i < n; ++i) {
+            if (!ptx::mbar_drain(&empty[s], ph)) return;
+            const long long t0 = (blockIdx.x + (long long)i * gridDim.x) * ty;
+            const int m = (int)min((long long)ty, a.T - t0);
+            uint8_t* to = ring + (size_t)s * place;
+            if constexpr (VEC > 1) {
+                ptx::mbar_arrive_expect_tx(&full[s], (dh != nullptr ? 3u : 2u) * m * row_bytes);
+                for (int q = 0; q < m; ++q, to += 3 * pitch) {
+                    ptx::bulk_copy(to, h + (t0 + q) * a.h_stride, row_bytes, &full[s]);
+                    ptx::bulk_copy(to + pitch, dy + (t0 + q) * a.dy_stride, row_bytes, &full[s]);
+                    if (dh != nullptr) ptx::bulk_copy(to + 2 * pitch, dh + (t0 + q) * a.dh_stride, row_bytes, &full[s]);
+                }
+            } else {
+                auto rows = [&](unsigned long long* bar) {
+                    uint32_t bytes = 0;
+                    for (int q = 0; q < m; ++q) {
+                        const long long t = t0 + q;
+                        const bool first = t == 0, last = t == a.T - 1;
+                        uint8_t* at = to + (size_t)q * 3 * pitch;
+                        bytes += fill_granules(at, h + t * a.h_stride, row_bytes, first, last, bar);
+                        bytes += fill_granules(at + pitch, dy + t * a.dy_stride, row_bytes, first, last, bar);
+                        if (dh != nullptr)
+                            bytes += fill_granules(at + 2 * pitch, dh + t * a.dh_stride, row_bytes, first, last, bar);
+                    }
+                    return bytes;
+                };
+                ptx::mbar_arrive_expect_tx(&full[s], rows(nullptr));
+                rows(&full[s]);
+            }
+            if (++s == depth) {
+                s = 0;
+                ph ^= 1;
+            }
+        }
+        return;
     }
+
+    const int ry = tid / tx, rx = tid - ry * tx, wpr = tx >> 5;
+    auto sync = [&] { asm volatile("bar.sync 1, %0;" ::"r"(workers) : "memory"); };
     float w[NV][VEC], dw[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int v = threadIdx.x + j * blockDim.x;
-        if (v < nvec) load_weight<T, VEC>(a.w, a.w32, (size_t)v * VEC, a.w_offset, w[j]);
+        const int v = rx + j * tx;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) dw[j][k] = 0.f;
+        for (int k = 0; k < VEC; ++k) w[j][k] = dw[j][k] = 0.f;
+        if (v < nvec) load_weight<T, VEC>(a.w, a.w32, (size_t)v * VEC, a.w_offset, w[j]);
     }
-    T* dx = static_cast<T*>(a.dx) + blockIdx.x * a.dx_stride;
-    for (int i = 0; i < n; ++i, dx += step * a.dx_stride) {
-        const int s = i % depth;
-        const T* hs = reinterpret_cast<const T*>(ring + (size_t)s * 3 * row_bytes);
-        const T* ys = reinterpret_cast<const T*>(ring + ((size_t)s * 3 + 1) * row_bytes);
-        const T* es = reinterpret_cast<const T*>(ring + ((size_t)s * 3 + 2) * row_bytes);
-        const bool there = ptx::mbar_drain(&full[s], (i / depth) & 1u);
+    for (int i = 0, s = 0, ph = 0; i < n; ++i) {
+        const long long token = (blockIdx.x + (long long)i * gridDim.x) * ty + ry;
+        const bool live = token < a.T;
+        const uint8_t* pl = ring + (size_t)s * place + (uint32_t)ry * 3 * pitch;
+        auto at = [&](const uint8_t* p, const void* base, long long stride) {  // where a row lies in its place
+            const uintptr_t b = VEC > 1 ? 0 : reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + token * stride);
+            return reinterpret_cast<const T*>(p + (b & 15));
+        };
+        const T* hs = at(pl, a.h, a.h_stride);
+        const T* ys = at(pl + pitch, a.dy, a.dy_stride);
+        const T* es = at(pl + 2 * pitch, a.dh, a.dh_stride);
+        const bool there = ptx::mbar_drain(&full[s], ph);
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
-            if (v < nvec) {
+            const int v = rx + j * tx;
+            if (live && v < nvec) {
                 RawVec<T, VEC> hv, yv;
                 hv.load(hs + v * VEC);
                 yv.load(ys + v * VEC);
@@ -346,14 +427,14 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_grad_ring(const NormGradAr
                 }
             }
         }
-        const float2 tot = reduce_row<false>(ss, dot, red, i & 1);
-        if (threadIdx.x == 0 && i > 0 && i - 1 + depth < n) fill(i - 1 + depth);
+        const float2 tot = reduce_row<false>(ss, dot, red[i & 1] + ry * wpr, rx >> 5, wpr, sync);
         const float rstd = there ? row_rstd(tot.x, a.inv_h, a.eps) : quiet_nan();
         const float back = -tot.y * rstd * rstd * rstd * a.inv_h;  // dx = rstd g + back h + dh
+        T* dx = static_cast<T*>(a.dx) + token * a.dx_stride;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
-            if (v < nvec) {
+            const int v = rx + j * tx;
+            if (live && v < nvec) {
                 RawVec<T, VEC> hv, yv, ev;
                 hv.load(hs + v * VEC);
                 yv.load(ys + v * VEC);
@@ -370,88 +451,33 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_grad_ring(const NormGradAr
                 p.store(dx + (size_t)v * VEC);
             }
         }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&empty[s]);
+        if (++s == depth) {
+            s = 0;
+            ph ^= 1;
+        }
     }
+    // The grid is one resident wave: CTAs of the next kernel that came before this one's end would take places that the
+    // wave after needs (8192 x 2048 bf16: 39.7 us a call with the signal at the start).
+    rows_launch_dependents();
     if (a.part == nullptr) return;
     float* p = a.part + (size_t)blockIdx.x * a.H;
+    float* sum = reinterpret_cast<float*>(ring) + (size_t)ry * a.H;  // [ty][H]
+    if (ty > 1) sync();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int v = threadIdx.x + j * blockDim.x;
+        const int v = rx + j * tx;
         if (v < nvec)
 #pragma unroll
-            for (int k = 0; k < VEC; k += 4)
-                *reinterpret_cast<float4*>(p + (size_t)v * VEC + k) =
-                    make_float4(dw[j][k], dw[j][k + 1], dw[j][k + 2], dw[j][k + 3]);
+            for (int k = 0; k < VEC; ++k) (ty > 1 ? sum : p)[(size_t)v * VEC + k] = dw[j][k];
     }
-}
-
-// Any other alignment or width: NE elements a thread, the next token's in registers while one is reduced and written.
-template <typename T, int NE>
-__global__ void __launch_bounds__(kMaxThreads) k_norm_grad(const NormGradArgs a) {
-    __shared__ float2 red[2][32];
-    rows_launch_dependents();
-    rows_wait();
-    T hn[NE], yn[NE], en[NE];
-    auto request = [&](long long row) {
-        const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
-        const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
-        const T* dh = static_cast<const T*>(a.dh) + row * a.dh_stride;
-#pragma unroll
-        for (int j = 0; j < NE; ++j) {
-            const int c = threadIdx.x + j * blockDim.x;
-            if (c < a.H) {
-                hn[j] = h[c];
-                yn[j] = dy[c];
-                if (a.dh != nullptr) en[j] = dh[c];
-            }
-        }
-    };
-    if (blockIdx.x < a.T) request(blockIdx.x);
-    float w[NE], dw[NE];
-#pragma unroll
-    for (int j = 0; j < NE; ++j) {
-        const int c = threadIdx.x + j * blockDim.x;
-        float f[1] = {0.f};
-        if (c < a.H) load_weight<T, 1>(a.w, a.w32, c, a.w_offset, f);
-        w[j] = f[0];
-        dw[j] = 0.f;
-    }
-    int slot = 0;
-    for (long long row = blockIdx.x; row < a.T; row += gridDim.x, slot ^= 1) {
-        T hv[NE], yv[NE], ev[NE];
-#pragma unroll
-        for (int j = 0; j < NE; ++j) {
-            hv[j] = hn[j];
-            yv[j] = yn[j];
-            ev[j] = en[j];
-        }
-        if (row + gridDim.x < a.T) request(row + gridDim.x);
-        float ss = 0.f, dot = 0.f;
-#pragma unroll
-        for (int j = 0; j < NE; ++j)
-            if (threadIdx.x + j * blockDim.x < a.H) {
-                const float f = to_f32(hv[j]);
-                ss = fmaf(f, f, ss);
-                dot = fmaf(to_f32(yv[j]) * w[j], f, dot);
-            }
-        const float2 tot = reduce_row<false>(ss, dot, red, slot);
-        const float rstd = row_rstd(tot.x, a.inv_h, a.eps);
-        const float mean = tot.y * rstd * a.inv_h;  // mean(g n)
-        T* dx = static_cast<T*>(a.dx) + row * a.dx_stride;
-#pragma unroll
-        for (int j = 0; j < NE; ++j) {
-            const int c = threadIdx.x + j * blockDim.x;
-            if (c < a.H) {
-                const float n = to_f32(hv[j]) * rstd, d = to_f32(yv[j]);
-                dw[j] = fmaf(d, n, dw[j]);
-                dx[c] = from_f32<T>(fmaf(rstd, fmaf(-n, mean, d * w[j]), a.dh != nullptr ? to_f32(ev[j]) : 0.f));
-            }
-        }
-    }
-    if (a.part == nullptr) return;
-#pragma unroll
-    for (int j = 0; j < NE; ++j) {
-        const int c = threadIdx.x + j * blockDim.x;
-        if (c < a.H) a.part[(size_t)blockIdx.x * a.H + c] = dw[j];
+    if (ty == 1) return;
+    sync();
+    for (int c = tid; c < a.H; c += workers) {
+        float t = 0.f;
+        for (int q = 0; q < ty; ++q) t += reinterpret_cast<const float*>(ring)[(size_t)q * a.H + c];
+        p[c] = t;
     }
 }
 
@@ -485,7 +511,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_grad_wide(const NormGradA
                 dot = fmaf(yv.get(k) * w[k], f, dot);
             }
         }
-        const float2 tot = reduce_row<false>(ss, dot, red, slot);
+        const float2 tot = reduce_row<false>(ss, dot, red[slot]);
         const float rstd = row_rstd(tot.x, a.inv_h, a.eps);
         const float mean = tot.y * rstd * a.inv_h;
         for (int v = threadIdx.x; v < nvec; v += kWideThreads) {
@@ -516,7 +542,6 @@ constexpr int kSumGroups = 32;
 __global__ void __launch_bounds__(32 * kSumGroups) k_sum_parts(const float* part, int n, int H, float* out) {
     constexpr int kBatch = 10;
     __shared__ float s[kSumGroups][33];
-    rows_launch_dependents();
     rows_wait();
     const int c = blockIdx.x * 32 + threadIdx.x;
     float v = 0.f;
@@ -532,6 +557,7 @@ __global__ void __launch_bounds__(32 * kSumGroups) k_sum_parts(const float* part
             for (int i = 0; i < kBatch; ++i) v += x[i];
         }
     s[threadIdx.y][threadIdx.x] = v;
+    rows_launch_dependents();
     __syncthreads();
     if (threadIdx.y == 0 && c < H) {
         float t = 0.f;
@@ -576,6 +602,9 @@ static cudaError_t norm_vec(const NormArgs& a, cudaStream_t s) {
     if (nvec <= 64) return go(k_norm<T, VEC, 1>, 1);
     if (nvec <= kMaxThreads * 2) return go(k_norm<T, VEC, 2>, 2);
     if (nvec <= kMaxThreads * 4) return go(k_norm<T, VEC, 4>, 4);
+    if constexpr (VEC == 1) {
+        if (nvec <= kMaxThreads * 8) return go(k_norm<T, VEC, 8>, 8);
+    }
     return launch(k_norm_wide<T, VEC>, dim3((unsigned)a.T), dim3(kWideThreads), 0, s, a);
 }
 
@@ -599,26 +628,32 @@ static cudaError_t grad_type(const NormGradArgs& a, int& parts, cudaStream_t s) 
     const bool vec = a.H % V == 0 && mult16(a.h, a.h_stride, size) && mult16(a.dy, a.dy_stride, size) &&
                      (!a.dh || mult16(a.dh, a.dh_stride, size)) && mult16(a.dx, a.dx_stride, size) &&
                      (!a.w || mult16(a.w, 0, size));
-    dim3 grid((unsigned)parts);
-    if (!vec) {
-        if (a.H <= kMaxThreads) return launch(k_norm_grad<T, 1>, grid, dim3(row_threads(a.H, 1)), 0, s, a);
-        if (a.H <= kMaxThreads * 4) return launch(k_norm_grad<T, 4>, grid, dim3(row_threads(a.H, 4)), 0, s, a);
-        if (a.H <= kMaxThreads * 8) return launch(k_norm_grad<T, 8>, grid, dim3(row_threads(a.H, 8)), 0, s, a);
-        return launch(k_norm_grad_wide<T, 1>, grid, dim3(kWideThreads), 0, s, a);
-    }
-    const int nvec = a.H / V;
-    if (nvec > kMaxThreads * 2) return launch(k_norm_grad_wide<T, V>, grid, dim3(kWideThreads), 0, s, a);
-    const size_t token = 3 * (size_t)a.H * size;
-    const int depth = std::max(2, std::min(kMaxRing, (int)(kRingBytes / token)));
-    parts = std::min(parts, 152 * std::min(4, (int)(kSmRingBytes / (depth * token))));  // one resident wave
-    grid.x = (unsigned)parts;
-    auto go = [&](auto kernel, int nv) -> cudaError_t {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(depth * token));
+    auto go = [&](auto kernel, int n, int nv, size_t pitch) -> cudaError_t {  // n vectors (or elements), nv a thread
+        const int tx = row_threads(n, nv);
+        const int ty = std::max(1, std::min(256 / tx, (int)(kRingBytes / kMaxRing / (3 * pitch))));  // keeps the ring deep
+        const size_t place = (size_t)ty * 3 * pitch;
+        const int depth = std::max(2, std::min(kMaxRing, (int)(kRingBytes / place)));
+        const long long groups = ((long long)a.T + ty - 1) / ty;
+        // one resident wave
+        parts = (int)std::min({(long long)parts, groups, 152LL * std::min(4, (int)(kSmRingBytes / (depth * place)))});
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(depth * place));
         if (e != cudaSuccess) return e;
-        return launch(kernel, grid, dim3(row_threads(nvec, nv)), depth * token, s, a, depth);
+        return launch(kernel, dim3((unsigned)parts), dim3(tx * ty + 32), depth * place, s, a, tx, ty, depth, (uint32_t)pitch);
     };
-    // two vectors a thread halve what a thread spends on each token's reduction (8192 x 2048 bf16: 28.8 against 30.6 us)
-    return nvec <= 64 ? go(k_norm_grad_ring<T, 1>, 1) : go(k_norm_grad_ring<T, 2>, 2);
+    if (vec) {
+        // Two vectors a thread halve what a thread spends on each token's reduction (8192 x 2048 bf16: 28.8 against
+        // 30.6 us with one).
+        const int n = a.H / V;
+        const size_t pitch = (size_t)a.H * size;
+        if (n <= 64) return go(k_norm_grad<T, V, 1>, n, 1, pitch);
+        if (n <= kMaxThreads * 2) return go(k_norm_grad<T, V, 2>, n, 2, pitch);
+        if (n <= kMaxThreads * 4) return go(k_norm_grad<T, V, 4>, n, 4, pitch);
+        return launch(k_norm_grad_wide<T, V>, dim3((unsigned)parts), dim3(kWideThreads), 0, s, a);
+    }
+    const size_t pitch = ((size_t)a.H * size + 30) / 16 * 16;  // a row may start 15 bytes into its first granule
+    if (a.H <= kMaxThreads * 8) return go(k_norm_grad<T, 1, 8>, a.H, 8, pitch);
+    if (a.H <= kMaxThreads * 16) return go(k_norm_grad<T, 1, 16>, a.H, 16, pitch);
+    return launch(k_norm_grad_wide<T, 1>, dim3((unsigned)parts), dim3(kWideThreads), 0, s, a);
 }
 
 }  // namespace norm
