@@ -436,15 +436,39 @@ def spec_verify_greedy_nvfp4_packed(hidden, packed, tensor_scale, draft_ids, B: 
 _dtypes = {}  # torch dtype -> vh_dtype
 _f32 = _i32 = None  # torch.float32, torch.int32
 _current_device = None  # torch's query of the current device
+_compiled = None  # the compiled marshalling (csrc/marshal.cpp); False where it has not been built
 
 
 def _setup():
     """Fills the names above on the first call (torch is imported no earlier than it is needed)."""
-    global _f32, _i32, _current_device
+    global _f32, _i32, _current_device, _raw_stream
     torch = _torch()
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", False)
     _dtypes.update({torch.float32: VH_F32, torch.bfloat16: VH_BF16, torch.float16: VH_F16})
     _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _f32, _i32 = torch.float32, torch.int32
+
+
+def _compiled_calls():
+    """The compiled marshalling, bound to the loaded library, or False.  It takes the usual calls (outputs and
+    workspace given, torch's current stream) and leaves every other to the checks below."""
+    global _compiled
+    if _use_debug:
+        return False
+    if _compiled is None:
+        _torch()
+        L = lib()
+        try:
+            from . import _marshal as m
+        except ImportError:
+            _compiled = False
+        else:
+            for name in ("vh_add_rmsnorm", "vh_add_rmsnorm_grad", "vh_logits_logprobs", "vh_logits_logprobs_grad",
+                         "vh_head_logprobs"):
+                m.bind(name, ctypes.cast(getattr(L, name), ctypes.c_void_p).value)
+            _compiled = m
+    return _compiled
 
 
 def _dtype(t, name):
@@ -551,6 +575,13 @@ def add_rmsnorm(x, residual=None, weight=None, eps: float = 1e-6, weight_offset:
     x, residual [T,H] fp32 / bf16 / fp16 (rows may be strided), weight [H] of x's type or fp32.
     h may be `residual` itself (updated in place); without a residual h is x and nothing is written.
     -> (y, h)"""
+    if stream is None and y is not None:
+        m = _compiled_calls()
+        if m:
+            st = m.add_rmsnorm(x, residual, weight, eps, weight_offset, y, h, None)
+            if st <= 0:
+                _check(st, "add_rmsnorm")
+                return y, (x if h is None else h)
     if y is None or (residual is not None and h is None):
         with _allocating(stream):
             y = _empty_rows(x) if y is None else y
@@ -563,6 +594,13 @@ def add_rmsnorm_q8(x, residual=None, weight=None, eps: float = 1e-6, weight_offs
                    h=None, dtype=None, stream=None):
     """add_rmsnorm with 8-bit rows: q [T,H] (torch.int8, or torch.float8_e4m3fn; `dtype` where q is not given) and
     scales [T] fp32 with q * scales[:, None] standing for the normed rows.  -> (q, scales, h)"""
+    if stream is None and q is not None and scales is not None and dtype is None:
+        m = _compiled_calls()
+        if m:
+            st = m.add_rmsnorm(x, residual, weight, eps, weight_offset, q, h, scales)
+            if st <= 0:
+                _check(st, "add_rmsnorm_q8")
+                return q, scales, (x if h is None else h)
     torch = _torch()
     if q is None or scales is None or (residual is not None and h is None):
         with _allocating(stream):
@@ -587,6 +625,13 @@ def add_rmsnorm_grad(dy, h, weight=None, eps: float = 1e-6, weight_offset: float
                      ws=None, stream=None):
     """Gradient of add_rmsnorm from the sum h that it returned: dx [T,H] is the gradient of x and of the residual
     alike (dh, the gradient that reaches h, included), dweight [H] fp32 (None without a weight).  -> (dx, dweight)"""
+    if stream is None and dx is not None:
+        m = _compiled_calls()
+        if m:
+            st = m.add_rmsnorm_grad(dy, h, weight, eps, weight_offset, dh, dx, dweight, ws)
+            if st <= 0:
+                _check(st, "add_rmsnorm_grad")
+                return dx, dweight
     torch = _torch()
     dev = _device(h)
     dt = _dtype(h, "h")
@@ -648,6 +693,13 @@ def logits_logprobs(logits, tokens, top_n: int = 0, logprob=None, entropy=None, 
                     top_logprobs=None, ws=None, stream=None):
     """logits [R,V] fp32 / bf16 / fp16 (rows may be strided), tokens [R] int32 (outside [0,V): no token, logprob 0;
     None: logprob is None)  -> (logprob [R], entropy [R], lse [R], top_ids [R,top_n] int32, top_logprobs [R,top_n])."""
+    if stream is None and ws is not None:
+        m = _compiled_calls()
+        if m:
+            st = m.logits_logprobs(logits, tokens, top_n, logprob, entropy, lse, top_ids, top_logprobs, ws)
+            if st <= 0:
+                _check(st, "logits_logprobs")
+                return logprob if tokens is not None else None, entropy, lse, top_ids, top_logprobs
     dev = _device(logits)
     dt = _dtype(logits, "logits")
     shape = logits.shape
@@ -665,6 +717,13 @@ def logits_logprobs(logits, tokens, top_n: int = 0, logprob=None, entropy=None, 
 def logits_logprobs_grad(logits, tokens, lse, entropy=None, g_logprob=None, g_entropy=None, dlogits=None, stream=None):
     """Gradient of logits_logprobs' logprob and entropy (their gradients [R] fp32, either may be None) with respect to
     the logits, from the lse and entropy it returned; dlogits may be `logits` itself.  -> dlogits [R,V]"""
+    if stream is None and dlogits is not None:
+        m = _compiled_calls()
+        if m:
+            st = m.logits_logprobs_grad(logits, tokens, lse, entropy, g_logprob, g_entropy, dlogits)
+            if st <= 0:
+                _check(st, "logits_logprobs_grad")
+                return dlogits
     dev = _device(logits)
     dt = _dtype(logits, "logits")
     shape, dtype = logits.shape, logits.dtype
@@ -694,6 +753,13 @@ def head_logprobs(hidden, W_full, tokens, top_n: int = 0, logprob=None, entropy=
                   top_logprobs=None, ws=None, stream=None):
     """logits_logprobs of the scores hidden @ W_full.T, which are not returned: hidden [R,H] bf16, W_full [V,H] bf16,
     tokens [R] int32 -> (logprob [R], entropy [R], lse [R], top_ids [R,top_n] int32, top_logprobs [R,top_n])."""
+    if stream is None and ws is not None:
+        m = _compiled_calls()
+        if m:
+            st = m.head_logprobs(hidden, W_full, tokens, top_n, logprob, entropy, lse, top_ids, top_logprobs, ws)
+            if st <= 0:
+                _check(st, "head_logprobs")
+                return logprob if tokens is not None else None, entropy, lse, top_ids, top_logprobs
     dev = _device(hidden)
     _place(W_full, "W_full", dev)
     _require_cuda(hidden, W_full)

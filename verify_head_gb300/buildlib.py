@@ -2,7 +2,9 @@
 
 Each .cu file under csrc/ is compiled in parallel, then linked into one
 shared library next to this file.  Only one -gencode (sm_103a); host code is
-portable (x86_64 and aarch64).
+portable (x86_64 and aarch64).  Beside it _marshal.so, the compiled argument
+marshalling of the norm and log-probability calls: it needs Python's and
+torch's headers, and where they are missing the binding marshals in Python.
 """
 from __future__ import annotations
 
@@ -11,12 +13,16 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libverifyhead.so")
 LIB_DEBUG = os.path.join(HERE, "libverifyhead_debug.so")  # -DVH_DEBUG: device-side index guards
+MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -47,12 +53,41 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_marshal(force: bool = False):
+    """Compiles _marshal.so with the host compiler against the running torch; returns its path, or None (with the
+    compiler's message on stderr) where that is not possible."""
+    deps = (MARSHAL_SRC, os.path.join(ROOT, "include", "verifyhead.h"))
+    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
+        return MARSHAL
+    try:
+        import torch
+        top = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(nvcc()))
+        inc = [os.path.join(top, "include"), os.path.join(top, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+        lib = os.path.join(top, "lib")
+        tmp = MARSHAL + f".tmp{os.getpid()}"
+        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-I" + p for p in inc), MARSHAL_SRC,
+               "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath," + lib]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(r.stderr[-2000:])
+        os.replace(tmp, MARSHAL)
+        return MARSHAL
+    except (ImportError, OSError, RuntimeError, AttributeError) as e:
+        print(f"_marshal.so was not built (calls are marshalled in Python): {e}", file=sys.stderr)
+        return None
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: bool = False) -> str:
     """Compile and link libverifyhead.so (debug: libverifyhead_debug.so with
     -DVH_DEBUG, whose kernels guard their indices and report failures in the
     workspace error word); returns its path."""
     lib = LIB_DEBUG if debug else LIB
     if not force and up_to_date(lib):
+        if not debug:
+            build_marshal()
         return lib
     obj_dir = os.path.join(BUILD_DIR, "debug") if debug else BUILD_DIR
     os.makedirs(obj_dir, exist_ok=True)
@@ -70,7 +105,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
         return obj, r.stdout + r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        marshal = None if debug else ex.submit(build_marshal, force)
         results = list(ex.map(compile_one, sources()))
+        if marshal is not None:
+            marshal.result()
     if verbose:
         for _, log in results:
             if log.strip():

@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprob
 
 // One row per CTA: its statistics and its alternatives, after k_logprobs<T, true> of n_scan CTAs.
 template <typename T>
-__global__ void __launch_bounds__(kSelThreads, 4) k_logprobs_top(const LogprobArgs a, const Ws ws, const int row_segs,
+__global__ void __launch_bounds__(kSelThreads, 3) k_logprobs_top(const LogprobArgs a, const Ws ws, const int row_segs,
                                                                  const int n_scan) {
     constexpr int kHeld = 4;
     __shared__ SelectSmem s_sel;

@@ -425,20 +425,16 @@ template <int HELD, typename Segs, typename Meanwhile, typename Emit>
 __device__ __forceinline__ void select_top(SelectSmem& sm, int segs, int n, uint32_t floor, const Segs& sg,
                                            Meanwhile meanwhile, Emit emit) {
     constexpr int kHeld = HELD;
-    constexpr int kAtOnce = 3;   // segments a warp loads at once
+    constexpr int kAtOnce = 4;   // segments a warp loads at once
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float held[kHeld];
-    auto hold = [&](int base) {
+    auto hold = [&](int base) {  // no branches between the loads
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int g = base + i * kSelThreads + tid;
-            if (base + i * kSelThreads < segs) held[i] = g < segs ? sg.max(g) : neg_inf();
-        }
+        for (int i = 0; i < kHeld; ++i) held[i] = sg.max(min(base + i * kSelThreads + tid, segs - 1));
     };
     auto held_max = [&](int base, float m) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-            if (base + i * kSelThreads < segs) m = fmaxf(m, held[i]);
+        for (int i = 0; i < kHeld; ++i) m = fmaxf(m, base + i * kSelThreads + tid < segs ? held[i] : neg_inf());
         return m;
     };
     hold(0);
@@ -474,7 +470,7 @@ __device__ __forceinline__ void select_top(SelectSmem& sm, int segs, int n, uint
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
                 const int g = base + i * kSelThreads + tid;
-                if (base + i * kSelThreads < segs && g < segs && ord_f32(held[i]) >= bound) {
+                if (!(held[i] < least) && g < segs && ord_f32(held[i]) >= bound) {
                     const int e = atomicAdd(&sm.n_seg, 1);
                     if (e < kSelSegs) sm.seg[e] = (uint32_t)g;
                 }
