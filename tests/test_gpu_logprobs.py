@@ -380,3 +380,63 @@ def test_refusals(vh):
         vh.head_logprobs(h[:, :24].contiguous(), W[:, :24].contiguous(), t)  # H % 16
     with pytest.raises(vh.VHError):
         vh.head_logprobs(h, W, t, ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+
+
+# ---------------------------------------------------------------------------
+# The choice of alternatives: every way through it
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [33, 400, 513, 4633, 60771, 200001])
+@pytest.mark.parametrize("n", [1, 20, 32])
+@pytest.mark.parametrize("kind", ["plain", "few allowed", "equal", "two values", "late ties", "comb"])
+def test_alternatives(vh, V, n, kind, dtype):
+    """Units near and below n, rows with fewer allowed places than n, ties at the bound early and late in the row, and
+    large values laid out in one group of units."""
+    g = gen(V + n)
+    R = 3
+    x = (torch.randn(R, V, generator=g) * 2).to(dtype)
+    if kind == "few allowed":
+        keep = torch.randperm(V, generator=g)[:7]
+        y = torch.full_like(x, -math.inf)
+        y[:, keep] = x[:, keep]
+        y[1] = -math.inf
+        y[2, V // 2] = math.nan
+        x = y
+    elif kind == "equal":
+        x = torch.full_like(x, 1.5)
+        x[2] = 0.0
+        x[2, ::3] = -0.0
+    elif kind == "two values":
+        x = (torch.rand(R, V, generator=g) < 0.5).to(dtype)
+    elif kind == "late ties":
+        x = x.clamp(max=0.5)
+        x[:, : V // 2] = -1.0
+        x[:, V // 2 + 3] = 9.0
+    elif kind == "comb":  # descending values in every 64th slot of 32 bytes, so that one group holds them all
+        per = 32 // x.element_size()
+        at = torch.arange(V)
+        x = torch.where(at // per % 64 == 0, 1000.0 - (at / V * 500), torch.zeros(V)).to(dtype).repeat(R, 1)
+    tokens = torch.randint(0, V, (R,), generator=g, dtype=torch.int32)
+    x = x.cuda()
+    got = vh.logits_logprobs(x, tokens.cuda(), n)
+    _, _, _, ids, top = logprobs64(x, tokens, n)
+    assert torch.equal(got[3].cpu(), ids)
+    close(got[4], top, 2.0 ** -22, sums(V) + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("R,V,n", [(2, 999, 32), (150, 999, 32), (3, 300, 20), (130, 9000, 32)])
+def test_head_alternatives_with_ties(vh, R, V, n):
+    """Equal scores throughout, then in half of the head, and none: in the order of the ids."""
+    H = 64
+    x = torch.ones(R, H, dtype=BF, device="cuda")
+    for kind in range(3):
+        W = torch.zeros(V, H, dtype=BF, device="cuda")
+        if kind == 1:
+            W[V // 2:, 0] = 1.0
+        if kind == 2:
+            W[:, 0] = torch.randint(-3, 4, (V,), generator=gen(V)).to(BF).cuda()
+        tokens = torch.zeros(R, dtype=torch.int32)
+        got = vh.head_logprobs(x, W, tokens.cuda(), n)
+        _, _, _, ids, _ = logprobs64((x[:1].double() @ W.double().t()), tokens[:1], n)
+        assert torch.equal(got[3].cpu(), ids.expand(R, n))

@@ -597,6 +597,7 @@ struct FinishArgs {
 
 // A row's blocks of scores for select_top.
 struct Blocks {
+    static constexpr bool kLane = false;
     using Item = float;
     const FinishArgs& a;
     int row;

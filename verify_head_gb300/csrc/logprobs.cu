@@ -7,9 +7,9 @@
 // Forward: one pass over the logits.  A row is cut into slots of 32 aligned
 // bytes and segments of 32 slots (one warp load of 1 KiB).  Each thread keeps
 // a running maximum and the two sums of Stat; where alternatives are wanted
-// the warp also writes each segment's maximum, and a second kernel, one CTA
-// per row, picks the alternatives from the segments with the largest maxima
-// (select_top), reading about n segments again.
+// the maxima of segments, or of slots, are written too, and a second kernel,
+// one CTA per row, picks the alternatives from the units with the largest
+// maxima (select_top), reading about n units again.
 //
 // All rows' segments are shared out evenly over one resident wave of CTAs; a
 // row that several CTAs hold pieces of meets in the workspace, where the last
@@ -64,30 +64,33 @@ struct Row {
     }
 };
 
-// A row's segments for select_top.
-template <typename T>
-struct Segments {
+// A row's units for select_top: segments, or single slots.
+template <typename T, bool SLOTS>
+struct RowUnits {
+    static constexpr bool kLane = SLOTS;
     using Item = RawVec<T, kSlot<T>>;
     const Row<T>& x;
     const float* maxima;
+    __device__ __forceinline__ int slot(int g) const { return SLOTS ? g : g * 32 + (threadIdx.x & 31); }
     __device__ __forceinline__ float max(int g) const { return __ldcg(maxima + g); }
     __device__ __forceinline__ Item load(int g) const {
         Item it;
-        x.load(g * 32 + (threadIdx.x & 31), it);
+        x.load(slot(g), it);
         return it;
     }
     __device__ __forceinline__ float peak(const Item& it) const { return it.max(); }
     template <typename F>
     __device__ __forceinline__ void each(const Item& it, int g, float b, F take) const {
-        const long long e0 = x.first(g * 32 + (threadIdx.x & 31));
+        const long long e0 = x.first(slot(g));
 #pragma unroll
         for (int j = 0; j < kSlot<T>; ++j)
             if (!(it.get(j) < b) && e0 + j >= 0 && e0 + j < x.V) take(make_key(it.get(j), (uint32_t)(e0 + j)));
     }
-    static constexpr int kBatches = kSlot<T>;
+    static constexpr int kBatches = SLOTS ? 1 : kSlot<T>;
     __device__ __forceinline__ unsigned long long key(int g, int i) const {
-        const long long e = x.first(g * 32) + i * 32 + (threadIdx.x & 31);
-        if (e < 0 || e >= x.V) return 0ull;
+        const int lane = threadIdx.x & 31;
+        const long long e = x.first(SLOTS ? g : g * 32) + i * 32 + lane;
+        if (e < 0 || e >= x.V || (SLOTS && lane >= kSlot<T>)) return 0ull;
         return make_key(to_f32((reinterpret_cast<const T*>(x.base) + x.shift)[e]), (uint32_t)e);
     }
 };
@@ -100,10 +103,15 @@ __host__ __device__ inline int max_segs(int V, int size) {
 
 // The call's units are the R x segs segments, cut into one range per CTA: every CTA has the same work to within a
 // segment, whatever R and V.  A range holds whole rows and, at its ends, pieces of rows that other CTAs share.
+// Rows of up to kSlotSegs segments keep the maximum of every slot for the alternatives, longer ones that of every
+// segment: there have to be clearly more units than alternatives, and a row of 65,536 bf16 has 128 segments.
+constexpr int kSlotSegs = 256;
+__host__ __device__ inline int row_units(int row_segs) { return row_segs <= kSlotSegs ? row_segs * 32 : row_segs; }
+
 struct Ws {
     unsigned int* ticket;  // [kTargetCtas], zero between calls: by the first CTA of a shared row
     float4* part;          // [kTargetCtas][2]: c, s, t of the CTA's first piece of a row begun before it, and of its last
-    float* seg_max;        // [R][segs], alternatives only
+    float* unit_max;       // [R][row_units], alternatives only
     float4* row;           // [R]: c, s, t of rows that are not shared, alternatives only
 };
 constexpr size_t kTicketEnd = kWsHeaderBytes + (size_t)kTargetCtas * 4;
@@ -151,7 +159,7 @@ struct Block {
 // request_after() puts the first block of the next piece there: loads are in flight while a block, or a row, is
 // summed up.
 template <typename T, bool TOP, typename F>
-__device__ __forceinline__ Stat scan(const Piece<T>& pc, Block<T>& next, float* seg_max, F request_after) {
+__device__ __forceinline__ Stat scan(const Piece<T>& pc, Block<T>& next, float* unit_max, bool slots, F request_after) {
     constexpr int VEC = kSlot<T>;
     constexpr bool kHalf = std::is_same<T, __half>::value;
     constexpr float lift = kHalf ? kLiftHalf : kLift, lift_from = kHalf ? kLiftFromHalf : kLiftFrom;
@@ -160,9 +168,13 @@ __device__ __forceinline__ Stat scan(const Piece<T>& pc, Block<T>& next, float* 
     run.clear();
     auto keep_max = [&](int g, float m) {
         if (TOP) {
-            float w;
-            asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(w) : "f"(m));
-            if (lane == 0) seg_max[g] = w;
+            if (slots) {
+                unit_max[g * 32 + lane] = m;
+            } else {
+                float w;
+                asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(w) : "f"(m));
+                if (lane == 0) unit_max[g] = w;
+            }
         }
     };
     // The row's ends, element by element: the first segment by warp 0, the last by warp 1.
@@ -270,7 +282,7 @@ __global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprob
         const int g1 = (int)min((long long)row_segs, g0 + left);
         left -= g1 - g0;
         const T* p = static_cast<const T*>(a.logits) + (long long)row * a.stride;
-        float* seg_max = TOP ? ws.seg_max + (size_t)row * row_segs : nullptr;
+        float* unit_max = TOP ? ws.unit_max + (size_t)row * row_units(row_segs) : nullptr;
         float tok_score = 0.f;  // requested before the scan, used after it
         bool given = false;
         if (!TOP && threadIdx.x == 0 && a.logprob != nullptr) {
@@ -278,7 +290,7 @@ __global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprob
             given = tok >= 0 && tok < a.V;
             if (given) tok_score = to_f32(p[tok]);
         }
-        Stat st = stat_warp(scan<T, TOP>(Piece<T>(a, row, g0, g1), next, seg_max, [&] {
+        Stat st = stat_warp(scan<T, TOP>(Piece<T>(a, row, g0, g1), next, unit_max, row_segs <= kSlotSegs, [&] {
             if (left > 0) {
                 const Piece<T> after(a, row + 1, 0, (int)min((long long)row_segs, left));
                 next.request(after, after.first());
@@ -318,10 +330,10 @@ __global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprob
 }
 
 // One row per CTA: its statistics and its alternatives, after k_logprobs<T, true> of n_scan CTAs.
-template <typename T>
+template <typename T, bool SLOTS>
 __global__ void __launch_bounds__(kSelThreads, 3) k_logprobs_top(const LogprobArgs a, const Ws ws, const int row_segs,
                                                                  const int n_scan) {
-    constexpr int kHeld = 4;
+    constexpr int kHeld = SLOTS ? 16 : 4;
     __shared__ SelectSmem s_sel;
     __shared__ RowStat s_rs;
     rows_launch_dependents();
@@ -343,7 +355,8 @@ __global__ void __launch_bounds__(kSelThreads, 3) k_logprobs_top(const LogprobAr
         }
     };
     select_top<kHeld>(
-        s_sel, (x.slots() + 31) / 32, a.top_n, 0u, Segments<T>{x, ws.seg_max + (size_t)row * row_segs}, finish,
+        s_sel, SLOTS ? x.slots() : (x.slots() + 31) / 32, a.top_n, 0u,
+        RowUnits<T, SLOTS>{x, ws.unit_max + (size_t)row * row_units(row_segs)}, finish,
         [&](int i, unsigned long long k) {
             const size_t o = (size_t)row * a.top_n + i;
             a.top_ids[o] = k != 0ull ? (int32_t)key_gid(k) : -1;
@@ -433,12 +446,13 @@ static cudaError_t forward(const LogprobArgs& a, cudaStream_t s) {
     ws.ticket = reinterpret_cast<unsigned int*>(p + kWsHeaderBytes);
     ws.part = reinterpret_cast<float4*>(p + kTicketEnd);
     ws.row = reinterpret_cast<float4*>(p + kPartEnd);
-    ws.seg_max = reinterpret_cast<float*>(p + kPartEnd + (size_t)a.R * 16);
+    ws.unit_max = reinterpret_cast<float*>(p + kPartEnd + (size_t)a.R * 16);
     const dim3 grid((unsigned)ctas((long long)a.R * segs, a.top_n > 0 ? kPerSmTop : kPerSm));
     if (a.top_n == 0) return launch(k_logprobs<T, false>, grid, dim3(kThreadsL), s, a, ws, segs);
     const cudaError_t e = launch(k_logprobs<T, true>, grid, dim3(kThreadsL), s, a, ws, segs);
     if (e != cudaSuccess) return e;
-    return launch(k_logprobs_top<T>, dim3((unsigned)a.R), dim3(kSelThreads), s, a, ws, segs, (int)grid.x);
+    return segs <= kSlotSegs ? launch(k_logprobs_top<T, true>, dim3((unsigned)a.R), dim3(kSelThreads), s, a, ws, segs, (int)grid.x)
+                             : launch(k_logprobs_top<T, false>, dim3((unsigned)a.R), dim3(kSelThreads), s, a, ws, segs, (int)grid.x);
 }
 
 template <typename T, int VEC>
@@ -473,8 +487,8 @@ static cudaError_t grad(const LogprobGradArgs& a, cudaStream_t s) {
 }  // namespace lp
 
 size_t logits_logprobs_ws_bytes(int R, int V, int top_n) {
-    // 32-bit logits have the most segments
-    return lp::kPartEnd + (top_n > 0 ? (size_t)R * 16 + round16((size_t)R * lp::max_segs(V, 4) * 4) : 0);
+    const int units = std::max(lp::row_units(lp::max_segs(V, 4)), lp::row_units(lp::max_segs(V, 2)));
+    return lp::kPartEnd + (top_n > 0 ? (size_t)R * 16 + round16((size_t)R * units * 4) : 0);
 }
 
 cudaError_t launch_logits_logprobs(const LogprobArgs& a, int dtype, cudaStream_t s) {

@@ -382,76 +382,86 @@ __device__ __forceinline__ void top_insert(unsigned long long& top, unsigned lon
 }
 
 // ---------------------------------------------------------------------------
-// The n <= kMaxTop largest elements of a row from its segments' maxima, by a
-// CTA of kSelThreads threads.  The n largest elements lie in the n segments
-// with the largest maxima (equal maxima: the lower segment first, since a
-// segment is a range of ids): any element elsewhere is preceded by n others.
+// The n <= kMaxTop largest elements of a row, from the maxima of the units it
+// is cut into, by a CTA of kSelThreads threads.
 //
-// Usual way, a few dependent steps in all: 64 groups of segments give a bound
-// (the n-th largest of their maxima: n elements at least reach it, and about
-// 1.2 n segments do); the segments that reach the bound are listed, then their
-// elements that do; an element's place is the number of listed keys above its
-// own.  Where a list overflows (many elements equal to the bound, as in a row
-// that is masked to fewer than n places) the CTA sorts instead: each warp
-// keeps the 32 largest keys of its share, first of the maxima, then of the
-// elements of the n best segments, and the lists are merged.
+// 64 groups of units give a bound: the n-th largest of their maxima, which n
+// elements at least reach, and about 1.3 n units do.  Those units are listed,
+// then their elements that reach the bound; an element's place is the number
+// of listed keys above its own.  No step depends on a search, so the whole is
+// a chain of a few loads and barriers.
+//
+// Where a list overflows many elements are equal to the bound (a row masked
+// to fewer than n places, equal logits): then only the elements above it are
+// listed, and the rest come, in the order of their ids, from the first units
+// that reach it.  Where even those overflow (rows laid out against the
+// groups) the CTA sorts: each warp keeps the 32 largest keys of its share,
+// first of the maxima, then of the elements of the n best units, which hold
+// the n largest elements since any element elsewhere is preceded by n others
+// (equal maxima: the lower unit first, as a unit is a range of ids).
 
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelGroups = 64;
-constexpr int kSelSegs = 128;   // listed segments
-constexpr int kSelElems = 256;  // listed elements
+constexpr int kSelUnits = 256;  // listed units
+constexpr int kSelElems = 512;  // listed elements: 31 units of 16, which a row of fewer units than n has at most
 
 struct SelectSmem {
+    uint32_t mine[kSelThreads];
     uint32_t group[kSelGroups];
-    uint32_t seg[kSelSegs];
+    uint32_t unit[kSelUnits];
     unsigned long long elem[kSelElems];
     unsigned long long sorted[kSelWarps][32];
     uint32_t bound;
-    int n_seg, n_elem;
+    int n_unit, n_elem;
 };
 
-// Segs: float max(int g), the maximum of segment g < segs (NaN left out);
-//   Item load(int g), this lane's elements of segment g (the warp loads it together);
+// HELD: maxima a thread holds in registers; up to HELD * kSelThreads units are read once, more are read twice.
+// Units: float max(int g), the maximum of unit g < units (NaN left out);
+//   kLane: whether a unit is read by one lane (each its own) or by a warp together;
+//   Item load(int g), this lane's elements of unit g;
 //   float peak(const Item&), the largest of them (NaN left out);
 //   void each(const Item&, int g, float b, f): f(key) with the argmax key of those that are not below b;
-//   kBatches, key(int g, int i): the lane's key in batch i < kBatches of the segment's elements, 0 outside the row.
+//   kBatches, key(int g, int i): by a warp, the lane's key in batch i < kBatches of the unit's elements, in the order of
+//   their ids; 0 past the last.
 // meanwhile(): called once, after the maxima are requested and before they are used.
 // emit(i, key): key of the i-th largest element, i < n (0 = the row has fewer).
 // floor: ord_f32 of a value that n elements are known to reach, 0 = none.
-// All threads call it; sm.n_seg, sm.n_elem and sm.bound need not be set.
-// HELD: maxima a thread holds in registers; up to HELD * kSelThreads segments are read once, more are read twice.
-template <int HELD, typename Segs, typename Meanwhile, typename Emit>
-__device__ __forceinline__ void select_top(SelectSmem& sm, int segs, int n, uint32_t floor, const Segs& sg,
+// All threads call it; nothing of sm need be set.
+template <int HELD, typename Units, typename Meanwhile, typename Emit>
+__device__ __forceinline__ void select_top(SelectSmem& sm, int units, int n, uint32_t floor, const Units& un,
                                            Meanwhile meanwhile, Emit emit) {
-    constexpr int kHeld = HELD;
-    constexpr int kAtOnce = 4;   // segments a warp loads at once
+    constexpr int kAtOnce = 4;  // units a warp loads at once
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    float held[kHeld];
+    float held[HELD];
     auto hold = [&](int base) {  // no branches between the loads
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) held[i] = sg.max(min(base + i * kSelThreads + tid, segs - 1));
+        for (int i = 0; i < HELD; ++i) held[i] = un.max(min(base + i * kSelThreads + tid, units - 1));
     };
     auto held_max = [&](int base, float m) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) m = fmaxf(m, base + i * kSelThreads + tid < segs ? held[i] : neg_inf());
+        for (int i = 0; i < HELD; ++i) m = fmaxf(m, base + i * kSelThreads + tid < units ? held[i] : neg_inf());
         return m;
     };
     hold(0);
     meanwhile();
     float m = held_max(0, neg_inf());
-    for (int base = kHeld * kSelThreads; base < segs; base += kHeld * kSelThreads) {
+    for (int base = HELD * kSelThreads; base < units; base += HELD * kSelThreads) {
         hold(base);
         m = held_max(base, m);
     }
-    const uint32_t mine = tid < segs ? ord_f32(m) : 0u;
-    uint32_t grp = max(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1));
-    grp = max(grp, __shfl_xor_sync(0xFFFFFFFFu, grp, 2));
-    if ((lane & 3) == 0) sm.group[tid >> 2] = grp;
-    if (tid == 0) sm.n_seg = sm.n_elem = 0;
+    const uint32_t mine = tid < units ? ord_f32(m) : 0u;
+    sm.mine[tid] = mine;
+    if (tid == 0) sm.n_unit = sm.n_elem = 0;
+    __syncthreads();
+    uint32_t me = 0u;
+    if (tid < kSelGroups) {
+#pragma unroll
+        for (int i = 0; i < kSelThreads; i += kSelGroups) me = max(me, sm.mine[tid + i]);
+        sm.group[tid] = me;
+    }
     __syncthreads();
     if (tid < kSelGroups) {
-        const uint32_t me = sm.group[tid];
         int above = 0;
 #pragma unroll
         for (int j = 0; j < kSelGroups; j += 4) {
@@ -464,61 +474,101 @@ __device__ __forceinline__ void select_top(SelectSmem& sm, int segs, int n, uint
     __syncthreads();
     const uint32_t bound = sm.bound;
     const float least = unord_f32(bound);  // may be NaN, which nothing is below
-    if (mine >= bound && mine != 0u) {
-        for (int base = 0; base < segs; base += kHeld * kSelThreads) {
-            if (segs > kHeld * kSelThreads) hold(base);
+
+    // Units and elements of ord_f32 `from` or more into the lists; false where a list overflows.
+    auto list = [&](uint32_t from) {
+        if (mine >= from && mine != 0u) {
+            for (int base = 0; base < units; base += HELD * kSelThreads) {
+                if (units > HELD * kSelThreads) hold(base);
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) {
-                const int g = base + i * kSelThreads + tid;
-                if (!(held[i] < least) && g < segs && ord_f32(held[i]) >= bound) {
-                    const int e = atomicAdd(&sm.n_seg, 1);
-                    if (e < kSelSegs) sm.seg[e] = (uint32_t)g;
+                for (int i = 0; i < HELD; ++i) {
+                    const int g = base + i * kSelThreads + tid;
+                    if (!(held[i] < least) && g < units && ord_f32(held[i]) >= from) {
+                        const int e = atomicAdd(&sm.n_unit, 1);
+                        if (e < kSelUnits) sm.unit[e] = (uint32_t)g;
+                    }
                 }
             }
         }
-    }
-    __syncthreads();
-    const int n_seg = sm.n_seg;
-    if (n_seg <= kSelSegs) {
-        for (int i0 = warp; i0 < n_seg; i0 += kSelWarps * kAtOnce) {
-            typename Segs::Item it[kAtOnce];
-#pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                const int i = i0 + u * kSelWarps;
-                if (i < n_seg) it[u] = sg.load((int)sm.seg[i]);
+        __syncthreads();
+        const int n_unit = sm.n_unit;
+        if (n_unit > kSelUnits) return false;
+        auto take = [&](unsigned long long k) {
+            if ((uint32_t)(k >> 32) >= from) {
+                const int e = atomicAdd(&sm.n_elem, 1);
+                if (e < kSelElems) sm.elem[e] = k;
             }
+        };
+        if constexpr (Units::kLane) {
+            if (tid < n_unit) {
+                const int g = (int)sm.unit[tid];
+                un.each(un.load(g), g, least, take);
+            }
+        } else {
+            for (int i0 = warp; i0 < n_unit; i0 += kSelWarps * kAtOnce) {
+                typename Units::Item it[kAtOnce];
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                const int i = i0 + u * kSelWarps;
-                if (i < n_seg && ord_f32(sg.peak(it[u])) >= bound)
-                    sg.each(it[u], (int)sm.seg[i], least, [&](unsigned long long k) {
-                        if ((uint32_t)(k >> 32) >= bound) {
-                            const int e = atomicAdd(&sm.n_elem, 1);
-                            if (e < kSelElems) sm.elem[e] = k;
-                        }
-                    });
+                for (int u = 0; u < kAtOnce; ++u) {
+                    const int i = i0 + u * kSelWarps;
+                    if (i < n_unit) it[u] = un.load((int)sm.unit[i]);
+                }
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
+                    const int i = i0 + u * kSelWarps;
+                    if (i < n_unit && ord_f32(un.peak(it[u])) >= from) un.each(it[u], (int)sm.unit[i], least, take);
+                }
             }
         }
         __syncthreads();
-        const int m2 = sm.n_elem;
-        if (m2 <= kSelElems) {
-            if (tid < m2) {
-                const unsigned long long k = sm.elem[tid];
-                int above = 0;
+        return sm.n_elem <= kSelElems;
+    };
+    auto emit_listed = [&](int m2) {
+        for (int e = tid; e < m2; e += kSelThreads) {
+            const unsigned long long k = sm.elem[e];
+            int above = 0;
 #pragma unroll 8
-                for (int j = 0; j < m2; ++j) above += sm.elem[j] > k;
-                if (above < n) emit(above, k);
-            } else if (tid < n) {
-                emit(tid, 0ull);  // fewer elements than n
-            }
-            return;
+            for (int j = 0; j < m2; ++j) above += sm.elem[j] > k;
+            if (above < n) emit(above, k);
         }
+    };
+
+    if (list(bound)) {
+        const int m2 = sm.n_elem;
+        emit_listed(m2);
+        if (tid >= m2 && tid < n) emit(tid, 0ull);  // fewer elements than n
+        return;
     }
-    // Sorted lists.
+    __syncthreads();
+    if (tid == 0) sm.n_unit = sm.n_elem = 0;
+    __syncthreads();
+    if (list(bound + 1u)) {
+        const int m2 = sm.n_elem;
+        emit_listed(m2);
+        if (m2 >= n || warp != 0) return;
+        int at = m2;
+        for (int g0 = 0; g0 < units && at < n; g0 += 32) {
+            uint32_t some = __ballot_sync(0xFFFFFFFFu, g0 + lane < units && ord_f32(un.max(min(g0 + lane, units - 1))) >= bound);
+            for (; some != 0u && at < n; some &= some - 1u) {
+                const int g = g0 + __ffs(some) - 1;
+#pragma unroll 1
+                for (int j = 0; j < Units::kBatches && at < n; ++j) {
+                    const unsigned long long k = un.key(g, j);
+                    const bool equal = k != 0ull && (uint32_t)(k >> 32) == bound;
+                    const uint32_t who = __ballot_sync(0xFFFFFFFFu, equal);
+                    const int i = at + __popc(who & ((1u << lane) - 1u));
+                    if (equal && i < n) emit(i, k);
+                    at += __popc(who);
+                }
+            }
+        }
+        for (int i = at + lane; i < n; i += 32) emit(i, 0ull);
+        return;
+    }
+    __syncthreads();
     unsigned long long top = 0ull;
-    for (int g = warp * 32; g < segs; g += kSelThreads) {
+    for (int g = warp * 32; g < units; g += kSelThreads) {
         const int gg = g + lane;
-        top_insert(top, gg < segs ? make_key(sg.max(gg), (uint32_t)gg) : 0ull, n);
+        top_insert(top, gg < units ? make_key(un.max(gg), (uint32_t)gg) : 0ull, n);
     }
     sm.sorted[warp][lane] = top;
     __syncthreads();
@@ -528,10 +578,10 @@ __device__ __forceinline__ void select_top(SelectSmem& sm, int segs, int n, uint
     __syncthreads();
     top = 0ull;
     for (int i = warp; i < n; i += kSelWarps) {
-        const unsigned long long kseg = __shfl_sync(0xFFFFFFFFu, best, i);
-        if (kseg == 0ull) break;
+        const unsigned long long k = __shfl_sync(0xFFFFFFFFu, best, i);
+        if (k == 0ull) break;
 #pragma unroll 1
-        for (int j = 0; j < Segs::kBatches; ++j) top_insert(top, sg.key((int)key_gid(kseg), j), n);
+        for (int j = 0; j < Units::kBatches; ++j) top_insert(top, un.key((int)key_gid(k), j), n);
     }
     sm.sorted[warp][lane] = top;
     __syncthreads();
