@@ -15,10 +15,11 @@
 //
 // Epilogue.  An accumulator lane is a head row and a column a hidden row, but
 // a row's softmax runs over head rows.  Each warp turns its 32 x 32 blocks in
-// shared memory (row pitch 36 floats: neither side has bank conflicts) and
-// then lane = hidden row: 32 scores in registers, a running maximum and the
-// sums of Stat per hidden row, kept across tiles.  That costs about 10
-// instructions per score and thread, under a tenth of the MMA time at H = 2048.
+// shared memory and then lane = hidden row: 32 scores in registers, a running
+// maximum and the sums of Stat per hidden row, kept across tiles.  About 10
+// instructions per score: with eight warps the epilogue of a tile is shorter
+// than its MMAs from H = 512 up (584 rows of 65,536 x 256, where it is not:
+// 75 us against 114 us with four warps).
 //
 // Alternatives.  Where they are wanted each block of 32 head rows (a segment)
 // leaves its maximum per hidden row in the workspace, and its 32 scores unless
@@ -53,16 +54,16 @@ constexpr int kGroup = 256;             // hidden rows per row group (MMA N)
 constexpr int kMaxGroups = 4;           // row groups per pass over the head
 constexpr int kPassRows = kGroup * kMaxGroups;
 constexpr int kOneCtaRows = 128;
-constexpr int kThreadsH = 224;
-constexpr int kBoundWarp = 6;
+constexpr int kEpiWarps = 8;            // two per quarter of the TMEM lanes, on alternate blocks of 32 hidden rows
+constexpr int kBoundWarp = 2 + kEpiWarps;
+constexpr int kThreadsH = 32 * (kBoundWarp + 1);
 constexpr int kMaxStages = 8;
 constexpr int kStageW = kTileM * kBlockK * 2;  // 16 KiB
 constexpr int kTmemCols = 512;
 constexpr int kSeg = 32;                // head rows per segment
-constexpr int kPitch = 36;              // floats per hidden row of a transposed block
-constexpr int kTransBytes = 32 * kPitch * 4;  // per epilogue warp
+constexpr int kTransBytes = 32 * 32 * 4;  // a transposed block, per epilogue warp
 constexpr int kMaxParts = 512;          // CTAs that leave statistics of one row
-static_assert(kGroup * 3 * 4 <= kTransBytes, "a warp's statistics fit its block");
+static_assert(kGroup / 2 * 3 * 4 <= kTransBytes, "a warp's statistics fit its block");
 
 struct alignas(8) Bars {
     unsigned long long full[kMaxStages];
@@ -78,7 +79,7 @@ struct alignas(8) Bars {
 struct Args {
     int R;       // hidden rows of this pass
     int Rp;      // row pitch of the workspace arrays
-    int N;       // one CTA: MMA N (R rounded up to 16)
+    int N;       // hidden rows of a row group, rounded up to 16: MMA N
     int H, V;
     int groups;  // row groups (pairs)
     const int32_t* tokens;
@@ -92,8 +93,13 @@ struct Args {
     unsigned int* err;
 };
 
+// A row group: hidden rows [begin, end) of the pass.
+struct Rows {
+    int group, begin, end;
+};
+
 __host__ __device__ constexpr size_t smem_bytes(int stages, int nmax) {
-    return 1024 + (size_t)stages * (kStageW + (size_t)nmax * kBlockK * 2) + sizeof(Bars) + 4 * kTransBytes + 64;
+    return 1024 + (size_t)stages * (kStageW + (size_t)nmax * kBlockK * 2) + sizeof(Bars) + kEpiWarps * kTransBytes + 64;
 }
 
 // ---------------------------------------------------------------------------
@@ -138,19 +144,19 @@ __device__ __forceinline__ uint32_t nth_largest(const float* p, int m, int n) {
 
 // The bounds of a row group, by one warp of each of its n_cta CTAs; `first_segs`: the segments of their first tiles.
 // bounds: the CTA's copy (shared, zero at the start); *done: the CTA's epilogue has finished.
-__device__ __forceinline__ void find_bounds(const Args& a, int row0, int cta, int n_cta, int first_segs,
+__device__ __forceinline__ void find_bounds(const Args& a, const Rows& rw, int cta, int n_cta, int first_segs,
                                             volatile uint32_t* bounds, volatile uint32_t* done) {
     first_segs = min(first_segs, kFirstSegs);
     // no later tiles (this CTA's, at least), or too few maxima
     if (a.seg_max == nullptr || first_segs >= a.segs || first_segs < kMinFirstSegs) return;
     const int lane = threadIdx.x & 31;
-    const int rows = min(kGroup, a.R - row0);
-    volatile uint32_t* seen = a.seen + row0 / kGroup;
+    const int row0 = rw.begin, rows = rw.end - rw.begin;
+    volatile uint32_t* seen = a.seen + rw.group;
     volatile uint32_t* shared = a.bound + row0;
     bool all = false;
     for (int i = 0; i < kTries && !all && *done == 0u; ++i) {
         if (i > 0) __nanosleep(kTryNs);
-        all = __shfl_sync(0xFFFFFFFFu, lane == 0 ? *seen : 0u, 0) == 4u * (uint32_t)n_cta;
+        all = __shfl_sync(0xFFFFFFFFu, lane == 0 ? *seen : 0u, 0) == (uint32_t)(kEpiWarps * n_cta);
     }
     if (!all) return;
     __threadfence();
@@ -172,55 +178,61 @@ __device__ __forceinline__ void find_bounds(const Args& a, int row0, int cta, in
 }
 
 // ---------------------------------------------------------------------------
-// Epilogue of one warp: NG groups of 32 hidden rows (row = row0 + 32 g + lane).
+// Epilogue of one warp: blocks `half`, half + 2, ... of 32 hidden rows (row = begin + 32 block + lane), NB at most.
+// A block is turned in shared memory; 16-byte pieces of hidden row j lie at piece p ^ (j % 8), so that the rows are
+// written (lane = head row) and read (lane = hidden row, four floats) without bank conflicts.
 
-template <int NG>
+template <int NB>
 struct Epilogue {
-    Stat st[NG];
-    int tok[NG];
+    Stat st[NB];
+    int tok[NB];
     float* tr;
+    int half;
     volatile uint32_t* bounds;  // of the row group's rows
 
-    __device__ __forceinline__ void begin(const Args& a, int row0, float* tr_, volatile uint32_t* bounds_) {
+    __device__ __forceinline__ static int place(int j, int c) { return j * 32 + ((((c >> 2) ^ j) & 7) << 2 | (c & 3)); }
+
+    __device__ __forceinline__ void begin(const Args& a, const Rows& rw, float* tr_, int half_, volatile uint32_t* bounds_) {
         tr = tr_;
+        half = half_;
         bounds = bounds_;
         const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const int row = row0 + g * 32 + lane;
-            st[g] = stat_none();
-            tok[g] = (a.tokens != nullptr && row < a.R) ? a.tokens[row] : -1;
+        for (int k = 0; k < NB; ++k) {
+            const int row = rw.begin + (2 * k + half) * 32 + lane;
+            st[k] = stat_none();
+            tok[k] = (a.tokens != nullptr && row < rw.end) ? a.tokens[row] : -1;
         }
     }
 
     // After the warp's first tile: its maxima are there (see find_bounds).
-    __device__ __forceinline__ void first_done(const Args& a, int row0) {
+    __device__ __forceinline__ void first_done(const Args& a, const Rows& rw) {
         if (a.seg_max == nullptr) return;
         __threadfence();
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) atomicAdd(a.seen + row0 / kGroup, 1u);
+        if ((threadIdx.x & 31) == 0) atomicAdd(a.seen + rw.group, 1u);
     }
 
-    // v[j]: the score of head row v0 + lane for column j of group g.
-    __device__ __forceinline__ void block(const Args& a, int g, int row0, int v0, const float (&v)[32]) {
+    // v[j]: the score of head row v0 + lane for hidden row j of this warp's k-th block.
+    __device__ __forceinline__ void block(const Args& a, const Rows& rw, int k, int v0, const float (&v)[32]) {
         const int lane = threadIdx.x & 31;
+        const int in_group = (2 * k + half) * 32 + lane, row = rw.begin + in_group;
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) tr[j * kPitch + lane] = v[j];
+        for (int j = 0; j < 32; ++j) tr[place(j, lane)] = v[j];
         __syncwarp();
         float x[32];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float4 q = *reinterpret_cast<const float4*>(tr + lane * kPitch + 4 * i);
+            const float4 q = *reinterpret_cast<const float4*>(tr + place(lane, 4 * i));
             x[4 * i] = q.x;
             x[4 * i + 1] = q.y;
             x[4 * i + 2] = q.z;
             x[4 * i + 3] = q.w;
         }
-        const int row = row0 + g * 32 + lane;
         const int n = a.V - v0;  // head rows of this block
-        const unsigned int at = (unsigned int)(tok[g] - v0);
-        if (at < 32u && (int)at < n && row < a.R) a.tok_score[row] = tr[lane * kPitch + at];
+        const unsigned int at = (unsigned int)(tok[k] - v0);
+        if (at < 32u && (int)at < n && row < rw.end) a.tok_score[row] = tr[place(lane, (int)at)];
         if (n < 32) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -231,17 +243,17 @@ struct Epilogue {
         for (int i = 0; i < 32; ++i) m = fmaxf(m, x[i]);
         if (a.seg_max != nullptr) {
             const int seg = v0 / kSeg;
-            if (row < a.R && vh_guard(seg < a.segs, a.err)) a.seg_max[(size_t)row * a.segs + seg] = m;
+            if (row < rw.end && vh_guard(seg < a.segs, a.err)) a.seg_max[(size_t)row * a.segs + seg] = m;
             // rows whose scores are kept: 128 bytes each, lane = head row again
-            const uint32_t keep = __ballot_sync(0xFFFFFFFFu, row < a.R && ord_f32(m) >= bounds[g * 32 + lane]);
-            float* p = a.scores + ((size_t)seg * a.Rp + row0 + g * 32) * kSeg + lane;
+            const uint32_t keep = __ballot_sync(0xFFFFFFFFu, row < rw.end && ord_f32(m) >= bounds[in_group]);
+            float* p = a.scores + ((size_t)seg * a.Rp + row - lane) * kSeg + lane;
             if (keep != 0u) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     if ((keep >> j) & 1u) p[j * kSeg] = v[j];
             }
         }
-        Stat2 run{st[g].c, f2(st[g].s, 0.f), f2(st[g].t, 0.f)};
+        Stat2 run{st[k].c, f2(st[k].s, 0.f), f2(st[k].t, 0.f)};
         run.raise(m);
         if (run.c > kLiftFrom && run.c < kNearLimit) {
             const F2 mcl = run.minus_cl();
@@ -251,33 +263,57 @@ struct Epilogue {
 #pragma unroll
             for (int i = 0; i < 32; i += 2) run.add(x[i], x[i + 1]);
         }
-        st[g] = run.get();
+        st[k] = run.get();
     }
 
-    // The warp's statistics of every hidden row, for the CTA to join.
+    // The accumulators of one tile, of whose 32 lanes (`taddr`: the first one's) lane 0 is head row v0; `free` hands
+    // them back once this warp has read its blocks of them.
+    template <typename Free>
+    __device__ __forceinline__ void tile(const Args& a, const Rows& rw, uint32_t taddr, int v0, Free free) {
+        const int blocks = (a.N + 31) / 32;
+        if (half >= blocks) free();
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            const int g = 2 * k + half;
+            if (g < blocks) {
+                float v[32];
+                tmem_ld32(taddr + g * 32u, v);
+                if (g + 2 >= blocks) free();
+                if (v0 < a.V && rw.begin + g * 32 < rw.end) block(a, rw, k, v0, v);
+            }
+        }
+    }
+
+    // The warp's statistics of its hidden rows, for the CTA to join.
     __device__ __forceinline__ void leave() {
         const int lane = threadIdx.x & 31;
         __syncwarp();
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            float* p = tr + (g * 32 + lane) * 3;
-            p[0] = st[g].c;
-            p[1] = st[g].s;
-            p[2] = st[g].t;
+        for (int k = 0; k < NB; ++k) {
+            float* p = tr + (k * 32 + lane) * 3;
+            p[0] = st[k].c;
+            p[1] = st[k].s;
+            p[2] = st[k].t;
         }
     }
 };
 
-// After __syncthreads: join the four warps' statistics of rows row0 .. row0 + n.
-__device__ __forceinline__ void publish(const Args& a, const float* trans, int slot, int row0, int n) {
-    for (int r = threadIdx.x; r < n; r += blockDim.x) {
+// The transposition buffer of the epilogue warp of a lane quarter and a half of the blocks.
+__device__ __forceinline__ float* trans_of(float* trans, int quarter, int half) {
+    return trans + (half * 4 + quarter) * (kTransBytes / 4);
+}
+
+// After __syncthreads: join the four quarters' statistics of the group's rows.
+__device__ __forceinline__ void publish(const Args& a, const Rows& rw, float* trans, int slot) {
+    for (int r = threadIdx.x; r < rw.end - rw.begin; r += blockDim.x) {
+        const int g = r >> 5;
         Stat s = stat_none();
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const float* p = trans + w * (kTransBytes / 4) + r * 3;
+            const float* p = trans_of(trans, w, g & 1) + ((g >> 1) * 32 + (r & 31)) * 3;
             s = stat_join(s, Stat{p[0], p[1], p[2]});
         }
-        a.part[(size_t)slot * a.Rp + row0 + r] = make_float4(s.c, s.s, s.t, 0.f);
+        a.part[(size_t)slot * a.Rp + rw.begin + r] = make_float4(s.c, s.s, s.t, 0.f);
     }
 }
 
@@ -300,25 +336,26 @@ __device__ __forceinline__ void init_bars(Bars* b, int stages, int empty_arrival
 
 // ---------------------------------------------------------------------------
 // Up to 128 hidden rows: one CTA per tile.  Warp 0 = TMA producer, warp 1 =
-// TMEM owner and MMA issuer, warps 2..5 = epilogue (TMEM lane quarter = warp % 4),
-// warp 6 = the alternatives' bounds.
+// TMEM owner and MMA issuer, warps 2..9 = epilogue (TMEM lane quarter = warp % 4),
+// warp 10 = the alternatives' bounds.
 
 template <int STAGES, int NMAX>
 __global__ void __launch_bounds__(kThreadsH, 1)
     k_head_logprobs(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a) {
     constexpr int kStageX = NMAX * kBlockK * 2;
-    constexpr int NG = NMAX / 32;
+    constexpr int NB = (NMAX / 32 + 1) / 2;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* stage_w = smem;
     uint8_t* stage_x = smem + (size_t)STAGES * kStageW;
     float* trans = reinterpret_cast<float*>(stage_x + (size_t)STAGES * kStageX);
-    Bars* bars = reinterpret_cast<Bars*>(reinterpret_cast<uint8_t*>(trans) + 4 * kTransBytes);
+    Bars* bars = reinterpret_cast<Bars*>(reinterpret_cast<uint8_t*>(trans) + kEpiWarps * kTransBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int k_stages = (a.H + kBlockK - 1) / kBlockK;  // TMA fills past H with zeros
     const int n_tiles = (a.V + kTileM - 1) / kTileM;
 
-    init_bars(bars, STAGES, 4);
+    const Rows rw{0, 0, a.R};
+    init_bars(bars, STAGES, kEpiWarps);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&bars->tmem_base)),
@@ -390,33 +427,23 @@ __global__ void __launch_bounds__(kThreadsH, 1)
         }
     } else if (warp == kBoundWarp) {
         rows_wait();
-        find_bounds(a, 0, blockIdx.x, gridDim.x, (int)gridDim.x * (kTileM / kSeg), bars->bounds, &bars->done);
+        find_bounds(a, rw, blockIdx.x, gridDim.x, (int)gridDim.x * (kTileM / kSeg), bars->bounds, &bars->done);
     } else {
         rows_wait();
-        const int quarter = warp & 3;
-        Epilogue<NG> ep;
-        ep.begin(a, 0, trans + quarter * (kTransBytes / 4), bars->bounds);
-        const int ngroups = (a.N + 31) / 32;
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        Epilogue<NB> ep;
+        ep.begin(a, rw, trans_of(trans, quarter, half), half, bars->bounds);
         uint32_t local = 0;
         for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x, ++local) {
             const uint32_t buf = local & 1u;
             if (!mbar_wait(&bars->tmem_full[buf], (local >> 1) & 1u, a.err)) break;
             tc_fence_after();
-            const int v0 = tile * kTileM + quarter * 32;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                if (g < ngroups) {
-                    float v[32];
-                    tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * 256u + g * 32u, v);
-                    if (g + 1 == ngroups) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars->tmem_empty[buf]);
-                    }
-                    if (v0 < a.V) ep.block(a, g, 0, v0, v);
-                }
-            }
-            if (local == 0) ep.first_done(a, 0);
+            ep.tile(a, rw, tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * 256u, tile * kTileM + quarter * 32, [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->tmem_empty[buf]);
+            });
+            if (local == 0) ep.first_done(a, rw);
         }
         ep.leave();
         *const_cast<volatile uint32_t*>(&bars->done) = 1u;
@@ -429,7 +456,7 @@ __global__ void __launch_bounds__(kThreadsH, 1)
                      : "memory");
     }
     rows_wait();
-    publish(a, trans, blockIdx.x, 0, a.R);
+    publish(a, rw, trans, blockIdx.x);
 }
 
 // ---------------------------------------------------------------------------
@@ -448,17 +475,18 @@ __global__ void __launch_bounds__(kThreadsH, 1)
     uint8_t* stage_w = smem;
     uint8_t* stage_x = smem + (size_t)kStages2 * kStageW;
     float* trans = reinterpret_cast<float*>(stage_x + (size_t)kStages2 * kStageX2);
-    Bars* bars = reinterpret_cast<Bars*>(reinterpret_cast<uint8_t*>(trans) + 4 * kTransBytes);
+    Bars* bars = reinterpret_cast<Bars*>(reinterpret_cast<uint8_t*>(trans) + kEpiWarps * kTransBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1;
-    const int row0 = (pair % a.groups) * kGroup;             // first hidden row of the row group
+    const int group = pair % a.groups, row0 = group * a.N;
+    const Rows rw{group, row0, min(row0 + a.N, a.R)};
     const int tile0 = pair / a.groups, step = (int)(gridDim.x >> 1) / a.groups;
     const int n_tiles = (a.V + kPairTile - 1) / kPairTile;
     const int k_stages = (a.H + kBlockK - 1) / kBlockK;
 
-    init_bars(bars, kStages2, 8);  // four epilogue warps in each CTA
+    init_bars(bars, kStages2, 2 * kEpiWarps);  // of both CTAs
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&bars->tmem_base)),
@@ -480,7 +508,7 @@ __global__ void __launch_bounds__(kThreadsH, 1)
             auto load_x = [&](uint32_t j) {
                 const int s = j % kStages2;
                 tma_load_2d_pair(stage_x + (size_t)s * kStageX2, &map_x, map_to_rank(smem_u32(&bars->full[s]), 0),
-                                 (int)(j % k_stages) * kBlockK, row0 + (int)rank * 128, pol_x);
+                                 (int)(j % k_stages) * kBlockK, row0 + (int)rank * (a.N / 2), pol_x);
             };
             auto release_first_ring = [&](uint32_t n) {
                 rows_wait();
@@ -492,7 +520,7 @@ __global__ void __launch_bounds__(kThreadsH, 1)
                 for (int ks = 0; ks < k_stages; ++ks, ++it) {
                     const int s = it % kStages2;
                     if (!mbar_wait(&bars->empty[s], ((it / kStages2) & 1u) ^ 1u, a.err)) { ok = false; break; }
-                    if (leader) mbar_arrive_expect_tx(&bars->full[s], 2u * (uint32_t)(kStageW + kStageX2));
+                    if (leader) mbar_arrive_expect_tx(&bars->full[s], 2u * kStageW + (uint32_t)(a.N * kBlockK * 2));
                     tma_load_2d_pair(stage_w + (size_t)s * kStageW, &map_w, map_to_rank(smem_u32(&bars->full[s]), 0),
                                      ks * kBlockK, tile * kPairTile + (int)rank * kTileM, pol_w);
                     if (waited)
@@ -508,7 +536,7 @@ __global__ void __launch_bounds__(kThreadsH, 1)
         }
     } else if (warp == 1) {
         if (lane == 0 && leader) {
-            const uint32_t idesc = idesc_bf16(kPairTile, kGroup);
+            const uint32_t idesc = idesc_bf16(kPairTile, a.N);
             uint32_t it = 0, local = 0;
             bool ok = true;
             for (int tile = tile0; tile < n_tiles && ok; tile += step, ++local) {
@@ -534,12 +562,12 @@ __global__ void __launch_bounds__(kThreadsH, 1)
         }
     } else if (warp == kBoundWarp) {
         rows_wait();
-        find_bounds(a, row0, tile0 * 2 + (int)rank, step * 2, step * (kPairTile / kSeg), bars->bounds, &bars->done);
+        find_bounds(a, rw, tile0 * 2 + (int)rank, step * 2, step * (kPairTile / kSeg), bars->bounds, &bars->done);
     } else {
         rows_wait();
-        const int quarter = warp & 3;
-        Epilogue<kGroup / 32> ep;
-        ep.begin(a, row0, trans + quarter * (kTransBytes / 4), bars->bounds);
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        Epilogue<kGroup / 64> ep;
+        ep.begin(a, rw, trans_of(trans, quarter, half), half, bars->bounds);
         const uint32_t empty0 = map_to_rank(smem_u32(&bars->tmem_empty[0]), 0);
         const uint32_t empty1 = map_to_rank(smem_u32(&bars->tmem_empty[1]), 0);
         uint32_t local = 0;
@@ -547,19 +575,13 @@ __global__ void __launch_bounds__(kThreadsH, 1)
             const uint32_t buf = local & 1u;
             if (!mbar_wait(&bars->tmem_full[buf], (local >> 1) & 1u, a.err)) break;
             tc_fence_after();
-            const int v0 = tile * kPairTile + (int)rank * kTileM + quarter * 32;
-#pragma unroll
-            for (int g = 0; g < kGroup / 32; ++g) {
-                float v[32];
-                tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * 256u + g * 32u, v);
-                if (g + 1 == kGroup / 32) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(buf ? empty1 : empty0);
-                }
-                if (v0 < a.V && row0 + g * 32 < a.R) ep.block(a, g, row0, v0, v);
-            }
-            if (local == 0) ep.first_done(a, row0);
+            ep.tile(a, rw, tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * 256u,
+                    tile * kPairTile + (int)rank * kTileM + quarter * 32, [&] {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(buf ? empty1 : empty0);
+                    });
+            if (local == 0) ep.first_done(a, rw);
         }
         ep.leave();
         *const_cast<volatile uint32_t*>(&bars->done) = 1u;
@@ -573,7 +595,7 @@ __global__ void __launch_bounds__(kThreadsH, 1)
                      : "memory");
     }
     rows_wait();
-    publish(a, trans, tile0 * 2 + (int)rank, row0, min(kGroup, a.R - row0));
+    publish(a, rw, trans, tile0 * 2 + (int)rank);
 }
 
 // ---------------------------------------------------------------------------
@@ -769,8 +791,11 @@ static cudaError_t pass(const HeadLogprobArgs& h, int r0, int nr, cudaStream_t s
         e = a.N <= 64 ? launch_tc(k_head_logprobs<8, 64>, n_parts, smem_bytes(8, 64), 1, s, mw, mx, a)
                       : launch_tc(k_head_logprobs<6, 128>, n_parts, smem_bytes(6, 128), 1, s, mw, mx, a);
     } else {
+        // groups of even size: the MMA's time goes with N (369 rows of 137,667 x 2560: 219 us in two groups of 192, 237 us
+        // in groups of 256)
         a.groups = (nr + kGroup - 1) / kGroup;
-        if (!make_map(&mx, x, nr, h.H, 128)) return cudaErrorNotSupported;
+        a.N = ((nr + a.groups - 1) / a.groups + 15) / 16 * 16;
+        if (!make_map(&mx, x, nr, h.H, a.N / 2)) return cudaErrorNotSupported;
         const int pairs = resident_pairs();
         const int tiles = (int)(((long long)h.V + kPairTile - 1) / kPairTile);
         const int per = std::min({pairs / a.groups, tiles, kMaxParts / 2});  // pairs of one row group
