@@ -496,9 +496,10 @@ VH_API vh_status vh_logits_logprobs_grad(const void* logits, int dtype, int R, i
 
 /* Workspace of vh_head_logprobs: 16-byte aligned, its first 8,192 bytes zeroed
  * once by the caller (every call leaves them zero but for the error word, see
- * vh_workspace_error_offset; zero them again after an error); about 4 * V bytes per row (up to 1,024 rows) when alternatives are wanted.  A
- * buffer serves calls of any sizes that need no more bytes.  0 for a size out
- * of range. */
+ * vh_workspace_error_offset; zero them again after an error); about 4 * V
+ * bytes per row (up to 1,024 rows) when alternatives are wanted.  A buffer
+ * serves calls of any sizes that need no more bytes.  0 for a size out of
+ * range. */
 VH_API size_t vh_head_logprobs_workspace_bytes(int R, int V, int top_n);
 
 /*

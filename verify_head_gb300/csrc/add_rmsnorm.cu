@@ -18,8 +18,8 @@
 
 #include <algorithm>
 
-#include "vh_kernels.h"
 #include "vh_ptx.cuh"
+#include "vh_row_kernels.h"
 #include "vh_rows.cuh"
 
 namespace vh {
@@ -30,6 +30,23 @@ constexpr int kWideThreads = 512;
 constexpr int kMaxRing = 4;                // tokens in flight per CTA of the gradient
 constexpr size_t kRingBytes = 56 * 1024;   // of shared memory per CTA that a ring of over two tokens stays below
 constexpr size_t kSmRingBytes = 220 * 1024;  // of shared memory per SM for rings
+
+// Bounded wait for a barrier's phase: whether it completed.
+__device__ __forceinline__ bool mbar_done(unsigned long long* bar, uint32_t parity) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = ptx::globaltimer();
+    while (!ptx::mbar_try_wait(bar, parity))
+        if (ptx::globaltimer() - t0 > ptx::kTimeoutNs) return false;
+    return true;
+}
+
+// 1-D copy global -> shared that completes on an mbarrier (both addresses and the size multiples of 16 bytes).
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, unsigned long long* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     ptx::smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+                 : "memory");
+}
 
 // Sums of two values over the threads of one row: wpr warps, of which this is number w; `row`: the row's wpr slots in
 // shared memory.  MAX_SECOND: the second value is a maximum instead of a sum.  sync(): a barrier of all threads that
@@ -313,7 +330,7 @@ __device__ __forceinline__ uint32_t fill_granules(uint8_t* to, const T* p, uint3
     window(b, bytes, first, last, lo, hi);
     if (bar != nullptr) {
         if (hi > lo)
-            ptx::bulk_copy(to + (lo - (b & ~uintptr_t(15))), reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo), bar);
+            bulk_copy(to + (lo - (b & ~uintptr_t(15))), reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo), bar);
     } else if (first || last) {
         T* at = reinterpret_cast<T*>(to + (b & 15));
         const int n = (int)(bytes / sizeof(T));
@@ -353,16 +370,16 @@ __global__ void __launch_bounds__(kMaxThreads + 32) k_norm_grad(const NormGradAr
         const T* dy = static_cast<const T*>(a.dy);
         const T* dh = static_cast<const T*>(a.dh);
         for (int i = 0, s = 0, ph = 1; i < n; ++i) {
-            if (!ptx::mbar_drain(&empty[s], ph)) return;
+            if (!mbar_done(&empty[s], ph)) return;
             const long long t0 = (blockIdx.x + (long long)i * gridDim.x) * ty;
             const int m = (int)min((long long)ty, a.T - t0);
             uint8_t* to = ring + (size_t)s * place;
             if constexpr (VEC > 1) {
                 ptx::mbar_arrive_expect_tx(&full[s], (dh != nullptr ? 3u : 2u) * m * row_bytes);
                 for (int q = 0; q < m; ++q, to += 3 * pitch) {
-                    ptx::bulk_copy(to, h + (t0 + q) * a.h_stride, row_bytes, &full[s]);
-                    ptx::bulk_copy(to + pitch, dy + (t0 + q) * a.dy_stride, row_bytes, &full[s]);
-                    if (dh != nullptr) ptx::bulk_copy(to + 2 * pitch, dh + (t0 + q) * a.dh_stride, row_bytes, &full[s]);
+                    bulk_copy(to, h + (t0 + q) * a.h_stride, row_bytes, &full[s]);
+                    bulk_copy(to + pitch, dy + (t0 + q) * a.dy_stride, row_bytes, &full[s]);
+                    if (dh != nullptr) bulk_copy(to + 2 * pitch, dh + (t0 + q) * a.dh_stride, row_bytes, &full[s]);
                 }
             } else {
                 auto rows = [&](unsigned long long* bar) {
@@ -410,7 +427,7 @@ __global__ void __launch_bounds__(kMaxThreads + 32) k_norm_grad(const NormGradAr
         const T* hs = at(pl, a.h, a.h_stride);
         const T* ys = at(pl + pitch, a.dy, a.dy_stride);
         const T* es = at(pl + 2 * pitch, a.dh, a.dh_stride);
-        const bool there = ptx::mbar_drain(&full[s], ph);
+        const bool there = mbar_done(&full[s], ph);
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {

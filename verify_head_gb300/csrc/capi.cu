@@ -9,6 +9,7 @@
 
 #include "../../include/verifyhead.h"
 #include "vh_kernels.h"
+#include "vh_row_kernels.h"
 #include "vh_verify.h"
 
 namespace {

@@ -33,6 +33,7 @@
 #include <atomic>
 
 #include "vh_kernels.h"
+#include "vh_row_kernels.h"
 #include "vh_rows.cuh"
 #include "vh_tc.cuh"
 

@@ -18,7 +18,7 @@
 // Bound: memory (the logits once; the gradient also writes them once).
 #include <algorithm>
 
-#include "vh_kernels.h"
+#include "vh_row_kernels.h"
 #include "vh_rows.cuh"
 
 namespace vh {
@@ -26,9 +26,9 @@ namespace lp {
 
 constexpr int kThreadsL = kSelThreads;
 constexpr int kWarpsL = kThreadsL / 32;
-constexpr int kUnroll = 2;             // segments in flight per warp (and two more requested)
-// CTAs per SM.  Four for statistics alone (2048 x 65536 bf16: 45.2 against 47.4 us with three); with alternatives
-// the rows are few and three, with more registers each, are faster (129 x 40001 fp16: 18.4 against 19.2 us).
+constexpr int kUnroll = 2;             // segments in flight per warp (and two more requested); three: 50.1 us for the same
+// CTAs per SM.  Four for statistics alone (2048 x 65536 bf16: 46.9 against 48.1 us with three); with alternatives
+// the rows are few and three, with more registers each, are faster (129 x 40001 fp16, 5 of them: 12.7 against 13.2 us).
 constexpr int kPerSm = 4, kPerSmTop = 3;
 constexpr int kTargetCtas = 152 * kPerSm;
 constexpr int kMinSegs = 2 * kWarpsL;  // segments per CTA below which the work is not cut further

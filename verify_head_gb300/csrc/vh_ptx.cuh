@@ -73,14 +73,11 @@ __device__ __forceinline__ bool mbar_wait(unsigned long long* bar, uint32_t pari
 }
 
 // Bounded wait that ignores the error word (draining in-flight copies or
-// MMAs before the CTA releases its shared memory / TMEM).  Whether the phase
-// completed.
-__device__ __forceinline__ bool mbar_drain(unsigned long long* bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
+// MMAs before the CTA releases its shared memory / TMEM).
+__device__ __forceinline__ void mbar_drain(unsigned long long* bar, uint32_t parity) {
     const unsigned long long t0 = globaltimer();
     while (!mbar_try_wait(bar, parity))
-        if (globaltimer() - t0 > kTimeoutNs) return false;
-    return true;
+        if (globaltimer() - t0 > kTimeoutNs) return;
 }
 
 // 1-D bulk copy global -> shared, completing on an mbarrier (bytes % 16 == 0,
@@ -92,14 +89,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
             "r"(smem_u32(dst)),
         "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
-}
-
-// The same without a cache hint.
-__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, unsigned long long* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
 }
 
 __device__ __forceinline__ unsigned long long policy_evict_first() {
