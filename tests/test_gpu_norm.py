@@ -311,3 +311,91 @@ def test_refusals(vh):
         vh.add_rmsnorm_grad(x, x, torch.zeros(8, device="cuda"), dx=torch.zeros(2, 8, device="cuda", dtype=BF))
     with pytest.raises(vh.VHError):
         vh.add_rmsnorm_grad(x, x, torch.zeros(8, device="cuda"), ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+
+
+def outside_unchanged(t, before):
+    """Nothing beside the rows of t was written."""
+    whole = torch.empty(0, dtype=t.dtype, device="cuda").set_(t.untyped_storage())
+    mask = torch.ones_like(whole, dtype=torch.bool)
+    mask.as_strided(t.shape, t.stride(), t.storage_offset()).fill_(False)
+    return torch.equal(whole.view(torch.uint8 if t.element_size() == 1 else t.dtype)[mask], before[mask])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("H,pitch,offset", [(1, 1, 3), (3, 5, 1), (9, 9, 7), (255, 255, 5), (520, 521, 2), (2561, 2561, 7),
+                                            (4105, 4107, 1), (8185, 8185, 6), (16369, 16371, 3), (16383, 16383, 1)])
+@pytest.mark.parametrize("w32", [False, True])
+def test_rows_that_lie_alike(vh, dtype, H, pitch, offset, w32):
+    """Rows of any alignment, the same for every tensor: 16-byte slots across the rows' ends, weights at an offset."""
+    T = 9
+    g = gen(H + pitch + offset)
+    x, r = (rows(g, T, H, dtype, s, pitch=pitch, offset=offset) for s in (1.0, 2.0))
+    w = torch.randn(H + 3, generator=g).to(F32 if w32 else dtype).cuda()[3:]
+    want_y, want_h = norm64(x, r, w, 1e-6, 0.0)
+    y, h = (rows(g, T, H, dtype, pitch=pitch, offset=offset) for _ in range(2))
+    whole = [torch.empty(0, dtype=dtype, device="cuda").set_(t.untyped_storage()).clone() for t in (y, h)]
+    vh.add_rmsnorm(x, r, w, 1e-6, y=y, h=h)
+    close(h, want_h, U[dtype] * (1 + 2 ** -10) + 2.0 ** -24, TINY[dtype])
+    close(y, want_y, U[dtype] * (1 + 2 ** -10) + sums(H), TINY[dtype])
+    assert outside_unchanged(y, whole[0]) and outside_unchanged(h, whole[1])
+    # the same values wherever the rows lie, up to the order of the squares' sum
+    apart = vh.add_rmsnorm(x.contiguous(), r.contiguous(), w, 1e-6)
+    assert torch.equal(h, apart[1])
+    close(y, apart[0].double(), 2 * U[dtype] * (1 + 2 ** -10) + sums(H), TINY[dtype])
+    # codes
+    flat = torch.full((T * pitch + offset + 16,), 77, dtype=torch.int8, device="cuda")
+    before = flat.clone()
+    q = flat[offset:offset + T * pitch].view(T, pitch)[:, :H]
+    _, s, _ = vh.add_rmsnorm_q8(x, r, w, 1e-6, q=q, h=h)
+    u = (x.float() + r.float()) * w.float()
+    assert torch.equal(q, torch.round(u * (127.0 / u.abs().amax(1, keepdim=True))).to(torch.int8))
+    assert outside_unchanged(q, before)
+    close(s, want_y.abs().max(1).values / 127.0, sums(H), 0.0)
+    # outputs on the inputs: a slot that two rows share is written by both
+    vh.add_rmsnorm(x, r, w, 1e-6, y=x, h=r)
+    assert torch.equal(x, y) and torch.equal(r, h)
+
+
+def test_grad_and_norm_of_ragged_batch(vh):
+    """Many rows of an odd width, no residual, no weights."""
+    g = gen(5)
+    x = rows(g, 3001, 1027, HF)
+    y = vh.add_rmsnorm(x, None, None, 1e-6)[0]
+    close(y, norm64(x, None, None, 1e-6, 0.0)[0], U[HF] * (1 + 2 ** -10) + sums(1027), TINY[HF])
+
+
+def grad_close(dx, dw, want_dx, want_dw, dy, h, w, dtype):
+    """The bounds of test_grad_matches_formula."""
+    T, H = h.shape
+    hd, gd = h.double(), dy.double() * w.double()
+    rstd = 1 / torch.sqrt((hd * hd).mean(1, keepdim=True) + 1e-6)
+    n = hd * rstd
+    size = rstd * (gd.abs() + n.abs() * (gd * n).abs().mean(1, keepdim=True))
+    close(dx, want_dx, U[dtype] * (1 + 2 ** -10) + 2.0 ** -24, size * sums(H) * 2 + TINY[dtype])
+    close(dw, want_dw, 2.0 ** -24, (dy.double() * n).abs().sum(0) * (T / 152 + 80 + sums(H) * 2 ** 24) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("T,H,pitch,offset", [(1, 1, 1, 3), (5, 3, 5, 1), (9, 9, 9, 7), (700, 255, 255, 5), (7, 520, 522, 2),
+                                              (4999, 129, 129, 1), (1301, 2561, 2561, 7), (17, 4105, 4108, 1),
+                                              (650, 8185, 8185, 6), (3, 16369, 16371, 3)])
+@pytest.mark.parametrize("dh", [False, True])
+def test_grad_of_rows_that_lie_alike(vh, dtype, T, H, pitch, offset, dh):
+    """Rows of any alignment, the same for every tensor; rows shorter than their slot's rest; nothing else is written."""
+    g = gen(T + H + offset)
+    dy, h, e = (rows(g, T, H, dtype, pitch=pitch, offset=offset) for _ in range(3))
+    for t in (dy, h, e):  # what lies beside the rows is no number
+        whole = torch.empty(0, dtype=dtype, device="cuda").set_(t.untyped_storage())
+        mask = torch.ones_like(whole, dtype=torch.bool)
+        mask.as_strided((T, H), (pitch, 1), offset).fill_(False)
+        whole[mask] = float("nan")
+    w = torch.randn(H + 1, generator=g).to(dtype).cuda()[1:]
+    dx = rows(g, T, H, dtype, pitch=pitch, offset=offset)
+    before = torch.empty(0, dtype=dtype, device="cuda").set_(dx.untyped_storage()).clone()
+    _, dw = vh.add_rmsnorm_grad(dy, h, w, 1e-6, dh=e if dh else None, dx=dx)
+    want_dx, want_dw = norm_grad64(dy, h, w, e if dh else None, 1e-6, 0.0)
+    grad_close(dx, dw, want_dx, want_dw, dy, h, w, dtype)
+    assert outside_unchanged(dx, before)
+    # dx on dy: a slot that two rows share is read by both and written by both
+    vh.add_rmsnorm_grad(dy, h, w, 1e-6, dh=e if dh else None, dx=dy)
+    assert torch.equal(dy, dx)
