@@ -209,9 +209,8 @@ struct Epilogue {
     // After the warp's first tile: its maxima are there (see find_bounds).
     __device__ __forceinline__ void first_done(const Args& a, const Rows& rw) {
         if (a.seg_max == nullptr) return;
-        __threadfence();
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) atomicAdd(a.seen + rw.group, 1u);
+        if ((threadIdx.x & 31) == 0) rows_take_ticket(a.seen + rw.group);
     }
 
     // v[j]: the score of head row v0 + lane for hidden row j of this warp's k-th block.

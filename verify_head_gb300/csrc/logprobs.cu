@@ -312,12 +312,11 @@ __global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprob
             int done = 0;
             if (lane == 0) {
                 __stcg(part, pack(st));
-                __threadfence();
-                done = atomicAdd(ws.ticket + first, 1u) == (unsigned)(last - first);
-                if (done) atomicExch(ws.ticket + first, 0u);
-                __threadfence();
+                done = rows_take_ticket(ws.ticket + first) == (unsigned)(last - first);
+                if (done) __stcg(ws.ticket + first, 0u);
             }
             if (__shfl_sync(0xFFFFFFFFu, done, 0) == 0) continue;
+            __syncwarp();
             st = join_pieces(ws, first, last);
         }
         if (lane == 0) {

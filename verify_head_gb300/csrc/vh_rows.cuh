@@ -18,6 +18,14 @@ __device__ __forceinline__ void rows_wait() { asm volatile("griddepcontrol.wait;
 // Before bulk or tensor copies read what kernels before this one wrote.
 __device__ __forceinline__ void rows_fence_async() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
+// Adds one to a counter, after everything that this thread wrote or (by a barrier) saw written and before everything that
+// it reads from then on: one ordered operation instead of full fences on both sides.
+__device__ __forceinline__ uint32_t rows_take_ticket(uint32_t* p) {
+    uint32_t old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+    return old;
+}
+
 // ---------------------------------------------------------------------------
 // Element types and vectors of VEC elements (16 bytes, or one element).
 
