@@ -27,6 +27,9 @@ namespace norm {
 
 constexpr int kMaxThreads = 512;  // register-resident rows: up to 128 registers a thread
 constexpr int kWideThreads = 512;
+// Shares of dweight that eight warps per 32 columns sum (67 x 5120 bf16, 67 shares: 6.1 us a call against 7.0 with 32
+// warps; 120 x 4096, 120 shares: 7.4 against 7.0).
+constexpr int kFewParts = 80;
 constexpr int kMaxRing = 4;                // tokens in flight per CTA of the gradient
 constexpr size_t kRingBytes = 56 * 1024;   // of shared memory per CTA that a ring of over two tokens stays below
 constexpr size_t kSmRingBytes = 220 * 1024;  // of shared memory per SM for rings
@@ -583,18 +586,32 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
     // wave after needs (8192 x 2048 bf16: 39.7 us a call with the signal at the start).
     rows_launch_dependents();
     if (a.part == nullptr) return;
-    float* p = a.part + (size_t)blockIdx.x * a.H;
-    float* sum = reinterpret_cast<float*>(ring) + (size_t)ry * a.H;  // [ty][H]
+    // A share lies as its vectors do, so that they are stored whole (27 x 8192 bf16: 5.7 us, against 8.4 us with stores of
+    // single elements 32 bytes apart): by slots it begins `shift` places before its first column (300 x 4097: 7.9 against
+    // 10.4 us).  Shares that are first added in shared memory leave it column by column anyway, and begin with the first
+    // (1000 x 1025: 8.2 against 9.9 us).
+    const bool slots = ROWS == kAlike && a.part_pitch != a.H;
+    float* p = a.part + (size_t)blockIdx.x * a.part_pitch;
+    float* to = ty > 1 ? reinterpret_cast<float*>(ring) + (size_t)ry * a.H : p;  // [ty][H]
+    const bool whole = VEC > 1 && (ROWS == kWhole || slots) && (reinterpret_cast<uintptr_t>(to) & 15) == 0;
     if (ty > 1) sync();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int v = rx + j * tx;
-        if (v < nvec)
+        if (v >= nvec) continue;
+        if constexpr (VEC > 1) {
+            if (whole) {
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                const int c = v * VEC - shift + k;
-                if (ROWS != kAlike || (c >= 0 && c < a.H)) (ty > 1 ? sum : p)[c] = dw[j][k];
+                for (int k = 0; k < VEC; k += 4)
+                    *reinterpret_cast<float4*>(to + v * VEC + k) = make_float4(dw[j][k], dw[j][k + 1], dw[j][k + 2], dw[j][k + 3]);
+                continue;
             }
+        }
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            const int c = v * VEC - shift + k;
+            if (ROWS != kAlike || (c >= 0 && c < a.H)) to[c] = dw[j][k];
+        }
     }
     if (ty == 1) return;
     sync();
@@ -661,21 +678,33 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_grad_wide(const NormGradA
     }
 }
 
-// dweight[c] = sum of part[0..n)[c], in order: 32 columns x 32 row groups per CTA, loads in batches.
-constexpr int kSumGroups = 32;
-__global__ void __launch_bounds__(32 * kSumGroups) k_sum_parts(const float* part, int n, int H, float* out) {
+// The tokens' shares of dweight: n of them, `pitch` floats apart; column c of share r lies (base + r step) & mask places on.
+struct Parts {
+    const float* at;
+    int n, pitch;
+    uint32_t base, step, mask;
+};
+
+// dweight[c] = sum of the shares' columns c, in order: 32 columns x GROUPS row groups per CTA, loads in batches.
+template <int GROUPS, bool SLOTS>
+__global__ void __launch_bounds__(32 * GROUPS) k_sum_parts(const Parts p, const int H, float* out) {
+    const float* part = p.at;
+    const int n = p.n;
     constexpr int kBatch = 10;
-    __shared__ float s[kSumGroups][33];
+    __shared__ float s[GROUPS][33];
     rows_wait();
     const int c = blockIdx.x * 32 + threadIdx.x;
     float v = 0.f;
     if (c < H)
-        for (int r0 = threadIdx.y; r0 < n; r0 += kSumGroups * kBatch) {
+        for (int r0 = threadIdx.y; r0 < n; r0 += GROUPS * kBatch) {
             float x[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const int r = r0 + i * kSumGroups;
-                x[i] = r < n ? part[(size_t)r * H + c] : 0.f;
+                const int r = r0 + i * GROUPS;
+                if constexpr (SLOTS)
+                    x[i] = r < n ? part[(size_t)r * p.pitch + c + ((p.base + (uint32_t)r * p.step) & p.mask)] : 0.f;
+                else
+                    x[i] = r < n ? part[(size_t)r * H + c] : 0.f;
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) v += x[i];
@@ -686,7 +715,7 @@ __global__ void __launch_bounds__(32 * kSumGroups) k_sum_parts(const float* part
     if (threadIdx.y == 0 && c < H) {
         float t = 0.f;
 #pragma unroll
-        for (int g = 0; g < kSumGroups; ++g) t += s[g][threadIdx.x];
+        for (int g = 0; g < GROUPS; ++g) t += s[g][threadIdx.x];
         out[c] = t;
     }
 }
@@ -756,9 +785,9 @@ static cudaError_t norm_type(const NormArgs& a, cudaStream_t s) {
     return slots ? norm_vec<T, V, true>(a, s) : norm_vec<T, 1, false>(a, s);
 }
 
-// `parts`: the CTAs that share the tokens (in: at most).
+// sum: the shares that are left to add up (in: at most n); one is dweight itself.
 template <typename T>
-static cudaError_t grad_type(const NormGradArgs& a, int& parts, cudaStream_t s) {
+static cudaError_t grad_type(NormGradArgs a, Parts& sum, float* dweight, cudaStream_t s) {
     constexpr int V = kVecOf<T>;
     const int size = (int)sizeof(T);
     const bool vec = a.H % V == 0 && mult16(a.h, a.h_stride, size) && mult16(a.dy, a.dy_stride, size) &&
@@ -769,7 +798,7 @@ static cudaError_t grad_type(const NormGradArgs& a, int& parts, cudaStream_t s) 
     };
     const bool dx_alike = alike(a.dx, a.dx_stride);
     // n vectors (or elements) a row, nv a thread; `period`: the tokens after which a row's start in its slot repeats
-    auto go = [&](auto kernel, int n, int nv, size_t pitch, int period) -> cudaError_t {
+    auto go = [&](auto kernel, int n, int nv, size_t pitch, int period, bool by_slots) -> cudaError_t {
         const int tx = row_threads(n, nv);
         const int ty = std::max(1, std::min(256 / tx, (int)(kRingBytes / kMaxRing / (3 * pitch))));  // keeps the ring deep
         const size_t place = (size_t)ty * 3 * pitch;
@@ -779,12 +808,21 @@ static cudaError_t grad_type(const NormGradArgs& a, int& parts, cudaStream_t s) 
         // against 20.5 us).  All of it for each start of a row.
         const int per_sm = std::min(4, (int)(kSmRingBytes / (depth * place)));
         const int groups = (a.T - 1) / period / ty + 1;
-        const int each = std::max(1, std::min({parts / period, groups, 152 * per_sm / period,
+        const int each = std::max(1, std::min({sum.n / period, groups, 152 * per_sm / period,
                                                std::max(76 * per_sm / period, groups / 3)}));
-        parts = std::min(parts, each * period);
+        sum.n = std::min(sum.n, each * period);
+        a.part_pitch = a.H;
+        if (sum.n == 1) {
+            a.part = dweight;  // the only share: no second launch (1 x 256: 2.6 against 4.6 us)
+        } else if (by_slots && ty == 1 && a.H % V != 0) {  // the workspace has room for slots in rows of such widths
+            sum.pitch = a.part_pitch = (a.H + 2 * (V - 1)) / V * V;
+            sum.base = (uint32_t)((reinterpret_cast<uintptr_t>(a.h) & 15) / size);
+            sum.step = (uint32_t)(a.h_stride % V);
+            sum.mask = V - 1;
+        }
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(depth * place));
         if (e != cudaSuccess) return e;
-        return launch(kernel, dim3((unsigned)parts), dim3(tx * ty + 32), depth * place, s, a, tx, ty, depth, (uint32_t)pitch,
+        return launch(kernel, dim3((unsigned)sum.n), dim3(tx * ty + 32), depth * place, s, a, tx, ty, depth, (uint32_t)pitch,
                       period, each, dx_alike);
     };
     if (vec) {
@@ -792,10 +830,11 @@ static cudaError_t grad_type(const NormGradArgs& a, int& parts, cudaStream_t s) 
         // 30.6 us with one).
         const int n = a.H / V;
         const size_t pitch = (size_t)a.H * size;
-        if (n <= 64) return go(k_norm_grad<T, V, 1, kWhole>, n, 1, pitch, 1);
-        if (n <= kMaxThreads * 2) return go(k_norm_grad<T, V, 2, kWhole>, n, 2, pitch, 1);
-        if (n <= kMaxThreads * 4) return go(k_norm_grad<T, V, 4, kWhole>, n, 4, pitch, 1);
-        return launch(k_norm_grad_wide<T, V>, dim3((unsigned)parts), dim3(kWideThreads), 0, s, a);
+        if (n <= 64) return go(k_norm_grad<T, V, 1, kWhole>, n, 1, pitch, 1, false);
+        if (n <= kMaxThreads * 2) return go(k_norm_grad<T, V, 2, kWhole>, n, 2, pitch, 1, false);
+        if (n <= kMaxThreads * 4) return go(k_norm_grad<T, V, 4, kWhole>, n, 4, pitch, 1, false);
+        if (sum.n == 1) a.part = dweight;
+        return launch(k_norm_grad_wide<T, V>, dim3((unsigned)sum.n), dim3(kWideThreads), 0, s, a);
     }
     const size_t pitch = ((size_t)a.H * size + 30) / 16 * 16;  // a row may start 15 bytes into its first granule
     // Where dx lies differently it is written by elements, so that its place does not change its bits.
@@ -803,13 +842,14 @@ static cudaError_t grad_type(const NormGradArgs& a, int& parts, cudaStream_t s) 
         int period = 1;
         while (a.h_stride * period % V != 0) period *= 2;  // V is a power of two
         const int n = (a.H + 2 * (V - 1)) / V;             // slots of the least favourable row
-        if (n <= 64) return go(k_norm_grad<T, V, 1, kAlike>, n, 1, pitch, period);
-        if (n <= kMaxThreads * 2) return go(k_norm_grad<T, V, 2, kAlike>, n, 2, pitch, period);
-        if (n <= kMaxThreads * 4) return go(k_norm_grad<T, V, 4, kAlike>, n, 4, pitch, period);
+        if (n <= 64) return go(k_norm_grad<T, V, 1, kAlike>, n, 1, pitch, period, true);
+        if (n <= kMaxThreads * 2) return go(k_norm_grad<T, V, 2, kAlike>, n, 2, pitch, period, true);
+        if (n <= kMaxThreads * 4) return go(k_norm_grad<T, V, 4, kAlike>, n, 4, pitch, period, true);
     }
-    if (a.H <= kMaxThreads * 8) return go(k_norm_grad<T, 1, 8, kAny>, a.H, 8, pitch, 1);
-    if (a.H <= kMaxThreads * 16) return go(k_norm_grad<T, 1, 16, kAny>, a.H, 16, pitch, 1);
-    return launch(k_norm_grad_wide<T, 1>, dim3((unsigned)parts), dim3(kWideThreads), 0, s, a);
+    if (a.H <= kMaxThreads * 8) return go(k_norm_grad<T, 1, 8, kAny>, a.H, 8, pitch, 1, false);
+    if (a.H <= kMaxThreads * 16) return go(k_norm_grad<T, 1, 16, kAny>, a.H, 16, pitch, 1, false);
+    if (sum.n == 1) a.part = dweight;
+    return launch(k_norm_grad_wide<T, 1>, dim3((unsigned)sum.n), dim3(kWideThreads), 0, s, a);
 }
 
 }  // namespace norm
@@ -823,13 +863,17 @@ cudaError_t launch_add_rmsnorm(const NormArgs& a, int dtype, cudaStream_t s) {
 }
 
 cudaError_t launch_add_rmsnorm_grad(const NormGradArgs& a, int dtype, float* dweight, cudaStream_t s) {
-    int parts = norm_grad_parts(a.T);
-    cudaError_t e = dtype == VH_BF16  ? norm::grad_type<__nv_bfloat16>(a, parts, s)
-                    : dtype == VH_F16 ? norm::grad_type<__half>(a, parts, s)
-                                      : norm::grad_type<float>(a, parts, s);
-    if (e != cudaSuccess || dweight == nullptr) return e;
-    return norm::launch(norm::k_sum_parts, dim3((unsigned)((a.H + 31) / 32)), dim3(32, norm::kSumGroups), 0, s,
-                        (const float*)a.part, parts, a.H, dweight);
+    norm::Parts sum = {a.part, norm_grad_parts(a.T), a.H, 0, 0, 0};
+    cudaError_t e = dtype == VH_BF16  ? norm::grad_type<__nv_bfloat16>(a, sum, dweight, s)
+                    : dtype == VH_F16 ? norm::grad_type<__half>(a, sum, dweight, s)
+                                      : norm::grad_type<float>(a, sum, dweight, s);
+    if (e != cudaSuccess || dweight == nullptr || sum.n == 1) return e;
+    auto add = [&](auto kernel, int groups) {
+        return norm::launch(kernel, dim3((unsigned)((a.H + 31) / 32)), dim3(32, groups), 0, s, sum, a.H, dweight);
+    };
+    if (sum.n <= norm::kFewParts)
+        return sum.mask ? add(norm::k_sum_parts<8, true>, 8) : add(norm::k_sum_parts<8, false>, 8);
+    return sum.mask ? add(norm::k_sum_parts<32, true>, 32) : add(norm::k_sum_parts<32, false>, 32);
 }
 
 }  // namespace vh

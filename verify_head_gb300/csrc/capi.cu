@@ -481,7 +481,7 @@ vh_status vh_add_rmsnorm(const void* x, const void* residual, const void* weight
 
 size_t vh_add_rmsnorm_grad_workspace_bytes(int T, int H) {
     if (T < 1 || H < 1) return 0;
-    return vh::round16((size_t)vh::norm_grad_parts(T) * (size_t)H * 4);
+    return vh::round16((size_t)vh::norm_grad_parts(T) * vh::norm_grad_pitch(H) * 4);
 }
 
 vh_status vh_add_rmsnorm_grad(const void* dy, const void* h, const void* weight, const void* dh, int dtype,

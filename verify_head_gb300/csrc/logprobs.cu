@@ -32,6 +32,8 @@ constexpr int kUnroll = 2;             // segments in flight per warp (and two m
 constexpr int kPerSm = 4, kPerSmTop = 3;
 constexpr int kTargetCtas = 152 * kPerSm;
 constexpr int kMinSegs = 2 * kWarpsL;  // segments per CTA below which the work is not cut further
+constexpr int kShortSegs = 64;         // segments per CTA up to which a call is short
+constexpr int kWholeSegs = 64, kRowSegs = 128;
 
 // A row as aligned 32-byte slots: slot v holds elements [v * kSlot - shift, +kSlot).
 constexpr int kSlotBytes = 32;
@@ -117,8 +119,26 @@ struct Ws {
 constexpr size_t kTicketEnd = kWsHeaderBytes + (size_t)kTargetCtas * 4;
 constexpr size_t kPartEnd = kTicketEnd + (size_t)kTargetCtas * 2 * 16;
 
-inline int ctas(long long units, int per_sm) {
-    return (int)std::max(1LL, std::min(152LL * per_sm, units / kMinSegs));
+// The CTAs of the scan, and into how many pieces each row is cut (0: the units are, whatever the rows).
+// With pieces of rows a CTA finishes one row or piece; with even ranges up to two pieces and the rows between them, one
+// after the other, but all CTAs have the same work.  So rows are cut for short calls (231 x 32768 bf16: 7.9 against
+// 10.0 us) and where that fills three quarters of the SMs' places (600 x 65536: 14.6 against 18.9 us; with half of
+// them, 310 x 131072, 23.8 against 19.0 us).
+// More rows than places: a CTA each up to kRowSegs segments (1645 x 32768: 21.9 against 24.5 us, 1024 x 65536: 26.1
+// against 27.0 us), even ranges above, where a last wave of few CTAs would weigh more; with alternatives, whose calls
+// write every unit's maximum, even ranges (1645 x 32768: 39.8 against 40.2 us).
+// Without alternatives the last piece's CTA joins a row, which takes 1.2 us: rows of up to kWholeSegs segments stay
+// whole (44 x 21479: 4.5 against 5.7 us, 2 x 65536 with 128 segments 5.8 against 4.6 us).
+inline void plan(int R, int segs, bool top, int& n, int& k) {
+    const long long units = (long long)R * segs;
+    const int wave = 152 * (top ? kPerSmTop : kPerSm);
+    k = top || segs > kWholeSegs ? std::max(1, std::min(wave / R, segs / kMinSegs)) : 1;
+    n = R * k;
+    if (R > wave && !top && segs <= kRowSegs) return;
+    if (R > wave || (units > (long long)wave * kShortSegs && n < wave / 4 * 3)) {
+        k = 0;
+        n = (int)std::min((long long)wave, std::max((long long)R, units / kMinSegs));
+    }
 }
 
 // A range of segments of one row.
@@ -229,18 +249,30 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
     return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// How the units are cut into ranges of n CTAs: `per` units each, the first `more` CTAs one more.
+// How the units are cut into ranges of n CTAs: `per` units each, the first `more` CTAs one more; or, with k > 0, every
+// row of `segs` units by itself into k ranges.
 struct Split {
     long long per, more;
-    __device__ __forceinline__ Split(long long units, int n) {
-        per = quotient(units, n);
+    int segs, k;
+    __device__ __forceinline__ Split(int rows, int segs_, int n, int k_) : segs(segs_), k(k_) {
+        const long long units = (long long)rows * segs;
+        per = k > 0 ? 0 : quotient(units, n);
         more = units - per * n;
     }
-    __device__ __forceinline__ long long begin(int c) const { return c * per + min((long long)c, more); }
+    __device__ __forceinline__ long long begin(int c) const {
+        if (k > 0) {
+            const int row = (int)((uint32_t)c / (uint32_t)k);
+            return (long long)row * segs + quotient((long long)(c - row * k) * segs, k);
+        }
+        return c * per + min((long long)c, more);
+    }
     __device__ __forceinline__ int cta_of(long long u) const {  // whose range holds unit u
         const long long big = more * (per + 1);
         return (int)(u < big ? quotient(u, per + 1) : more + quotient(u - big, per));
     }
+    // the CTAs that share a row
+    __device__ __forceinline__ int first(int row) const { return k > 0 ? row * k : cta_of((long long)row * segs); }
+    __device__ __forceinline__ int last(int row) const { return k > 0 ? row * k + k - 1 : cta_of((long long)(row + 1) * segs - 1); }
 };
 
 __device__ __forceinline__ float4 pack(const Stat& st) { return make_float4(st.c, st.s, st.t, 0.f); }
@@ -263,12 +295,13 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int row, const R
 // Everything after a row's scan is warp 0's; the other warps go on with the next row.  With alternatives (TOP) the
 // second kernel joins the pieces and writes the results; without, the last CTA of a row does.
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprobs(const LogprobArgs a, const Ws ws, const int row_segs) {
+__global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprobs(const LogprobArgs a, const Ws ws, const int row_segs,
+                                                                               const int pieces) {
     __shared__ float4 s_part[2][kWarpsL];
     rows_launch_dependents();
     rows_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Split split((long long)a.R * row_segs, gridDim.x);
+    const Split split(a.R, row_segs, gridDim.x, pieces);
     const long long u0 = split.begin(blockIdx.x), u1 = split.begin(blockIdx.x + 1);
     const int row0 = (int)quotient(u0, row_segs), first_g = (int)(u0 - (long long)row0 * row_segs);
     long long left = u1 - u0;  // units from the current piece on
@@ -301,14 +334,14 @@ __global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprob
         if (warp != 0) continue;
         st = stat_warp(lane < kWarpsL ? unpack(s_part[buf][lane]) : stat_none());
         if (g1 - g0 < row_segs) {
-            const int first = split.cta_of((long long)row * row_segs);
+            const int first = split.first(row);
             float4* part = ws.part + blockIdx.x * 2 + ((int)blockIdx.x == first);
             if (TOP) {
                 if (lane == 0) *part = pack(st);
                 continue;
             }
             // the last of the row's CTAs to get here joins the pieces
-            const int last = split.cta_of((long long)(row + 1) * row_segs - 1);
+            const int last = split.last(row);
             int done = 0;
             if (lane == 0) {
                 __stcg(part, pack(st));
@@ -331,7 +364,7 @@ __global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprob
 // One row per CTA: its statistics and its alternatives, after k_logprobs<T, true> of n_scan CTAs.
 template <typename T, bool SLOTS>
 __global__ void __launch_bounds__(kSelThreads, 3) k_logprobs_top(const LogprobArgs a, const Ws ws, const int row_segs,
-                                                                 const int n_scan) {
+                                                                 const int n_scan, const int pieces) {
     constexpr int kHeld = SLOTS ? 16 : 4;
     __shared__ SelectSmem s_sel;
     __shared__ RowStat s_rs;
@@ -342,11 +375,11 @@ __global__ void __launch_bounds__(kSelThreads, 3) k_logprobs_top(const LogprobAr
     const Row<T> x(p, a.V);
     auto finish = [&] {
         if (threadIdx.x >= 32) return;
-        const Split split((long long)a.R * row_segs, n_scan);
+        const Split split(a.R, row_segs, n_scan, pieces);
         const int tok = a.logprob != nullptr ? a.tokens[row] : -1;
         const bool given = tok >= 0 && tok < a.V;
         const float tok_score = given ? to_f32(p[tok]) : 0.f;
-        const int first = split.cta_of((long long)row * row_segs), last = split.cta_of((long long)(row + 1) * row_segs - 1);
+        const int first = split.first(row), last = split.last(row);
         const RowStat rs = stat_finish(first == last ? unpack(ws.row[row]) : join_pieces(ws, first, last));
         if (threadIdx.x == 0) {
             s_rs = rs;
@@ -446,12 +479,14 @@ static cudaError_t forward(const LogprobArgs& a, cudaStream_t s) {
     ws.part = reinterpret_cast<float4*>(p + kTicketEnd);
     ws.row = reinterpret_cast<float4*>(p + kPartEnd);
     ws.unit_max = reinterpret_cast<float*>(p + kPartEnd + (size_t)a.R * 16);
-    const dim3 grid((unsigned)ctas((long long)a.R * segs, a.top_n > 0 ? kPerSmTop : kPerSm));
-    if (a.top_n == 0) return launch(k_logprobs<T, false>, grid, dim3(kThreadsL), s, a, ws, segs);
-    const cudaError_t e = launch(k_logprobs<T, true>, grid, dim3(kThreadsL), s, a, ws, segs);
+    int n, k;
+    plan(a.R, segs, a.top_n > 0, n, k);
+    const dim3 grid((unsigned)n);
+    if (a.top_n == 0) return launch(k_logprobs<T, false>, grid, dim3(kThreadsL), s, a, ws, segs, k);
+    const cudaError_t e = launch(k_logprobs<T, true>, grid, dim3(kThreadsL), s, a, ws, segs, k);
     if (e != cudaSuccess) return e;
-    return segs <= kSlotSegs ? launch(k_logprobs_top<T, true>, dim3((unsigned)a.R), dim3(kSelThreads), s, a, ws, segs, (int)grid.x)
-                             : launch(k_logprobs_top<T, false>, dim3((unsigned)a.R), dim3(kSelThreads), s, a, ws, segs, (int)grid.x);
+    return segs <= kSlotSegs ? launch(k_logprobs_top<T, true>, dim3((unsigned)a.R), dim3(kSelThreads), s, a, ws, segs, n, k)
+                             : launch(k_logprobs_top<T, false>, dim3((unsigned)a.R), dim3(kSelThreads), s, a, ws, segs, n, k);
 }
 
 template <typename T, int VEC>

@@ -21,12 +21,13 @@ struct NormArgs {
 };
 cudaError_t launch_add_rmsnorm(const NormArgs& a, int dtype, cudaStream_t s);
 
-// Its gradient; dh may be null.  part: fp32 [norm_grad_parts(T)][H], or null
-// when dw is not wanted.
+// Its gradient; dh may be null.  part: fp32 [norm_grad_parts(T)][norm_grad_pitch(H)],
+// or null when dw is not wanted.
 struct NormGradArgs {
     const void *dy, *h, *w, *dh;
     void* dx;
     float* part;
+    int part_pitch;  // set by the launcher
     long long dy_stride, h_stride, dh_stride, dx_stride;
     int T, H;
     int w32;
@@ -34,6 +35,7 @@ struct NormGradArgs {
 };
 constexpr int kNormGradParts = 608;  // CTAs that share the tokens, at most: four per SM
 int norm_grad_parts(int T);
+inline size_t norm_grad_pitch(int H) { return H % 8 == 0 ? H : ((size_t)H + 14) / 8 * 8; }  // odd widths by slots
 cudaError_t launch_add_rmsnorm_grad(const NormGradArgs& a, int dtype, float* dweight, cudaStream_t s);
 
 // Log probabilities from logits (logprobs.cu).
