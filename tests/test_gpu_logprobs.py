@@ -440,3 +440,27 @@ def test_head_alternatives_with_ties(vh, R, V, n):
         got = vh.head_logprobs(x, W, tokens.cuda(), n)
         _, _, _, ids, _ = logprobs64((x[:1].double() @ W.double().t()), tokens[:1], n)
         assert torch.equal(got[3].cpu(), ids.expand(R, n))
+
+
+# how the scan is cut: rows into pieces, whole rows, a CTA per row past the SMs' places, even ranges (many rows of over 128
+# segments, rows that fill half of the places, with alternatives)
+@pytest.mark.parametrize("R,V,n", [(7, 30011, 0), (40, 60000, 0), (150, 20000, 0), (150, 20000, 3), (609, 2000, 0),
+                                   (1301, 5003, 0), (1301, 5003, 2), (620, 70001, 0), (310, 131072, 0), (310, 131072, 4),
+                                   (608, 33000, 0), (457, 40000, 1)])
+def test_every_cut_of_the_rows(vh, R, V, n):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(R + V)
+    x = (torch.randn(R, V, generator=g, device="cuda") * 2).to(BF)
+    tokens = torch.randint(0, V, (R,), generator=g, device="cuda", dtype=torch.int32)
+    ws = vh.logits_logprobs_workspace(R, V, n)
+    got = vh.logits_logprobs(x, tokens, n, ws=ws)
+    lse = torch.cat([torch.logsumexp(p.double(), 1) for p in x.split(64)])
+    close(got[2], lse, 2.0 ** -22, sums(V) + 2.0 ** -20)
+    ent = torch.cat([l - (torch.softmax(p.double(), 1) * p.double()).sum(1) for p, l in zip(x.split(64), lse.split(64))])
+    close(got[1], ent, 2.0 ** -22, 20 * sums(V))
+    close(got[0], x.gather(1, tokens.long()[:, None])[:, 0].double() - lse, 2.0 ** -22, sums(V) + 2.0 ** -20)
+    if n:
+        some = sorted({0, 1, R // 3, R // 2, R // 2 + 1, R - 2, R - 1})
+        check([t[some] for t in got], x[some], tokens[some].cpu(), n)
+    again = vh.logits_logprobs(x, tokens, n, ws=ws)  # the counters are left as they were
+    assert all(torch.equal(a, b) for a, b in zip(got, again) if a is not None)
