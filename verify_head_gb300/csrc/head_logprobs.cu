@@ -641,7 +641,8 @@ struct Blocks {
 };
 
 __global__ void __launch_bounds__(kThreadsF) k_head_logprobs_finish(const FinishArgs a) {
-    constexpr int kHeld = 5;  // shares of the statistics a lane of warp 0 loads at once (152 CTAs)
+    constexpr int kHeld = 5;  // shares of the statistics a lane of the joining warp loads at once (152 CTAs)
+    constexpr int kJoiner = kSelWarps - 1;
     __shared__ SelectSmem s_sel;
     __shared__ RowStat s_rs;
     rows_launch_dependents();
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(kThreadsF) k_head_logprobs_finish(const Finish
     const int tok = a.tokens != nullptr ? a.tokens[row] : -1;
     const bool given = tok >= 0 && tok < a.V;
     const float tok_score = given ? a.tok_score[row] : 0.f;
-    if (warp == 0) {
+    if (warp == kJoiner) {
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
             const int q = i * 32 + lane;
@@ -660,7 +661,6 @@ __global__ void __launch_bounds__(kThreadsF) k_head_logprobs_finish(const Finish
         }
     }
     auto join = [&] {
-        if (warp != 0) return;
         Stat st = stat_none();
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) st = stat_join(st, Stat{p[i].x, p[i].y, p[i].z});
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kThreadsF) k_head_logprobs_finish(const Finish
         }
     };
     if (a.top_n == 0) {
-        join();
+        if (warp == kJoiner) join();
         return;
     }
     const uint32_t floor = a.bound[row];

@@ -7,13 +7,18 @@
 // Forward: one pass over the logits.  A row is cut into slots of 32 aligned
 // bytes and segments of 32 slots (one warp load of 1 KiB).  Each thread keeps
 // a running maximum and the two sums of Stat; where alternatives are wanted
-// the maxima of segments, or of slots, are written too, and a second kernel,
-// one CTA per row, picks the alternatives from the units with the largest
-// maxima (select_top), reading about n units again.
+// the maxima of segments, or of slots, are written too, and one CTA per row
+// picks the alternatives from the units with the largest maxima (select_top),
+// reading about n units again.
 //
-// All rows' segments are shared out evenly over one resident wave of CTAs; a
-// row that several CTAs hold pieces of meets in the workspace, where the last
-// of them (a ticket, left zero again), or the second kernel, finishes it.
+// Rows are cut into pieces for about one resident wave of CTAs, or all rows'
+// segments are shared out evenly over it (see plan).  A row of several pieces
+// meets in the workspace, where the last of its CTAs (a ticket, left zero
+// again) finishes it, the choice included (129 x 40001 fp16 with 5
+// alternatives: 10.5 us, against 11.5 us with the choice in a second kernel;
+// 9.6 us since the statistics are joined while the listed units are read).
+// With even ranges a CTA may be the last one of two rows and more: then the
+// choice is a second kernel's.
 //
 // Bound: memory (the logits once; the gradient also writes them once).
 #include <algorithm>
@@ -28,7 +33,7 @@ constexpr int kThreadsL = kSelThreads;
 constexpr int kWarpsL = kThreadsL / 32;
 constexpr int kUnroll = 2;             // segments in flight per warp (and two more requested); three: 50.1 us for the same
 // CTAs per SM.  Four for statistics alone (2048 x 65536 bf16: 46.9 against 48.1 us with three); with alternatives
-// the rows are few and three, with more registers each, are faster (129 x 40001 fp16, 5 of them: 12.7 against 13.2 us).
+// the rows are few and three, with more registers each, are faster (129 x 40001 fp16, 5 of them, with even ranges: 12.7 against 13.2 us).
 constexpr int kPerSm = 4, kPerSmTop = 3;
 constexpr int kTargetCtas = 152 * kPerSm;
 constexpr int kMinSegs = 2 * kWarpsL;  // segments per CTA below which the work is not cut further
@@ -127,12 +132,12 @@ constexpr size_t kPartEnd = kTicketEnd + (size_t)kTargetCtas * 2 * 16;
 // More rows than places: a CTA each up to kRowSegs segments (1645 x 32768: 21.9 against 24.5 us, 1024 x 65536: 26.1
 // against 27.0 us), even ranges above, where a last wave of few CTAs would weigh more; with alternatives, whose calls
 // write every unit's maximum, even ranges (1645 x 32768: 39.8 against 40.2 us).
-// Without alternatives the last piece's CTA joins a row, which takes 1.2 us: rows of up to kWholeSegs segments stay
-// whole (44 x 21479: 4.5 against 5.7 us, 2 x 65536 with 128 segments 5.8 against 4.6 us).
+// The last piece's CTA joins a row, which takes 1.2 us: rows of up to kWholeSegs segments stay whole (44 x 21479: 4.5
+// against 5.7 us; 2 x 65536 with 128 segments 5.8 against 4.6 us).
 inline void plan(int R, int segs, bool top, int& n, int& k) {
     const long long units = (long long)R * segs;
     const int wave = 152 * (top ? kPerSmTop : kPerSm);
-    k = top || segs > kWholeSegs ? std::max(1, std::min(wave / R, segs / kMinSegs)) : 1;
+    k = segs > kWholeSegs ? std::max(1, std::min(wave / R, segs / kMinSegs)) : 1;
     n = R * k;
     if (R > wave && !top && segs <= kRowSegs) return;
     if (R > wave || (units > (long long)wave * kShortSegs && n < wave / 4 * 3)) {
@@ -278,11 +283,13 @@ struct Split {
 __device__ __forceinline__ float4 pack(const Stat& st) { return make_float4(st.c, st.s, st.t, 0.f); }
 __device__ __forceinline__ Stat unpack(float4 v) { return Stat{v.x, v.y, v.z}; }
 
-// The pieces of a row that CTAs first .. last share, by one warp.
-__device__ __forceinline__ Stat join_pieces(const Ws& ws, int first, int last) {
-    Stat st = stat_none();
-    for (int c = first + (threadIdx.x & 31); c <= last; c += 32)
-        st = stat_join(st, unpack(__ldcg(ws.part + c * 2 + (c == first))));
+// The pieces of a row that CTAs first .. last share, by one warp; `held`: what the lane has of them already.
+__device__ __forceinline__ float4 lane_piece(const Ws& ws, int first, int c, int last) {
+    return c <= last ? __ldcg(ws.part + c * 2 + (c == first)) : pack(stat_none());
+}
+__device__ __forceinline__ Stat join_pieces(const Ws& ws, int first, int last, float4 held) {
+    Stat st = unpack(held);
+    for (int c = first + 32 + (threadIdx.x & 31); c <= last; c += 32) st = stat_join(st, unpack(lane_piece(ws, first, c, last)));
     return stat_warp(st);
 }
 
@@ -292,11 +299,54 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int row, const R
     if (a.lse != nullptr) a.lse[row] = rs.lse;
 }
 
-// Everything after a row's scan is warp 0's; the other warps go on with the next row.  With alternatives (TOP) the
-// second kernel joins the pieces and writes the results; without, the last CTA of a row does.
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprobs(const LogprobArgs a, const Ws ws, const int row_segs,
-                                                                               const int pieces) {
+// A row's statistics (request(): what the lane reads of them, stat(): those of the whole row, by one warp) and its
+// alternatives, by all threads of a CTA.  EARLY: what a warp reads of the statistics and the token is requested before
+// the choice, not during it.  Many rows at once gain by it (the second kernel, 1024 x 65536 bf16 with 20 alternatives:
+// 40.8 against 42.6 us), a row by itself loses, as the warp's share of the maxima waits (9 x 1365: 6.7 against 6.3 us).
+template <typename T, bool SLOTS, bool EARLY, typename Request, typename GetStat>
+__device__ __forceinline__ void choose(SelectSmem& s_sel, RowStat& s_rs, const LogprobArgs& a, const Ws& ws, int row, int row_segs,
+                                       Request request, GetStat stat) {
+    constexpr int kHeld = SLOTS ? 16 : 4;
+    const T* p = static_cast<const T*>(a.logits) + (long long)row * a.stride;
+    const Row<T> x(p, a.V);
+    float4 held;
+    bool given = false;
+    float tok_score = 0.f;
+    auto read = [&] {
+        const int tok = a.logprob != nullptr ? a.tokens[row] : -1;
+        held = request();
+        given = tok >= 0 && tok < a.V;
+        if (given) tok_score = to_f32(p[tok]);
+    };
+    if (EARLY && threadIdx.x >= kSelThreads - 32) read();
+    auto finish = [&] {
+        if (!EARLY) read();
+        const RowStat rs = stat_finish(stat(held));
+        if ((threadIdx.x & 31) == 0) {
+            s_rs = rs;
+            write_row(a, row, rs, given, tok_score);
+        }
+    };
+    select_top<kHeld>(
+        s_sel, SLOTS ? x.slots() : (x.slots() + 31) / 32, a.top_n, 0u,
+        RowUnits<T, SLOTS>{x, ws.unit_max + (size_t)row * row_units(row_segs)}, finish,
+        [&](int i, unsigned long long k) {
+            const size_t o = (size_t)row * a.top_n + i;
+            a.top_ids[o] = k != 0ull ? (int32_t)key_gid(k) : -1;
+            a.top_logprobs[o] = k != 0ull ? stat_logprob(s_rs, key_score(k)) : neg_inf();
+        });
+}
+
+// What a scan does besides the statistics: nothing; the units' maxima, for the second kernel; or the choice itself, by the
+// last CTA of a row, where every CTA has one row or piece (by slots or by segments).
+enum Mode { kStats, kMaxima, kChooseSlots, kChooseSegs };
+
+// Everything after a row's scan is warp 0's; the other warps go on with the next row.  Without alternatives the last
+// CTA of a row joins the pieces and writes the results.
+template <typename T, Mode MODE>
+__global__ void __launch_bounds__(kThreadsL, MODE != kStats ? kPerSmTop : kPerSm)
+    k_logprobs(const LogprobArgs a, const Ws ws, const int row_segs, const int pieces) {
+    constexpr bool TOP = MODE != kStats, CHOOSE = MODE == kChooseSlots || MODE == kChooseSegs;
     __shared__ float4 s_part[2][kWarpsL];
     rows_launch_dependents();
     rows_wait();
@@ -331,6 +381,31 @@ __global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprob
         }));
         if (lane == 0) s_part[buf][warp] = pack(st);
         __syncthreads();
+        if constexpr (CHOOSE) {
+            __shared__ SelectSmem s_sel;
+            __shared__ RowStat s_rs;
+            __shared__ bool s_last;
+            const bool shared_row = g1 - g0 < row_segs;
+            const int first = split.first(row), last = split.last(row);
+            auto mine = [&] { return stat_warp(lane < kWarpsL ? unpack(s_part[buf][lane]) : stat_none()); };
+            if (shared_row) {
+                if (warp == 0) {
+                    st = mine();
+                    if (lane == 0) {
+                        __stcg(ws.part + blockIdx.x * 2 + ((int)blockIdx.x == first), pack(st));
+                        s_last = rows_take_ticket(ws.ticket + first) == (unsigned)(last - first);
+                        if (s_last) __stcg(ws.ticket + first, 0u);
+                    }
+                }
+                __syncthreads();
+                if (!s_last) return;
+            }
+            choose<T, MODE == kChooseSlots, false>(
+                s_sel, s_rs, a, ws, row, row_segs,
+                [&] { return shared_row ? lane_piece(ws, first, first + lane, last) : pack(stat_none()); },
+                [&](float4 held) { return shared_row ? join_pieces(ws, first, last, held) : mine(); });
+            return;
+        }
         if (warp != 0) continue;
         st = stat_warp(lane < kWarpsL ? unpack(s_part[buf][lane]) : stat_none());
         if (g1 - g0 < row_segs) {
@@ -350,7 +425,7 @@ __global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprob
             }
             if (__shfl_sync(0xFFFFFFFFu, done, 0) == 0) continue;
             __syncwarp();
-            st = join_pieces(ws, first, last);
+            st = join_pieces(ws, first, last, lane_piece(ws, first, first + lane, last));
         }
         if (lane == 0) {
             if (TOP)
@@ -361,39 +436,21 @@ __global__ void __launch_bounds__(kThreadsL, TOP ? kPerSmTop : kPerSm) k_logprob
     }
 }
 
-// One row per CTA: its statistics and its alternatives, after k_logprobs<T, true> of n_scan CTAs.
+// One row per CTA: its statistics and its alternatives, after k_logprobs<T, kMaxima> of n_scan CTAs.
 template <typename T, bool SLOTS>
-__global__ void __launch_bounds__(kSelThreads, 3) k_logprobs_top(const LogprobArgs a, const Ws ws, const int row_segs,
-                                                                 const int n_scan, const int pieces) {
-    constexpr int kHeld = SLOTS ? 16 : 4;
+__global__ void __launch_bounds__(kSelThreads, 3)
+    k_logprobs_top(const LogprobArgs a, const Ws ws, const int row_segs, const int n_scan) {
     __shared__ SelectSmem s_sel;
     __shared__ RowStat s_rs;
     rows_launch_dependents();
     rows_wait();
     const int row = blockIdx.x;
-    const T* p = static_cast<const T*>(a.logits) + (long long)row * a.stride;
-    const Row<T> x(p, a.V);
-    auto finish = [&] {
-        if (threadIdx.x >= 32) return;
-        const Split split(a.R, row_segs, n_scan, pieces);
-        const int tok = a.logprob != nullptr ? a.tokens[row] : -1;
-        const bool given = tok >= 0 && tok < a.V;
-        const float tok_score = given ? to_f32(p[tok]) : 0.f;
-        const int first = split.first(row), last = split.last(row);
-        const RowStat rs = stat_finish(first == last ? unpack(ws.row[row]) : join_pieces(ws, first, last));
-        if (threadIdx.x == 0) {
-            s_rs = rs;
-            write_row(a, row, rs, given, tok_score);
-        }
-    };
-    select_top<kHeld>(
-        s_sel, SLOTS ? x.slots() : (x.slots() + 31) / 32, a.top_n, 0u,
-        RowUnits<T, SLOTS>{x, ws.unit_max + (size_t)row * row_units(row_segs)}, finish,
-        [&](int i, unsigned long long k) {
-            const size_t o = (size_t)row * a.top_n + i;
-            a.top_ids[o] = k != 0ull ? (int32_t)key_gid(k) : -1;
-            a.top_logprobs[o] = k != 0ull ? stat_logprob(s_rs, key_score(k)) : neg_inf();
-        });
+    const Split split(a.R, row_segs, n_scan, 0);
+    const int first = split.first(row), last = split.last(row), lane = threadIdx.x & 31;
+    choose<T, SLOTS, true>(
+        s_sel, s_rs, a, ws, row, row_segs,
+        [&] { return first == last ? ws.row[row] : lane_piece(ws, first, first + lane, last); },
+        [&](float4 held) { return first == last ? unpack(held) : join_pieces(ws, first, last, held); });
 }
 
 // ---------------------------------------------------------------------------
@@ -482,11 +539,17 @@ static cudaError_t forward(const LogprobArgs& a, cudaStream_t s) {
     int n, k;
     plan(a.R, segs, a.top_n > 0, n, k);
     const dim3 grid((unsigned)n);
-    if (a.top_n == 0) return launch(k_logprobs<T, false>, grid, dim3(kThreadsL), s, a, ws, segs, k);
-    const cudaError_t e = launch(k_logprobs<T, true>, grid, dim3(kThreadsL), s, a, ws, segs, k);
+    const dim3 block(kThreadsL);
+    const bool slots = segs <= kSlotSegs;
+    if (a.top_n == 0) return launch(k_logprobs<T, kStats>, grid, block, s, a, ws, segs, k);
+    if (k > 0)
+        return slots ? launch(k_logprobs<T, kChooseSlots>, grid, block, s, a, ws, segs, k)
+                     : launch(k_logprobs<T, kChooseSegs>, grid, block, s, a, ws, segs, k);
+    const cudaError_t e = launch(k_logprobs<T, kMaxima>, grid, block, s, a, ws, segs, 0);
     if (e != cudaSuccess) return e;
-    return segs <= kSlotSegs ? launch(k_logprobs_top<T, true>, dim3((unsigned)a.R), dim3(kSelThreads), s, a, ws, segs, n, k)
-                             : launch(k_logprobs_top<T, false>, dim3((unsigned)a.R), dim3(kSelThreads), s, a, ws, segs, n, k);
+    const dim3 rows((unsigned)a.R), sel(kSelThreads);
+    return slots ? launch(k_logprobs_top<T, true>, rows, sel, s, a, ws, segs, n)
+                 : launch(k_logprobs_top<T, false>, rows, sel, s, a, ws, segs, n);
 }
 
 template <typename T, int VEC>

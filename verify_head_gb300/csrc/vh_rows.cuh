@@ -427,7 +427,8 @@ struct SelectSmem {
 //   void each(const Item&, int g, float b, f): f(key) with the argmax key of those that are not below b;
 //   kBatches, key(int g, int i): by a warp, the lane's key in batch i < kBatches of the unit's elements, in the order of
 //   their ids; 0 past the last.
-// meanwhile(): called once, after the maxima are requested and before they are used.
+// meanwhile(): called once, by the last warp, while the others read the listed units; emit() may use what it left in
+//   shared memory.
 // emit(i, key): key of the i-th largest element, i < n (0 = the row has fewer).
 // floor: ord_f32 of a value that n elements are known to reach, 0 = none.
 // All threads call it; nothing of sm need be set.
@@ -435,6 +436,7 @@ template <int HELD, typename Units, typename Meanwhile, typename Emit>
 __device__ __forceinline__ void select_top(SelectSmem& sm, int units, int n, uint32_t floor, const Units& un,
                                            Meanwhile meanwhile, Emit emit) {
     constexpr int kAtOnce = 4;  // units a warp loads at once
+    constexpr int kReaders = kSelWarps - 1;  // warps that read units
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float held[HELD];
     auto hold = [&](int base) {  // no branches between the loads
@@ -447,7 +449,6 @@ __device__ __forceinline__ void select_top(SelectSmem& sm, int units, int n, uin
         return m;
     };
     hold(0);
-    meanwhile();
     float m = held_max(0, neg_inf());
     for (int base = HELD * kSelThreads; base < units; base += HELD * kSelThreads) {
         hold(base);
@@ -478,6 +479,7 @@ __device__ __forceinline__ void select_top(SelectSmem& sm, int units, int n, uin
     const uint32_t bound = sm.bound;
     const float least = unord_f32(bound);  // may be NaN, which nothing is below
 
+    bool told = false;
     // Units and elements of ord_f32 `from` or more into the lists; false where a list overflows.
     auto list = [&](uint32_t from) {
         if (mine >= from && mine != 0u) {
@@ -495,6 +497,8 @@ __device__ __forceinline__ void select_top(SelectSmem& sm, int units, int n, uin
         }
         __syncthreads();
         const int n_unit = sm.n_unit;
+        if (!told && warp == kReaders) meanwhile();
+        told = true;
         if (n_unit > kSelUnits) return false;
         auto take = [&](unsigned long long k) {
             if ((uint32_t)(k >> 32) >= from) {
@@ -508,16 +512,16 @@ __device__ __forceinline__ void select_top(SelectSmem& sm, int units, int n, uin
                 un.each(un.load(g), g, least, take);
             }
         } else {
-            for (int i0 = warp; i0 < n_unit; i0 += kSelWarps * kAtOnce) {
+            for (int i0 = warp; i0 < n_unit && warp < kReaders; i0 += kReaders * kAtOnce) {
                 typename Units::Item it[kAtOnce];
 #pragma unroll
                 for (int u = 0; u < kAtOnce; ++u) {
-                    const int i = i0 + u * kSelWarps;
+                    const int i = i0 + u * kReaders;
                     if (i < n_unit) it[u] = un.load((int)sm.unit[i]);
                 }
 #pragma unroll
                 for (int u = 0; u < kAtOnce; ++u) {
-                    const int i = i0 + u * kSelWarps;
+                    const int i = i0 + u * kReaders;
                     if (i < n_unit && ord_f32(un.peak(it[u])) >= from) un.each(it[u], (int)sm.unit[i], least, take);
                 }
             }
