@@ -18,8 +18,9 @@
 // shared memory and then lane = hidden row: 32 scores in registers, a running
 // maximum and the sums of Stat per hidden row, kept across tiles.  About 10
 // instructions per score: with eight warps the epilogue of a tile is shorter
-// than its MMAs from H = 512 up (584 rows of 65,536 x 256, where it is not:
-// 75 us against 114 us with four warps).
+// than its MMAs from H = 512 up (584 rows of 65,536 x 256, where it is not,
+// 20 alternatives: 68 us, against 114 us with four warps and 80 us with
+// sixteen on blocks of 16 hidden rows).
 //
 // Alternatives.  Where they are wanted each block of 32 head rows (a segment)
 // leaves its maximum per hidden row in the workspace, and its 32 scores unless
