@@ -256,13 +256,14 @@ struct Epilogue {
         }
         Stat2 run{st[k].c, f2(st[k].s, 0.f), f2(st[k].t, 0.f)};
         run.raise(m);
-        if (run.c > kLiftFrom && run.c < kNearLimit) {
+        if (fabsf(run.c) < kFar) {
             const F2 mcl = run.minus_cl();
 #pragma unroll
             for (int i = 0; i < 32; i += 2) run.add_plain(fmaxf(x[i], kLift), fmaxf(x[i + 1], kLift), mcl);
         } else if (run.c != neg_inf()) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) run.add(x[i], x[i + 1]);
+#pragma unroll 1
+            for (int i = 0; i < n && i < 32; i += 2)
+                run.add_far(tr[place(lane, i)], i + 1 < n ? tr[place(lane, i + 1)] : neg_inf());
         }
         st[k] = run.get();
     }

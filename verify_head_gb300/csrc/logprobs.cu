@@ -232,7 +232,7 @@ __device__ __forceinline__ Stat scan(const Piece<T>& pc, Block<T>& next, float* 
             if (g + u * kWarpsL < pc.in1) keep_max(g + u * kWarpsL, mu);
         }
         run.raise(m);
-        if (run.c > lift_from && run.c < kNearLimit) {
+        if (run.c > lift_from && run.c < kFar) {
             const F2 mcl = run.minus_cl();
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {

@@ -196,17 +196,20 @@ __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
 // where the row is peaked, so nothing cancels.  c = -inf: nothing summed yet
 // (s = t = 0).  A +inf score leaves c = +inf and the row's statistics are NaN.
 //
-// y is taken as fma(x, log2e, -round(c log2e)); every use of c rounds that
-// product the same way, and what the rounding took is given back at the end.
-// Where |c| is near the type's limits the product would be infinite (a row
-// that holds the lowest value and nothing else) and y is (x - c) log2e.
+// Where |c| < kFar, y is taken as fma(x, log2e, -round(c log2e)); every use of
+// such a c rounds that product the same way, and what the rounding took
+// (stat_rest, a sixteenth at most) is given back at the end.  The rounding
+// grows with |c|: from about 1e9 it is an exponent that 2^y cannot hold, and a
+// row with nothing but a mask value in it (-1e10, -1e30, the type's lowest)
+// has such a maximum.  From kFar on y is (x - c) log2e, which costs a
+// subtraction more per score.
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNearLimit = 1e38f;
+constexpr float kFar = 1048576.0f;
 // Scores below kLift carry no probability beside a maximum above kLiftFrom and may be lifted to it.  A type whose
 // lowest value is above kLift is lifted to that value, beside a maximum that is well above it.
-constexpr float kLift = -1e30f, kLiftFrom = -1e29f;
+constexpr float kLift = -1e30f, kLiftFrom = -kFar;
 constexpr float kLiftHalf = -65504.f, kLiftFromHalf = -60000.f;
 // y below this is lifted to it: 2^y is 0 in either case and y * 2^y must not
 // become -inf * 0 at masked places (NaN scores land here too: they count as -inf).
@@ -228,19 +231,22 @@ struct Stat {
 
 __device__ __forceinline__ Stat stat_none() { return Stat{neg_inf(), 0.f, 0.f}; }
 
-// y of a score or of an older maximum.
+// What the rounding of c log2e took.
+__device__ __forceinline__ float stat_rest(float c) {
+    return fabsf(c) < kFar ? fmaf(c, kLog2e, -__fmul_rn(c, kLog2e)) : 0.f;
+}
+
+// y of a score.
 __device__ __forceinline__ float stat_y(float x, float c) {
-    const float y = fabsf(c) < kNearLimit ? fmaf(x, kLog2e, -(c * kLog2e)) : (x - c) * kLog2e;
+    const float y = fabsf(c) < kFar ? fmaf(x, kLog2e, -(c * kLog2e)) : (x - c) * kLog2e;
     return fmaxf(y, kFloorY);
 }
 
 // Move statistics to a larger maximum.
 __device__ __forceinline__ void stat_shift(Stat& a, float c) {
     if (a.s != 0.f) {
-        // both maxima's products rounded alike (no fma)
-        const float d = fabsf(a.c) < kNearLimit && fabsf(c) < kNearLimit
-                            ? fmaxf(__fmul_rn(a.c, kLog2e) - __fmul_rn(c, kLog2e), kFloorY)
-                            : fmaxf((a.c - c) * kLog2e, kFloorY);
+        // each maximum's sums lack what its own product's rounding took
+        const float d = fmaxf(fmaf(a.c - c, kLog2e, stat_rest(c) - stat_rest(a.c)), kFloorY);
         const float f = ex2(d);
         a.t = f * fmaf(d, a.s, a.t);
         a.s *= f;
@@ -278,7 +284,11 @@ struct Stat2 {
     }
     // Two scores; c is their maximum or more, not -inf.
     __device__ __forceinline__ void add(float x0, float x1) { add_y(stat_y(x0, c), stat_y(x1, c)); }
-    // Two scores of which none is -inf or NaN, where |c| < kNearLimit: minus_cl = -c log2e twice.
+    // The same where |c| >= kFar.
+    __device__ __forceinline__ void add_far(float x0, float x1) {
+        add_y(fmaxf((x0 - c) * kLog2e, kFloorY), fmaxf((x1 - c) * kLog2e, kFloorY));
+    }
+    // Two scores of which none is -inf or NaN, where |c| < kFar: minus_cl = -c log2e twice.
     __device__ __forceinline__ void add_plain(float x0, float x1, F2 minus_cl) {
         const F2 y = f2_fma(f2(x0, x1), f2(kLog2e, kLog2e), minus_cl);
         const float2 v = f2_get(y);
@@ -316,8 +326,7 @@ __device__ __forceinline__ RowStat stat_finish(const Stat& a) {
     RowStat r;
     r.c = a.c;
     const float l = log2f(a.s);
-    const float rest = fabsf(a.c) < kNearLimit ? fmaf(a.c, kLog2e, -(a.c * kLog2e)) : 0.f;
-    r.log2_s = l - rest;
+    r.log2_s = l - stat_rest(a.c);
     if (a.c == neg_inf()) {  // nothing but -inf (or NaN)
         r.lse = neg_inf();
         r.entropy = 0.f;
