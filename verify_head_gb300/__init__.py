@@ -495,6 +495,13 @@ def _stream_on(stream, dev):
     return _raw_stream(dev) if stream is None and _raw_stream else _stream_ptr(stream)
 
 
+def _int32(*sizes):
+    """Refuses sizes that the C ABI's ints do not hold (ctypes would pass their low 32 bits on)."""
+    for n in sizes:
+        if not -0x80000000 <= n <= 0x7FFFFFFF:
+            raise ValueError(f"a size of {n} is past 32 bits")
+
+
 def _place(t, name, dev):
     if t.get_device() != dev:
         raise ValueError(f"{name}: a CUDA tensor on device {dev} wanted")
@@ -559,6 +566,7 @@ def _add_rmsnorm(where, x, residual, weight, eps, weight_offset, y, out_dtype, k
     shape, dtype = x.shape, x.dtype
     xs = _rows(x, "x", dev, shape, dtype)
     T, H = shape
+    _int32(T, H)
     rp, rs = (residual.data_ptr(), _rows(residual, "residual", dev, shape, dtype)) if residual is not None else (None, 0)
     hp, hs = (h.data_ptr(), _rows(h, "h", dev, shape, dtype)) if h is not None else (None, 0)
     ys = _rows(y, "q" if kind else "y", dev, shape, out_dtype)
@@ -618,6 +626,7 @@ def add_rmsnorm_q8(x, residual=None, weight=None, eps: float = 1e-6, weight_offs
 
 def add_rmsnorm_grad_workspace(T: int, H: int, device=None):
     torch = _torch()
+    _int32(T, H)
     return torch.empty(int(lib().vh_add_rmsnorm_grad_workspace_bytes(T, H)), dtype=torch.uint8, device=device or "cuda")
 
 
@@ -638,6 +647,7 @@ def add_rmsnorm_grad(dy, h, weight=None, eps: float = 1e-6, weight_offset: float
     shape, dtype = h.shape, h.dtype
     hs = _rows(h, "h", dev, shape, dtype)
     T, H = shape
+    _int32(T, H)
     dys = _rows(dy, "dy", dev, shape, dtype)
     ep, es = (dh.data_ptr(), _rows(dh, "dh", dev, shape, dtype)) if dh is not None else (None, 0)
     w, w32 = _norm_weight(weight, H, dtype, dev)
@@ -685,6 +695,7 @@ def _logprob_results(outs, tokens):
 def logits_logprobs_workspace(R: int, V: int, top_n: int = 0, device=None):
     """A zeroed workspace for logits_logprobs calls of this R, V and top_n."""
     torch = _torch()
+    _int32(R, V, top_n)
     n = int(lib().vh_logits_logprobs_workspace_bytes(R, V, top_n))
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
@@ -705,6 +716,7 @@ def logits_logprobs(logits, tokens, top_n: int = 0, logprob=None, entropy=None, 
     shape = logits.shape
     stride = _rows(logits, "logits", dev, shape, logits.dtype)
     R, V = shape
+    _int32(R, V, top_n)
     tp = _vector(tokens, "tokens", dev, R, _i32)
     outs, at = _logprob_outputs(R, top_n, logits, dev, stream, tokens,
                                 (logprob, entropy, lse, top_ids, top_logprobs, ws),
@@ -729,6 +741,7 @@ def logits_logprobs_grad(logits, tokens, lse, entropy=None, g_logprob=None, g_en
     shape, dtype = logits.shape, logits.dtype
     stride = _rows(logits, "logits", dev, shape, dtype)
     R, V = shape
+    _int32(R, V)
     if dlogits is None:
         with _allocating(stream):
             dlogits = _empty_rows(logits)
@@ -744,6 +757,7 @@ def logits_logprobs_grad(logits, tokens, lse, entropy=None, g_logprob=None, g_en
 def head_logprobs_workspace(R: int, V: int, top_n: int = 0, device=None):
     """A workspace for head_logprobs calls of this R, V and top_n (about 4 V bytes per row with alternatives)."""
     torch = _torch()
+    _int32(R, V, top_n)
     ws = torch.empty(int(lib().vh_head_logprobs_workspace_bytes(R, V, top_n)), dtype=torch.uint8, device=device or "cuda")
     ws[:8192].zero_()
     return ws
@@ -766,6 +780,7 @@ def head_logprobs(hidden, W_full, tokens, top_n: int = 0, logprob=None, entropy=
     bf16 = _torch().bfloat16
     R, H = hidden.shape
     V = W_full.shape[0]
+    _int32(R, H, V, top_n)
     if W_full.shape[1] != H or hidden.dtype != bf16 or W_full.dtype != bf16:
         raise ValueError("shape/dtype mismatch")
     tp = _vector(tokens, "tokens", dev, R, _i32)
