@@ -35,11 +35,18 @@
  *  - Kernels launch as programmatic dependents of the previous kernel in the
  *    stream and may begin reading their weight table (W_cand, W_full, the
  *    4-bit tables) before that kernel has finished; everything else is read
- *    only after it has.  A kernel lets its dependent start early only if it
- *    signals so (griddepcontrol.launch_dependents): this library's kernels
- *    do and never write a weight table.  A table written by a copy, or by a
+ *    only after it has, but hidden rows and candidate ids partly on the
+ *    read-only path.  A kernel lets its dependent start early only if it
+ *    signals so (griddepcontrol.launch_dependents).  What a copy wrote, or a
  *    kernel that does not signal early, is seen complete; do not write a
- *    weight table from a kernel that signals early right before a call.
+ *    weight table, hidden rows or candidate ids from a kernel that signals
+ *    early right before a call.  Of this library's calls those that write
+ *    rows or lists of ids for general use do not signal early
+ *    (vh_add_rmsnorm; dx of vh_add_rmsnorm_grad; dlogits; log probabilities
+ *    with alternatives; vh_nvfp4_pack): a table, rows or a list that they
+ *    write can be the next call's.  The draft and verify kernels signal early:
+ *    their ids may be any later call's row_ids or draft_ids, and its cand_ids
+ *    after a call or an operation that does not signal.
  *  - The same sources also build as libverifyhead_debug.so (-DVH_DEBUG): an
  *    identical ABI whose kernels check their row indices on the device and
  *    report a failed check in the workspace error word (bit 2) instead of

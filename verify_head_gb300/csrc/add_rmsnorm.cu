@@ -229,7 +229,6 @@ __device__ __forceinline__ void load_weight_slot(const void* w, int w32, int e, 
 template <typename T, int VEC, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a) {
     __shared__ float2 red[32];
-    rows_launch_dependents();
     rows_wait();
     const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = row < a.T;
@@ -333,7 +332,6 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a) {
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kWideThreads) k_norm_wide(const NormArgs a) {
     __shared__ float2 red[32];
-    rows_launch_dependents();
     rows_wait();
     const long long row = blockIdx.x;
     const int nvec = a.H / VEC;
@@ -582,10 +580,10 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
             ph ^= 1;
         }
     }
-    // The grid is one resident wave: CTAs of the next kernel that came before this one's end would take places that the
-    // wave after needs (8192 x 2048 bf16: 39.7 us a call with the signal at the start).
-    rows_launch_dependents();
     if (a.part == nullptr) return;
+    // Only where the summing kernel follows.  The grid is one resident wave: CTAs of the next kernel that came before this
+    // one's end would take places that the wave after needs (8192 x 2048 bf16: 39.7 us a call with the signal at the start).
+    if (a.summed) rows_launch_dependents();
     // A share lies as its vectors do, so that they are stored whole (27 x 8192 bf16: 5.7 us, against 8.4 us with stores of
     // single elements 32 bytes apart): by slots it begins `shift` places before its first column (300 x 4097: 7.9 against
     // 10.4 us).  Shares that are first added in shared memory leave it column by column anyway, and begin with the first
@@ -627,7 +625,7 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kWideThreads) k_norm_grad_wide(const NormGradArgs a) {
     __shared__ float2 red[2][32];
-    rows_launch_dependents();
+    if (a.summed) rows_launch_dependents();
     rows_wait();
     const int nvec = a.H / VEC;
     float* p = a.part == nullptr ? nullptr : a.part + (size_t)blockIdx.x * a.H;
@@ -812,6 +810,7 @@ static cudaError_t grad_type(NormGradArgs a, Parts& sum, float* dweight, cudaStr
                                                std::max(76 * per_sm / period, groups / 3)}));
         sum.n = std::min(sum.n, each * period);
         a.part_pitch = a.H;
+        a.summed = a.part != nullptr && sum.n > 1;
         if (sum.n == 1) {
             a.part = dweight;  // the only share: no second launch (1 x 256: 2.6 against 4.6 us)
         } else if (by_slots && ty == 1 && a.H % V != 0) {  // the workspace has room for slots in rows of such widths
@@ -833,6 +832,7 @@ static cudaError_t grad_type(NormGradArgs a, Parts& sum, float* dweight, cudaStr
         if (n <= 64) return go(k_norm_grad<T, V, 1, kWhole>, n, 1, pitch, 1, false);
         if (n <= kMaxThreads * 2) return go(k_norm_grad<T, V, 2, kWhole>, n, 2, pitch, 1, false);
         if (n <= kMaxThreads * 4) return go(k_norm_grad<T, V, 4, kWhole>, n, 4, pitch, 1, false);
+        a.summed = a.part != nullptr && sum.n > 1;
         if (sum.n == 1) a.part = dweight;
         return launch(k_norm_grad_wide<T, V>, dim3((unsigned)sum.n), dim3(kWideThreads), 0, s, a);
     }
@@ -848,6 +848,7 @@ static cudaError_t grad_type(NormGradArgs a, Parts& sum, float* dweight, cudaStr
     }
     if (a.H <= kMaxThreads * 8) return go(k_norm_grad<T, 1, 8, kAny>, a.H, 8, pitch, 1, false);
     if (a.H <= kMaxThreads * 16) return go(k_norm_grad<T, 1, 16, kAny>, a.H, 16, pitch, 1, false);
+    a.summed = a.part != nullptr && sum.n > 1;
     if (sum.n == 1) a.part = dweight;
     return launch(k_norm_grad_wide<T, 1>, dim3((unsigned)sum.n), dim3(kWideThreads), 0, s, a);
 }

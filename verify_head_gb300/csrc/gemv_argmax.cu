@@ -130,6 +130,13 @@ __device__ __forceinline__ void finish_argmax(const unsigned long long (&best)[N
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A row id of a list that may have been written while this kernel was waiting.
+__device__ __forceinline__ int32_t ld_id(const int32_t* p) {
+    int32_t v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Rows (per warp) whose lines are prefetched into L2 ahead of the row being
@@ -153,8 +160,9 @@ __global__ void __launch_bounds__(kThreads, (NB == 1 ? 4 : 1)) k_gemv_bf16(const
     const long long r0 = gw * a.n_rows / nw;
     const long long r1 = (gw + 1) * a.n_rows / nw;
 
-    // physical W row of scan position r (the identity unless gathering)
-    auto wrow = [&](long long r) -> long long { return GATHER ? (long long)__ldg(a.cand + r) : r; };
+    // physical W row of scan position r (the identity unless gathering; then from L2, past L1: the previous kernel may
+    // still be writing the list.  Before the wait it serves as a hint for the prefetch alone.)
+    auto wrow = [&](long long r) -> long long { return GATHER ? (long long)ld_id(a.cand + r) : r; };
     auto in_range = [&](long long pr) -> bool { return !GATHER || (pr >= 0 && pr < a.V); };
 
     pdl_launch_dependents();
@@ -184,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, (NB == 1 ? 4 : 1)) k_gemv_bf16(const
     for (long long r = r0; r < r1; r += RPI) {
         if (GATHER && ((r - r0) & 31) == 0) {
             const long long rr = r + lane;
-            idx_cache = rr < r1 ? __ldg(a.cand + rr) : -1;
+            idx_cache = rr < r1 ? ld_id(a.cand + rr) : -1;
         }
         if constexpr (kPrefetchRows > 0 && !GATHER) {  // keep rows ahead of the loads in flight to L2
             const long long rp = r + kPrefetchRows * RPI;

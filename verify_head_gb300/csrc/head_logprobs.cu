@@ -607,6 +607,7 @@ constexpr int kThreadsF = kSelThreads;
 
 struct FinishArgs {
     int Rp, V, n_parts, segs, top_n;
+    bool signal;  // no ids are written, or this call's next pass follows
     const int32_t* tokens;
     const float* tok_score;
     const float4* part;
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(kThreadsF) k_head_logprobs_finish(const Finish
     constexpr int kJoiner = kSelWarps - 1;
     __shared__ SelectSmem s_sel;
     __shared__ RowStat s_rs;
-    rows_launch_dependents();
+    if (a.signal) rows_launch_dependents();
     rows_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x;
@@ -812,6 +813,7 @@ static cudaError_t pass(const HeadLogprobArgs& h, int r0, int nr, cudaStream_t s
     f.n_parts = n_parts;
     f.segs = l.segs;
     f.top_n = h.top_n;
+    f.signal = h.top_n == 0 || r0 + nr < h.R;
     f.tokens = a.tokens;
     f.tok_score = a.tok_score;
     f.part = a.part;

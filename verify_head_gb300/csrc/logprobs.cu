@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreadsL, MODE != kStats ? kPerSmTop : kPerSm
     k_logprobs(const LogprobArgs a, const Ws ws, const int row_segs, const int pieces) {
     constexpr bool TOP = MODE != kStats, CHOOSE = MODE == kChooseSlots || MODE == kChooseSegs;
     __shared__ float4 s_part[2][kWarpsL];
-    rows_launch_dependents();
+    if (!CHOOSE) rows_launch_dependents();
     rows_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Split split(a.R, row_segs, gridDim.x, pieces);
@@ -442,7 +442,6 @@ __global__ void __launch_bounds__(kSelThreads, 3)
     k_logprobs_top(const LogprobArgs a, const Ws ws, const int row_segs, const int n_scan) {
     __shared__ SelectSmem s_sel;
     __shared__ RowStat s_rs;
-    rows_launch_dependents();
     rows_wait();
     const int row = blockIdx.x;
     const Split split(a.R, row_segs, n_scan, 0);
@@ -461,7 +460,6 @@ constexpr int kGradUnroll = 4;
 // VEC: elements of a 16-byte slot, as the forward pass cuts a row (both tensors' rows lie alike in their slots), or 1.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreadsL) k_logprobs_grad(const LogprobGradArgs a, int chunks) {
-    rows_launch_dependents();
     rows_wait();
     const int row = (int)(blockIdx.x / chunks);
     const int chunk = (int)(blockIdx.x % chunks);

@@ -27,7 +27,8 @@ struct NormGradArgs {
     const void *dy, *h, *w, *dh;
     void* dx;
     float* part;
-    int part_pitch;  // set by the launcher
+    int part_pitch;  // set by the launcher, as is:
+    bool summed;     // the shares' sum is left to a second kernel
     long long dy_stride, h_stride, dh_stride, dx_stride;
     int T, H;
     int w32;

@@ -13,6 +13,10 @@
 
 namespace vh {
 
+// Lets the next kernel in the stream start.  The head kernels read their weight table, and the read-only path their ids
+// and rows, without regard to kernels that are still running: a kernel signals only if it writes neither rows nor ids
+// that a caller could hand on (workspaces and fp32 vectors are read after the wait), or if a kernel of the same call,
+// which waits for it, follows.
 __device__ __forceinline__ void rows_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void rows_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Before bulk or tensor copies read what kernels before this one wrote.
