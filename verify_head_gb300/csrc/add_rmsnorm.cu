@@ -33,6 +33,9 @@ constexpr int kFewParts = 80;
 constexpr int kMaxRing = 4;                // tokens in flight per CTA of the gradient
 constexpr size_t kRingBytes = 56 * 1024;   // of shared memory per CTA that a ring of over two tokens stays below
 constexpr size_t kSmRingBytes = 220 * 1024;  // of shared memory per SM for rings
+// The largest ring: two tokens' three rows of four vectors a thread, each begun in its granule.  A kernel's limit of
+// shared memory is set to this whatever the call needs, so that it never falls between another thread's setting it and its launch.
+constexpr size_t kMaxRingBytes = 2 * 3 * ((size_t)kMaxThreads * 4 * 16 + 16);
 
 // Bounded wait for a barrier's phase: whether it completed.
 __device__ __forceinline__ bool mbar_done(unsigned long long* bar, uint32_t parity) {
@@ -819,7 +822,8 @@ static cudaError_t grad_type(NormGradArgs a, Parts& sum, float* dweight, cudaStr
             sum.step = (uint32_t)(a.h_stride % V);
             sum.mask = V - 1;
         }
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(depth * place));
+        if (depth * place > kMaxRingBytes) return cudaErrorInvalidValue;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxRingBytes);
         if (e != cudaSuccess) return e;
         return launch(kernel, dim3((unsigned)sum.n), dim3(tx * ty + 32), depth * place, s, a, tx, ty, depth, (uint32_t)pitch,
                       period, each, dx_alike);

@@ -715,11 +715,16 @@ static cudaError_t occupancy(const void* kernel, size_t smem, int& per_sm) {
     return cudaSuccess;
 }
 
+// What gemv_group leaves a launch group.  A kernel's limit is set to this whatever the call needs, so that it never falls
+// between another thread's setting it and its launch.
+constexpr size_t kMaxDynSmem = 128 * 1024;
+
 template <typename K>
 static cudaError_t launch_split_v(K kernel, size_t smem, int n_rows, GemvArgs& a, cudaStream_t s, bool pdl,
                                   bool even_rows = false) {
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (smem > kMaxDynSmem) return cudaErrorInvalidValue;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDynSmem);
         if (e != cudaSuccess) return e;
     }
     int per_sm = 0;

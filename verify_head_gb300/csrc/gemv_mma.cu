@@ -303,12 +303,16 @@ __global__ void __launch_bounds__(kThreadsG, 2) k_gemv_mma_bf16(const Args a) {
     }
 }
 
+// The most hidden-row fragments a launch may hold.  A kernel's limit is set to this whatever the call needs, so that it
+// never falls between another thread's setting it and its launch.
+constexpr size_t kMaxDynSmem = 160 * 1024;
+
 template <int STEP, int NBUF, int NR>
 static cudaError_t launch_steps(const Args& a, cudaStream_t s) {
     auto kernel = k_gemv_mma_bf16<STEP, NBUF, NR>;
     const size_t smem = (size_t)a.H * (NR == 16 ? 32 : 16);
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDynSmem);
         if (e != cudaSuccess) return e;
     }
     static std::mutex mu;
@@ -347,7 +351,7 @@ static cudaError_t launch_steps(const Args& a, cudaStream_t s) {
 
 bool gemv_mma_supported(int nb, int H) {  // 1-16 hidden rows, H % 256 == 0, hidden rows fit shared memory
     return nb >= 1 && nb <= gmma::kMaxRows && H >= gmma::kStepK && H % gmma::kStepK == 0 &&
-           (size_t)H * (nb > 8 ? 32 : 16) <= 160 * 1024;
+           (size_t)H * (nb > 8 ? 32 : 16) <= gmma::kMaxDynSmem;
 }
 
 cudaError_t launch_gemv_mma_bf16(const uint16_t* x, int nb, int H, const uint16_t* W, const int32_t* cand, int n_rows,

@@ -540,7 +540,8 @@ cudaError_t launch_nvfp4_packed(const uint16_t* x, int nb, int H, const uint8_t*
     a.tail = tail;
     auto kernel = nb <= 8 ? k_nvfp4_packed<1, kWarpsNT1> : k_nvfp4_packed<2, kWarpsNT2>;
     const int threads = 32 * (nb <= 8 ? kWarpsNT1 : kWarpsNT2);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the same for every call: the limit never falls between another thread's setting it and its launch
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDynSmem);
     if (e != cudaSuccess) return e;
     int per_sm = 0;
     e = resident_ctas(reinterpret_cast<const void*>(kernel), threads, smem, per_sm);
