@@ -1,0 +1,52 @@
+"""The norm's gradient of rows that begin and end inside a 16-byte granule: the ends of the tensor, which are stored
+element by element into the ring that the rest of the row is copied to, and rows that lie differently in each tensor."""
+import pytest
+import torch
+
+from rows_util import TINY, U, close, norm_grad64, sums
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def vh():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import verify_head_gb300 as vh
+    vh.build()
+    return vh
+
+
+def rows(g, T, H, dtype, scale=1.0, pitch=None, offset=0):
+    """A [T,H] CUDA tensor with rows `pitch` apart and `offset` elements into its storage; NaN beside the rows."""
+    pitch = pitch or H
+    flat = torch.full((T * pitch + offset + 16,), float("nan"), dtype=dtype, device="cuda")
+    t = flat[offset:offset + T * pitch].view(T, pitch)[:, :H]
+    t.copy_((torch.randn(T, H, generator=g) * scale).to(dtype))
+    return t
+
+
+def check(dx, dw, dy, h, w, e, dtype):
+    """dx = rstd g - rstd n mean(g n) + dh: the errors of its terms add up; dw: a sum over tokens in three steps."""
+    want_dx, want_dw = norm_grad64(dy, h, w, e, 1e-6, 0.0)
+    T, H = h.shape
+    hd, gd = h.double(), dy.double() * w.double()
+    rstd = 1 / torch.sqrt((hd * hd).mean(1, keepdim=True) + 1e-6)
+    n = hd * rstd
+    size = rstd * (gd.abs() + n.abs() * (gd * n).abs().mean(1, keepdim=True))
+    close(dx, want_dx, U[dtype] * (1 + 2 ** -10) + 2.0 ** -24, size * sums(H) * 2 + TINY[dtype])
+    close(dw, want_dw, 2.0 ** -24, (dy.double() * n).abs().sum(0) * (T / 152 + 80 + sums(H) * 2 ** 24) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,H", [(1, 21), (2, 1029), (3, 2561)])
+def test_ends_of_the_tensor_every_time(vh, T, H, dtype):
+    """Nothing but first and last tokens, again and again with other values."""
+    g = torch.Generator().manual_seed(H)
+    w = torch.randn(H, generator=g).to(dtype).cuda()
+    for i in range(40):
+        dy, h, e = (rows(g, T, H, dtype, offset=1 + i % 7) for _ in range(3))
+        dx, dw = vh.add_rmsnorm_grad(dy, h, w, 1e-6, dh=e)
+        check(dx, dw, dy, h, w, e, dtype)

@@ -482,6 +482,7 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
             }
             const uint32_t bytes = on ? (uint32_t)(hi - lo) : 0;
             const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, bytes);
+            __syncwarp();  // lane 0 arrives for all: after every lane's stores of row ends
             if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], all);
             __syncwarp();
             if (bytes != 0) bulk_copy(to, reinterpret_cast<const void*>(lo), bytes, &full[s]);
