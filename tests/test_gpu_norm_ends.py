@@ -50,3 +50,16 @@ def test_ends_of_the_tensor_every_time(vh, T, H, dtype):
         dy, h, e = (rows(g, T, H, dtype, offset=1 + i % 7) for _ in range(3))
         dx, dw = vh.add_rmsnorm_grad(dy, h, w, 1e-6, dh=e)
         check(dx, dw, dy, h, w, e, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("H", [1, 2, 3, 5, 7, 9])
+@pytest.mark.parametrize("T", [1, 2, 4, 9, 40])
+def test_rows_shorter_than_a_granule(vh, T, H, dtype):
+    """Several tokens in the tensor's first and last granule."""
+    g = torch.Generator().manual_seed(T * 10 + H)
+    w = torch.randn(H, generator=g).to(dtype).cuda()
+    for pitch, offset in ((H, 0), (H, 1), (H, 3), (H + 1, 2)):
+        dy, h, e = (rows(g, T, H, dtype, pitch=pitch, offset=offset) for _ in range(3))
+        dx, dw = vh.add_rmsnorm_grad(dy, h, w, 1e-6, dh=e)
+        check(dx, dw, dy, h, w, e, dtype)

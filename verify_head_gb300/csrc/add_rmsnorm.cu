@@ -21,6 +21,7 @@
 #include "vh_ptx.cuh"
 #include "vh_row_kernels.h"
 #include "vh_rows.cuh"
+#include "vh_window.h"
 
 namespace vh {
 namespace norm {
@@ -401,31 +402,23 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(const NormArgs a) {
 //
 // ROWS: whole aligned vectors of VEC elements; or rows that lie alike in their 16-byte slots (VEC as before); or rows of
 // any alignment (VEC 1).  In the last two a token's place holds the 16-byte granules that its row touches.  What those
-// hold beside the row is its neighbours' (or the gap between rows); at the two ends of the tensor, where there is no
-// neighbour, only whole granules are copied and the elements outside them are stored one by one.
+// hold beside the row is its neighbours' (or the gap between rows); granules that reach past the ends of the tensor are not
+// copied, and the elements in them are stored one by one.
 // Where rows lie alike, the start of a row in its slot repeats every `period` tokens, and a CTA takes tokens of one
 // start only: so a thread's vectors hold the same columns of every token, as its weights and its share of dw need.
 //   8191 x 2561 bf16: 98.9 us with loads of single elements, 63.1 us element by element out of the ring, 43 us by slots;
 //   2047 x 8191: 61 and 41 us, 16383 x 257: 40 and 21 us, 4000 x 1025 fp16: 19 and 20 us.
 enum Rows { kWhole, kAlike, kAny };
 
-// The granules of a row of `bytes` that may be copied: [lo, hi).
-__device__ __forceinline__ void window(uintptr_t b, uint32_t bytes, bool first, bool last, uintptr_t& lo, uintptr_t& hi) {
-    lo = (first ? b + 15 : b) & ~uintptr_t(15);
-    hi = (last ? b + bytes : b + bytes + 15) & ~uintptr_t(15);
-    if (hi < lo) hi = lo;
-}
-
 // What a row at `p` holds outside [lo, hi), into its place.
 template <typename T>
 __device__ __forceinline__ void store_ends(uint8_t* to, const T* p, uint32_t bytes, uintptr_t lo, uintptr_t hi) {
     const uintptr_t b = reinterpret_cast<uintptr_t>(p);
     T* at = reinterpret_cast<T*>(to + (b & 15));
-    const int n = (int)(bytes / sizeof(T));
-    const int head = min(n, (int)((lo - b) / sizeof(T)));               // elements before the window
-    const int tail = hi > b ? min(n, (int)((hi - b) / sizeof(T))) : 0;  // the first one behind it
+    int head, tail;
+    outside_window(b, bytes, (int)sizeof(T), lo, hi, head, tail);
     for (int i = 0; i < head; ++i) at[i] = p[i];
-    for (int i = max(head, tail); i < n; ++i) at[i] = p[i];
+    for (int i = tail; i < (int)(bytes / sizeof(T)); ++i) at[i] = p[i];
 }
 
 template <typename T, int VEC, int NV, Rows ROWS>
@@ -474,10 +467,9 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
             uint8_t* to = ring + (size_t)s * place + (size_t)lane * pitch;
             uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + row_bytes;
             if (ROWS != kWhole) {
-                const bool first = t == 0, last = t == a.T - 1;
-                const uintptr_t b = lo;
-                window(b, row_bytes, first, last, lo, hi);
-                if (on && (first || last)) store_ends(to, p, row_bytes, lo, hi);
+                const uintptr_t b = lo, start = reinterpret_cast<uintptr_t>(rows);
+                copy_window(b, row_bytes, start, start + (uintptr_t)((a.T - 1) * pitch_of) * sizeof(T) + row_bytes, lo, hi);
+                if (on && (lo > b || hi < b + row_bytes)) store_ends(to, p, row_bytes, lo, hi);
                 to += lo - (b & ~uintptr_t(15));
             }
             const uint32_t bytes = on ? (uint32_t)(hi - lo) : 0;
