@@ -450,6 +450,7 @@ VH_API size_t vh_add_rmsnorm_grad_workspace_bytes(int T, int H);
  *
  *  dy, h, dh, dx  device, dtype [T][H]; dx may be dy, h or dh itself
  *  dweight        device, fp32 [H] (out) or NULL: not computed, ws may then be NULL
+ *                 (should a wait for a copy inside the kernel expire, the rows concerned and dweight are NaN)
  *  ws             device, 16-byte aligned, >= vh_add_rmsnorm_grad_workspace_bytes(T, H)
  */
 VH_API vh_status vh_add_rmsnorm_grad(const void* dy, const void* h, const void* weight, const void* dh, int dtype,

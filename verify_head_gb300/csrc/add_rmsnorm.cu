@@ -397,8 +397,9 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(const NormArgs a) {
 //   8192 x 2048 bf16: 29.6 us, against 30.2 us with the next token's vectors in registers, where 64 registers a
 //   thread left no room for a second token, and 42.1 us with a thread of the summing warps refilling.
 //   16384 x 512: 18.9 us, against 46.0 us with one token at a time.
-// Waits are for copies that the CTA has issued and for its own warps; should one expire (they are bounded) the
-// group's results are NaN.
+// Waits are for copies that the CTA has issued and for its own warps; should one expire (they are bounded) the results
+// of that group and of the CTA's later ones are NaN, no further copies are made, and the refilling warp waits (again with
+// a limit) for those in flight before it leaves.
 //
 // ROWS: whole aligned vectors of VEC elements; or rows that lie alike in their 16-byte slots (VEC as before); or rows of
 // any alignment (VEC 1).  In the last two a token's place holds the 16-byte granules that its row touches.  What those
@@ -428,6 +429,7 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
     extern __shared__ __align__(128) uint8_t ring[];  // [depth][ty tokens][h, dy, dh][pitch]
     __shared__ float2 red[2][32];
     __shared__ unsigned long long full[kMaxRing], empty[kMaxRing];
+    __shared__ volatile bool lost;  // a wait for a copy has expired
     const int workers = tx * ty;
     const int tid = threadIdx.x, lane = tid & 31;
     // this CTA's tokens are tok0, tok0 + period, ..: `mine` of them, in groups of ty
@@ -445,6 +447,7 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
             ptx::mbar_init(&full[i], 1);
             ptx::mbar_init(&empty[i], (uint32_t)workers / 32);
         }
+        lost = false;
         ptx::fence_barrier_init();
     }
     __syncthreads();
@@ -458,8 +461,9 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
         const int q = lane / 3, which = lane - 3 * q;
         const T* rows = static_cast<const T*>(which == 0 ? a.h : which == 1 ? a.dy : a.dh);
         const long long pitch_of = which == 0 ? a.h_stride : which == 1 ? a.dy_stride : a.dh_stride;
-        for (int i = 0, s = 0, ph = 1; i < n; ++i) {
-            if (!__all_sync(0xFFFFFFFFu, mbar_done(&empty[s], ph))) return;
+        int i = 0;
+        for (int s = 0, ph = 1; i < n; ++i) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_done(&empty[s], ph) && !lost)) break;
             const int i0 = (cta + i * stride) * ty;
             const bool on = rows != nullptr && q < min(ty, mine - i0);
             const long long t = tok0 + ((long long)i0 + q) * step;
@@ -483,6 +487,7 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
                 ph ^= 1;
             }
         }
+        for (int j = max(0, i - depth); j < i; ++j) ptx::mbar_drain(&full[j % depth], (uint32_t)(j / depth) & 1u);
         return;
     }
 
@@ -501,6 +506,7 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
                 load_weight<T, VEC>(a.w, a.w32, (size_t)v * VEC, a.w_offset, w[j]);
         }
     }
+    bool there = true;
     for (int i = 0, s = 0, ph = 0; i < n; ++i) {
         const int i0 = (cta + i * stride) * ty;
         const bool live = ry < mine - i0;
@@ -513,8 +519,8 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
         const T* hs = at(pl, a.h, a.h_stride);
         const T* ys = at(pl + pitch, a.dy, a.dy_stride);
         const T* es = at(pl + 2 * pitch, a.dh, a.dh_stride);
-        const bool there = mbar_done(&full[s], ph);
-        float ss = 0.f, dot = 0.f;
+        there = there && mbar_done(&full[s], ph);
+        float ss = there ? 0.f : quiet_nan(), dot = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int v = rx + j * tx;
@@ -542,7 +548,7 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
             }
         }
         const float2 tot = reduce_row<false>(ss, dot, red[i & 1] + ry * wpr, rx >> 5, wpr, sync);
-        const float rstd = there ? row_rstd(tot.x, a.inv_h, a.eps) : quiet_nan();
+        const float rstd = row_rstd(tot.x, a.inv_h, a.eps);
         const float back = -tot.y * rstd * rstd * rstd * a.inv_h;  // dx = rstd g + back h + dh
         T* dx = static_cast<T*>(a.dx) + token * a.dx_stride;
 #pragma unroll
@@ -569,6 +575,7 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
                 }
             }
         }
+        if (!there) lost = true;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&empty[s]);
         if (++s == depth) {
