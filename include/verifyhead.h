@@ -419,7 +419,9 @@ typedef enum { VH_NORM_SAME = 0, VH_NORM_INT8 = 1, VH_NORM_E4M3 = 2 } vh_norm_ou
  *     8 bits:        y = code of u * (Q * (1 / max|u|)), scales[t] = max|u| * rstd / Q, Q = 127 or 448,
  *                    rounded to nearest even, so that code * scale stands for u * rstd
  * The norm is taken of the fp32 sum; h is written rounded.  A row of zeros
- * has codes and scale 0; a row with an infinite or NaN element has scale NaN.
+ * has codes and scale 0.  A row with an infinite or NaN element, or an infinite
+ * or NaN product with the weight, has scale NaN, and so has one whose squares'
+ * sum is past fp32's range (its y is 0): elements from about 1e19 / sqrt(H) on.
  *
  *  x, residual  device, dtype [T][H] (residual may be NULL)
  *  weight       device, [H] of dtype, or fp32 when weight_f32 != 0; may be NULL

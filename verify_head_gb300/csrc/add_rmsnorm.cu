@@ -55,6 +55,13 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
+// The larger value; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Sums of two values over the threads of one row: wpr warps, of which this is number w; `row`: the row's wpr slots in
 // shared memory.  MAX_SECOND: the second value is a maximum instead of a sum.  sync(): a barrier of all threads that
 // call this together (not called where a row has one warp).  The lower half of a warp goes on with the first value and
@@ -63,7 +70,7 @@ template <bool MAX_SECOND, typename Sync>
 __device__ __forceinline__ float2 reduce_row(float a, float b, float2* row, int w, int wpr, Sync sync) {
     const int lane = threadIdx.x & 31;
     const bool second = lane >= 16;
-    auto join = [&](float v, float o) { return MAX_SECOND && second ? fmaxf(v, o) : v + o; };
+    auto join = [&](float v, float o) { return MAX_SECOND && second ? max_nan(v, o) : v + o; };
     const float other = __shfl_xor_sync(0xFFFFFFFFu, second ? a : b, 16);
     float v = join(second ? b : a, other);
 #pragma unroll
@@ -76,7 +83,7 @@ __device__ __forceinline__ float2 reduce_row(float a, float b, float2* row, int 
     for (int i = 1; i < wpr; ++i) {
         const float2 o = row[i];
         t.x += o.x;
-        t.y = MAX_SECOND ? fmaxf(t.y, o.y) : t.y + o.y;
+        t.y = MAX_SECOND ? max_nan(t.y, o.y) : t.y + o.y;
     }
     return t;
 }
@@ -128,6 +135,13 @@ __device__ __forceinline__ Quant make_quant(float amax, float q) {
     z.pre = amax < 1e-30f ? 18446744073709551616.0f : 1.0f;
     z.inv = amax > 0.0f ? q * (1.0f / (amax * z.pre)) : 0.0f;
     return z;
+}
+
+// A row's scale: NaN where the row, its sum of squares or a product with its weight is infinite or NaN, and 0 where all
+// products are 0, whatever rstd is (infinite for a row of zeros without eps).
+__device__ __forceinline__ float row_scale(float sum, float amax, float rstd, float q) {
+    const float inf = -neg_inf();
+    return !(sum < inf && amax < inf) ? quiet_nan() : amax > 0.f ? amax * rstd / q : 0.f;
 }
 
 // Codes of VEC elements.  |u inv| is at most Q up to a few roundings, so rounding cannot leave the codes' range.
@@ -281,7 +295,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a) {
             for (int k = 0; k < VEC; ++k) {
                 ss = fmaf(u[j][k], u[j][k], ss);
                 u[j][k] *= w[k];
-                amax = fmaxf(amax, fabsf(u[j][k]));
+                amax = max_nan(amax, fabsf(u[j][k]));
             }
         }
     }
@@ -326,7 +340,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a) {
                 }
             }
         }
-        if (threadIdx.x == 0) a.scales[row] = tot.y * rstd / q;
+        if (threadIdx.x == 0) a.scales[row] = row_scale(tot.x, tot.y, rstd, q);
     }
 }
 
@@ -356,7 +370,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(const NormArgs a) {
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
             ss = fmaf(hv[k], hv[k], ss);
-            amax = fmaxf(amax, fabsf(hv[k] * w[k]));
+            amax = max_nan(amax, fabsf(hv[k] * w[k]));
         }
     }
     const float2 tot = reduce_row<true>(ss, amax, red);
@@ -383,7 +397,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(const NormArgs a) {
             store_codes<VEC>(static_cast<uint8_t*>(a.y) + row * a.y_stride + (size_t)v * VEC, hv, z, a.out);
         }
     }
-    if (a.out != VH_NORM_SAME && threadIdx.x == 0) a.scales[row] = tot.y * rstd / q;
+    if (a.out != VH_NORM_SAME && threadIdx.x == 0) a.scales[row] = row_scale(tot.x, tot.y, rstd, q);
 }
 
 // ---------------------------------------------------------------------------
