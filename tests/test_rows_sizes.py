@@ -52,3 +52,17 @@ def test_calls(vh, given):
         vh.logits_logprobs_grad(wide, t, t.float(), t.float(), t.float(), dlogits=y.view(1, PAST) if given else None)
     with pytest.raises(ValueError):
         vh.logits_logprobs(wide[:, :100], t, 2 ** 32)
+
+
+@pytest.mark.gpu
+def test_most_rows(vh):
+    """2^31 - 1 rows: the launch's rounding up to whole blocks stays within 32 bits."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    x = torch.empty(2 ** 31 - 1, 1, dtype=torch.float16, device="cuda")
+    x.fill_(2.0)
+    x[-1] = -3.0
+    y = torch.zeros_like(x)
+    vh.add_rmsnorm(x, None, None, 1e-6, y=y)
+    # 2 / sqrt(4 + eps) and -3 / sqrt(9 + eps) round to 1 and -1 in 16 bits
+    assert float(y[-1]) == -1.0 and bool((y[:-1] == 1.0).all())

@@ -763,7 +763,7 @@ static cudaError_t norm_vec(const NormArgs& a, cudaStream_t s) {
     auto go = [&](auto kernel, int nv) {
         const int tx = row_threads(nvec, nv);
         const int ty = std::max(1, 128 / tx);
-        return launch(kernel, dim3((unsigned)((a.T + ty - 1) / ty)), dim3(tx, ty), 0, s, a);
+        return launch(kernel, dim3((unsigned)((a.T - 1) / ty + 1)), dim3(tx, ty), 0, s, a);
     };
     // Two vectors a thread: 16384 x 2048 bf16 36.8 us to int8, 40.4 us to bf16, against 42.4 / 41.2 us with one, 37.2 /
     // 41.1 us with four and 41.3 / 43.5 us with eight (a warp per row).  One where that leaves less than two warps.
