@@ -110,6 +110,17 @@ int as_count(PyObject* o) {
     return as_int(v);
 }
 
+// The call itself, without the interpreter's lock: a launch may wait for room in the stream's queue, and a host function
+// in that queue may want the lock.  The caller's arguments keep the tensors alive.
+template <typename F, typename... A>
+int launch(F f, A... a) {
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = f(a...);
+    Py_END_ALLOW_THREADS;
+    return st;
+}
+
 template <typename F>
 PyObject* call(Py_ssize_t n, Py_ssize_t wanted, F f) {
     long st = 1;
@@ -140,8 +151,8 @@ PyObject* add_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* yp = c.rows(a[5], T, H, out, &ys);
         void* hp = c.rows(a[6], T, H, type, &hs);
         float* sp = static_cast<float*>(c.vector(a[7], T, at::kFloat));
-        return p_add_rmsnorm(xp, rp, wp, row_type(type), f32, as_int(T), as_int(H), xs, rs, as_float(a[3]), as_float(a[4]), yp,
-                             ys, kind, hp, hs, sp, c.stream);
+        return launch(p_add_rmsnorm, xp, rp, wp, row_type(type), f32, as_int(T), as_int(H), xs, rs, as_float(a[3]),
+                      as_float(a[4]), yp, ys, kind, hp, hs, sp, c.stream);
     });
 }
 
@@ -164,8 +175,8 @@ PyObject* add_rmsnorm_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* xp = c.rows(a[6], T, H, type, &xs);
         float* dw = static_cast<float*>(c.vector(a[7], H, at::kFloat));
         void* ws = c.workspace(a[8], &bytes);
-        return p_add_rmsnorm_grad(yp, hp, wp, ep, row_type(type), f32, as_int(T), as_int(H), ys, hs, es, as_float(a[3]),
-                                  as_float(a[4]), xp, xs, dw, ws, bytes, c.stream);
+        return launch(p_add_rmsnorm_grad, yp, hp, wp, ep, row_type(type), f32, as_int(T), as_int(H), ys, hs, es,
+                      as_float(a[3]), as_float(a[4]), xp, xs, dw, ws, bytes, c.stream);
     });
 }
 
@@ -200,8 +211,8 @@ PyObject* logits_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* xp = c.rows(x, R, V, x.scalar_type(), &stride);
         const int32_t* tp = static_cast<const int32_t*>(c.vector(a[1], R, at::kInt));
         const Outputs o(c, a + 3, R, top, tp != nullptr);
-        return p_logits_logprobs(xp, row_type(x.scalar_type()), as_int(R), as_int(V), stride, tp, top, o.logprob, o.entropy,
-                                 o.lse, o.top_ids, o.top_logprobs, o.ws, o.bytes, c.stream);
+        return launch(p_logits_logprobs, xp, row_type(x.scalar_type()), as_int(R), as_int(V), stride, tp, top, o.logprob,
+                      o.entropy, o.lse, o.top_ids, o.top_logprobs, o.ws, o.bytes, c.stream);
     });
 }
 
@@ -218,8 +229,8 @@ PyObject* logits_logprobs_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const float* f[4];
         for (int i = 0; i < 4; ++i) f[i] = static_cast<const float*>(c.vector(a[2 + i], R, at::kFloat));
         void* dp = c.rows(a[6], R, V, x.scalar_type(), &ds);
-        return p_logits_logprobs_grad(xp, row_type(x.scalar_type()), as_int(R), as_int(V), xs, tp, f[0], f[1], f[2], f[3], dp,
-                                      ds, c.stream);
+        return launch(p_logits_logprobs_grad, xp, row_type(x.scalar_type()), as_int(R), as_int(V), xs, tp, f[0], f[1], f[2],
+                      f[3], dp, ds, c.stream);
     });
 }
 
@@ -238,8 +249,8 @@ PyObject* head_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int top = as_count(a[3]);
         const int32_t* tp = static_cast<const int32_t*>(c.vector(a[2], R, at::kInt));
         const Outputs o(c, a + 4, R, top, tp != nullptr);
-        return p_head_logprobs(x.data_ptr(), w.data_ptr(), tp, as_int(R), as_int(x.size(1)), as_int(w.size(0)), top, o.logprob,
-                               o.entropy, o.lse, o.top_ids, o.top_logprobs, o.ws, o.bytes, c.stream);
+        return launch(p_head_logprobs, x.data_ptr(), w.data_ptr(), tp, as_int(R), as_int(x.size(1)), as_int(w.size(0)), top,
+                      o.logprob, o.entropy, o.lse, o.top_ids, o.top_logprobs, o.ws, o.bytes, c.stream);
     });
 }
 
