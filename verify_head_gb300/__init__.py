@@ -450,6 +450,24 @@ def _setup():
     _f32, _i32 = torch.float32, torch.int32
 
 
+def _load_marshal():
+    """The compiled marshalling that was built for this interpreter and this torch, or None."""
+    from importlib import machinery, util
+    from . import buildlib as _b
+    _torch()
+    path = _b.marshal_path()
+    if not os.path.exists(path):
+        return None
+    try:
+        name = __name__ + "._marshal"
+        spec = util.spec_from_file_location(name, path, loader=machinery.ExtensionFileLoader(name, path))
+        m = util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        return m
+    except ImportError:
+        return None
+
+
 def _compiled_calls():
     """The compiled marshalling, bound to the loaded library, or False.  It takes the usual calls (outputs and
     workspace given, torch's current stream) and leaves every other to the checks below."""
@@ -457,11 +475,9 @@ def _compiled_calls():
     if _use_debug:
         return False
     if _compiled is None:
-        _torch()
         L = lib()
-        try:
-            from . import _marshal as m
-        except ImportError:
+        m = _load_marshal()
+        if m is None:
             _compiled = False
         else:
             for name in ("vh_add_rmsnorm", "vh_add_rmsnorm_grad", "vh_logits_logprobs", "vh_logits_logprobs_grad",

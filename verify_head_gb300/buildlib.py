@@ -2,15 +2,16 @@
 
 Each .cu file under csrc/ is compiled in parallel, then linked into one
 shared library next to this file.  Only one -gencode (sm_103a); host code is
-portable (x86_64 and aarch64).  Beside it _marshal.so, the compiled argument
-marshalling of the norm and log-probability calls: it needs Python's and
-torch's headers, and where they are missing the binding marshals in Python.
+portable (x86_64 and aarch64).  Beside it _marshal_<versions>.so, the compiled
+argument marshalling of the norm and log-probability calls: it needs Python's
+and torch's headers, and where they are missing the binding marshals in Python.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -21,7 +22,6 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libverifyhead.so")
 LIB_DEBUG = os.path.join(HERE, "libverifyhead_debug.so")  # -DVH_DEBUG: device-side index guards
-MARSHAL = os.path.join(HERE, "_marshal.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
@@ -53,30 +53,40 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def marshal_path() -> str:
+    """Where the marshalling for the running interpreter and torch lies.  It reads tensors by torch's own layout, so a
+    file that was compiled against another Python, torch or C++ ABI must not be loaded: the name says which they were."""
+    import torch
+    tag = "-".join((sysconfig.get_config_var("SOABI") or sys.implementation.cache_tag, torch.__version__,
+                    str(getattr(torch.version, "git_version", ""))[:10], f"abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"))
+    return os.path.join(HERE, "_marshal_" + re.sub(r"[^0-9A-Za-z.]+", "_", tag) + ".so")
+
+
 def build_marshal(force: bool = False):
-    """Compiles _marshal.so with the host compiler against the running torch; returns its path, or None (with the
+    """Compiles the marshalling with the host compiler against the running torch; returns its path, or None (with the
     compiler's message on stderr) where that is not possible."""
     deps = (MARSHAL_SRC, os.path.join(ROOT, "include", "verifyhead.h"))
-    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
-        return MARSHAL
     try:
         import torch
+        out = marshal_path()
+        if not force and os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps):
+            return out
         top = os.path.dirname(torch.__file__)
         cuda = os.path.dirname(os.path.dirname(nvcc()))
         inc = [os.path.join(top, "include"), os.path.join(top, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
         lib = os.path.join(top, "lib")
-        tmp = MARSHAL + f".tmp{os.getpid()}"
+        tmp = out + f".tmp{os.getpid()}"
         cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-I" + p for p in inc), MARSHAL_SRC,
                "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath," + lib]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(r.stderr[-2000:])
-        os.replace(tmp, MARSHAL)
-        return MARSHAL
+        os.replace(tmp, out)
+        return out
     except (ImportError, OSError, RuntimeError, AttributeError) as e:
-        print(f"_marshal.so was not built (calls are marshalled in Python): {e}", file=sys.stderr)
+        print(f"the compiled marshalling was not built (calls are marshalled in Python): {e}", file=sys.stderr)
         return None
 
 
