@@ -63,3 +63,39 @@ def test_rows_shorter_than_a_granule(vh, T, H, dtype):
         dy, h, e = (rows(g, T, H, dtype, pitch=pitch, offset=offset) for _ in range(3))
         dx, dw = vh.add_rmsnorm_grad(dy, h, w, 1e-6, dh=e)
         check(dx, dw, dy, h, w, e, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("T,H", [(1, 1), (9, 5), (700, 33), (2, 255), (300, 257), (13, 2561), (5, 4096), (5, 4097), (1, 8191),
+                                 (3, 8192), (2, 8200)])
+@pytest.mark.parametrize("which", ["dy", "dh", "pitch"])
+def test_rows_that_lie_differently(vh, T, H, dtype, which):
+    """One tensor of another alignment, or of rows another distance apart, than the rest."""
+    g = torch.Generator().manual_seed(T * 7 + H)
+    dy = rows(g, T, H, dtype, offset=3 if which == "dy" else 1)
+    h = rows(g, T, H, dtype, 2.0, offset=1)
+    e = rows(g, T, H, dtype, offset=2 if which == "dh" else 1, pitch=H + 3 if which == "pitch" else None)
+    w = (1 + 0.1 * torch.randn(H + 1, generator=g)).to(dtype).cuda()[1:]
+    dx = rows(g, T, H, dtype, pitch=H + 5, offset=1)
+    whole = torch.empty(0, dtype=dtype, device="cuda").set_(dx.untyped_storage())
+    whole.fill_(7.0)
+    _, dw = vh.add_rmsnorm_grad(dy, h, w, 1e-6, dh=e, dx=dx)
+    check(dx, dw, dy, h, w, e, dtype)
+    mask = torch.ones_like(whole, dtype=torch.bool)
+    mask.as_strided((T, H), (H + 5, 1), 1).fill_(False)
+    assert bool((whole[mask] == 7.0).all())  # nothing beside the rows was written
+    if which != "pitch":
+        assert torch.equal(vh.add_rmsnorm_grad(dy, h, w, 1e-6, dh=e, dx=dy)[0], dx)  # on its input
+    alone, none = vh.add_rmsnorm_grad(rows(g, T, H, dtype, offset=5), h, None, 1e-6)
+    assert none is None and bool(torch.isfinite(alone.float()).all())
+
+
+@pytest.mark.parametrize("H", [8186, 8187, 8190, 8191])
+def test_widest_single_precision_rows(vh, H):
+    """On either side of the widest rows that go by slots."""
+    g = torch.Generator().manual_seed(H)
+    w = (1 + 0.1 * torch.randn(H, generator=g)).cuda()
+    for T in (1, 7, 400):
+        dy, h, e = (rows(g, T, H, F32, s) for s in (1.0, 2.0, 1.0))
+        dx, dw = vh.add_rmsnorm_grad(dy, h, w, 1e-6, dh=e)
+        check(dx, dw, dy, h, w, e, F32)
