@@ -38,7 +38,7 @@ constexpr int kPerSm = 4, kPerSmTop = 3;
 constexpr int kTargetCtas = 152 * kPerSm;
 constexpr int kMinSegs = 2 * kWarpsL;  // segments per CTA below which the work is not cut further
 constexpr int kShortSegs = 64;         // segments per CTA up to which a call is short
-constexpr int kWholeSegs = 64, kRowSegs = 128;
+constexpr int kWholeSegs = 64, kRowSegs = 129;  // see plan
 
 // A row as aligned 32-byte slots: slot v holds elements [v * kSlot - shift, +kSlot).
 constexpr int kSlotBytes = 32;
@@ -102,7 +102,8 @@ struct RowUnits {
     }
 };
 
-// Upper bound of the segments of a row of V elements of `size` bytes, whatever its alignment.
+// Upper bound of the segments of a row of V elements of `size` bytes, whatever its alignment: what the call's rows are
+// counted by.  It is one more than an aligned row of whole segments has (65 for 32,768 elements of 16 bits, 129 for 65,536).
 __host__ __device__ inline int max_segs(int V, int size) {
     const long long per = 32 * kSlotBytes / size;
     return (int)(((long long)V + kSlotBytes / size - 1 + per - 1) / per);
@@ -111,7 +112,8 @@ __host__ __device__ inline int max_segs(int V, int size) {
 // The call's units are the R x segs segments, cut into one range per CTA: every CTA has the same work to within a
 // segment, whatever R and V.  A range holds whole rows and, at its ends, pieces of rows that other CTAs share.
 // Rows of up to kSlotSegs segments keep the maximum of every slot for the alternatives, longer ones that of every
-// segment: there have to be clearly more units than alternatives, and a row of 65,536 bf16 has 128 segments.
+// segment: there have to be clearly more units than alternatives.  At the limit the two cost the same (64 to 300 rows of
+// 131,072 bf16 and 1024 of 65,536 fp32, of 257 segments each, with 20 alternatives: within 2% either way).
 constexpr int kSlotSegs = 256;
 __host__ __device__ inline int row_units(int row_segs) { return row_segs <= kSlotSegs ? row_segs * 32 : row_segs; }
 
@@ -129,11 +131,13 @@ constexpr size_t kPartEnd = kTicketEnd + (size_t)kTargetCtas * 2 * 16;
 // after the other, but all CTAs have the same work.  So rows are cut for short calls (231 x 32768 bf16: 7.9 against
 // 10.0 us) and where that fills three quarters of the SMs' places (600 x 65536: 14.6 against 18.9 us; with half of
 // them, 310 x 131072, 23.8 against 19.0 us).
-// More rows than places: a CTA each up to kRowSegs segments (1645 x 32768: 21.9 against 24.5 us, 1024 x 65536: 26.1
-// against 27.0 us), even ranges above, where a last wave of few CTAs would weigh more; with alternatives, whose calls
-// write every unit's maximum, even ranges (1645 x 32768: 39.8 against 40.2 us).
+// More rows than places: a CTA each up to kRowSegs segments, which rows of 65,536 elements of 16 bits have (1645 x 32768:
+// 21.9 against 24.5 us, 1024 x 65536: 25.9 against 27.7 us, 2048 x 65536: 46.1 against 47.3 us; 610 x 65536, hardly more
+// rows than places, 19.6 against 18.9 us), even ranges above, where a last wave of few CTAs would weigh more; with
+// alternatives, whose calls write every unit's maximum, even ranges (1645 x 32768: 39.8 against 40.2 us).
 // The last piece's CTA joins a row, which takes 1.2 us: rows of up to kWholeSegs segments stay whole (44 x 21479: 4.5
-// against 5.7 us; 2 x 65536 with 128 segments 5.8 against 4.6 us).
+// against 5.7 us; whole rows of 65 segments, 32,768 bf16: 231 rows 9.0 against 8.2 us cut, 304 rows 6.6 against 8.1 us,
+// 16 rows 5.0 against 4.8 us).
 inline void plan(int R, int segs, bool top, int& n, int& k) {
     const long long units = (long long)R * segs;
     const int wave = 152 * (top ? kPerSmTop : kPerSm);
