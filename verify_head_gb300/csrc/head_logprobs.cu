@@ -161,7 +161,8 @@ __device__ __forceinline__ void find_bounds(const Args& a, const Rows& rw, int c
         all = __shfl_sync(0xFFFFFFFFu, lane == 0 ? *seen : 0u, 0) == (uint32_t)(kEpiWarps * n_cta);
     }
     if (!all) return;
-    __threadfence();
+    __threadfence();  // lane 0 saw the count: what the epilogue warps wrote before is then seen by all lanes
+    __syncwarp();
     for (int r = cta; r < rows; r += n_cta) {
         const uint32_t b = nth_largest(a.seg_max + (size_t)(row0 + r) * a.segs, first_segs, a.top_n);
         if (lane == 0) shared[r] = b;
