@@ -487,7 +487,10 @@ __global__ void __launch_bounds__(kMaxThreads + 32)
             if (ROWS != kWhole) {
                 const uintptr_t b = lo, start = reinterpret_cast<uintptr_t>(rows);
                 copy_window(b, row_bytes, start, start + (uintptr_t)((a.T - 1) * pitch_of) * sizeof(T) + row_bytes, lo, hi);
-                if (on && (lo > b || hi < b + row_bytes)) store_ends(to, p, row_bytes, lo, hi);
+                if (on && (lo > b || hi < b + row_bytes)) {
+                    store_ends(to, p, row_bytes, lo, hi);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a later token's copy goes there
+                }
                 to += lo - (b & ~uintptr_t(15));
             }
             const uint32_t bytes = on ? (uint32_t)(hi - lo) : 0;
