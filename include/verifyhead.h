@@ -402,7 +402,8 @@ VH_API vh_status spec_verify_greedy_nvfp4_packed(const void* hidden, const void*
  * case, and a result is rounded to the row type once.  Strides are in
  * elements between rows; the elements of a row are contiguous.  Any width,
  * stride and element-aligned address is taken; 16-byte aligned rows of whole
- * 16-byte vectors are read fastest.
+ * 16-byte vectors are read fastest.  The 8-bit rows are for the caller's own
+ * 8-bit layers: no call of this library takes them.
  * ------------------------------------------------------------------------ */
 typedef enum { VH_F32 = 0, VH_BF16 = 1, VH_F16 = 2 } vh_dtype;
 
@@ -492,8 +493,11 @@ VH_API vh_status vh_logits_logprobs(const void* logits, int dtype, int R, int V,
 /*
  * Gradient of vh_logits_logprobs with respect to the logits:
  *     dlogits[r,v] = g_logprob[r] * ([v == tokens[r]] - p_v) - g_entropy[r] * p_v * (log p_v + entropy[r])
- * from the forward pass's lse and entropy.  Either gradient may be NULL (then
- * tokens, or entropy, may be too).  Masked places have p = 0; a token outside
+ * from the forward pass's lse and entropy: p_v = exp(logits - lse), so that lse
+ * as an fp32 number gives p a relative error of |lse| 2^-24.  A row with nothing
+ * but a far mask value in it (-1e10, the type's lowest) keeps its statistics but
+ * has no gradient to speak of: give it g_logprob and g_entropy 0.
+ * Either gradient may be NULL (then tokens, or entropy, may be too).  Masked places have p = 0; a token outside
  * [0, V) contributes nothing; a row whose lse is -inf has gradient 0, one
  * whose lse is NaN has NaN.
  *

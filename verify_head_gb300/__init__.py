@@ -431,7 +431,8 @@ def spec_verify_greedy_nvfp4_packed(hidden, packed, tensor_scale, draft_ids, B: 
 
 
 # ----------------------------------------------------------------------------
-# Norm and log probabilities.
+# Norm and log probabilities.  None of these calls is recorded by autograd: results of inputs that require a gradient are
+# cut off from them, and the gradients are the _grad calls' (to be called from a torch.autograd.Function, say).
 
 _dtypes = {}  # torch dtype -> vh_dtype
 _f32 = _i32 = None  # torch.float32, torch.int32
@@ -617,7 +618,8 @@ def add_rmsnorm(x, residual=None, weight=None, eps: float = 1e-6, weight_offset:
 def add_rmsnorm_q8(x, residual=None, weight=None, eps: float = 1e-6, weight_offset: float = 0.0, q=None, scales=None,
                    h=None, dtype=None, stream=None):
     """add_rmsnorm with 8-bit rows: q [T,H] (torch.int8, or torch.float8_e4m3fn; `dtype` where q is not given) and
-    scales [T] fp32 with q * scales[:, None] standing for the normed rows.  -> (q, scales, h)"""
+    scales [T] fp32 with q * scales[:, None] standing for the normed rows, for layers of the caller's that take 8-bit rows.
+    -> (q, scales, h)"""
     if stream is None and q is not None and scales is not None and dtype is None:
         m = _compiled_calls()
         if m:
@@ -744,7 +746,8 @@ def logits_logprobs(logits, tokens, top_n: int = 0, logprob=None, entropy=None, 
 
 def logits_logprobs_grad(logits, tokens, lse, entropy=None, g_logprob=None, g_entropy=None, dlogits=None, stream=None):
     """Gradient of logits_logprobs' logprob and entropy (their gradients [R] fp32, either may be None) with respect to
-    the logits, from the lse and entropy it returned; dlogits may be `logits` itself.  -> dlogits [R,V]"""
+    the logits, from the lse and entropy it returned; dlogits may be `logits` itself.  Rows that hold nothing but a far mask
+    value (-1e10, the type's lowest) want gradients of 0: their lse in fp32 says too little.  -> dlogits [R,V]"""
     if stream is None and dlogits is not None:
         m = _compiled_calls()
         if m:

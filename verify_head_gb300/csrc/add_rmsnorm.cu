@@ -423,6 +423,8 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_wide(const NormArgs a) {
 // start only: so a thread's vectors hold the same columns of every token, as its weights and its share of dw need.
 //   8191 x 2561 bf16: 98.9 us with loads of single elements, 63.1 us element by element out of the ring, 43 us by slots;
 //   2047 x 8191: 61 and 41 us, 16383 x 257: 40 and 21 us, 4000 x 1025 fp16: 19 and 20 us.
+// kAny is left with rows that lie differently in each tensor and fp32 rows too wide for slots; from 4,097 elements on, 16 a
+// thread, it spills registers.
 enum Rows { kWhole, kAlike, kAny };
 
 // What a row at `p` holds outside [lo, hi), into its place.

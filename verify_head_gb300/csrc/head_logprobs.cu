@@ -16,11 +16,12 @@
 // Epilogue.  An accumulator lane is a head row and a column a hidden row, but
 // a row's softmax runs over head rows.  Each warp turns its 32 x 32 blocks in
 // shared memory and then lane = hidden row: 32 scores in registers, a running
-// maximum and the sums of Stat per hidden row, kept across tiles.  About 10
-// instructions per score: with eight warps the epilogue of a tile is shorter
-// than its MMAs from H = 512 up (584 rows of 65,536 x 256, where it is not,
-// 20 alternatives: 68 us, against 114 us with four warps and 80 us with
-// sixteen on blocks of 16 hidden rows).
+// maximum and the sums of Stat per hidden row, kept across tiles.  A warp
+// loads, turns and sums one block after the other, so a tile's epilogue is a
+// chain of waits and not of instructions: two warps per scheduler hide it
+// under the MMAs of long rows (H from 512 up), but not of short ones (584 rows
+// of 65,536 x 256: 43 us, with 20 alternatives 73 us, against 114 us with four
+// warps and 80 us with sixteen on blocks of 16 hidden rows).
 //
 // Alternatives.  Where they are wanted each block of 32 head rows (a segment)
 // leaves its maximum per hidden row in the workspace, and its 32 scores unless

@@ -56,7 +56,6 @@ struct RawVec<T, 1> {
     T v;
     __device__ __forceinline__ float get(int) const { return to_f32(v); }
     __device__ __forceinline__ void set(int, float f) { v = from_f32<T>(f); }
-    __device__ __forceinline__ void clear() { v = from_f32<T>(0.f); }
     __device__ __forceinline__ void load(const T* p) { v = *p; }
     __device__ __forceinline__ void store(T* p) const { *p = v; }
 };
@@ -111,10 +110,6 @@ struct RawVec {
             const uint32_t h = *reinterpret_cast<const uint16_t*>(&v);
             u[i >> 1] = (i & 1) ? (u[i >> 1] & 0xFFFFu) | (h << 16) : (u[i >> 1] & 0xFFFF0000u) | h;
         }
-    }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < N; ++i) u[i] = 0u;
     }
     __device__ __forceinline__ void fill_lowest() {  // -inf
 #pragma unroll
