@@ -770,7 +770,8 @@ static cudaError_t norm_vec(const NormArgs& a, cudaStream_t s) {
         const int ty = std::max(1, 128 / tx);
         return launch(kernel, dim3((unsigned)((a.T - 1) / ty + 1)), dim3(tx, ty), 0, s, a);
     };
-    // Two vectors a thread: 16384 x 2048 bf16 36.8 us to int8, 40.4 us to bf16, against 42.4 / 41.2 us with one, 37.2 /
+    // Two vectors a thread: 16384 x 2048 bf16 36.8 us to int8, 40.4 us to bf16 (36.4 / 40.8 since the kernel lets no other
+    // start early), against 42.4 / 41.2 us with one, 37.2 /
     // 41.1 us with four and 41.3 / 43.5 us with eight (a warp per row).  One where that leaves less than two warps.
     if (nvec <= 64) return go(k_norm<T, VEC, 1, SHIFT>, 1);
     if (nvec <= kMaxThreads * 2) return go(k_norm<T, VEC, 2, SHIFT>, 2);
