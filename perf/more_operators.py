@@ -238,7 +238,8 @@ def _plain_round(x, tensor_scale):
     x = x.float()
     scale = tensor_scale
     if scale is None:
-        scale = x.abs().amax(1, keepdim=True) / TOP
+        scale = x.abs().amax(1, keepdim=True)
+        scale = scale / torch.full_like(scale, TOP)  # the quotient: a number's reciprocal would be multiplied with
     else:
         scale = torch.full((T, 1), scale, dtype=torch.float32, device=x.device)
     b = x.view(T, H // 16, 16).double()
@@ -405,7 +406,7 @@ def _exact_round(x, tensor_scale):
     x = x.double()
     T, H = x.shape
     if tensor_scale is None:
-        g = (x.abs().max(1).values.float() / TOP).double()
+        g = (x.abs().max(1).values / TOP).float().double()
     else:
         g = torch.tensor(tensor_scale, dtype=torch.float32).double().to(x.device).expand(T)
     blocks = x.reshape(-1, 16)
