@@ -530,6 +530,146 @@ VH_API vh_status vh_head_logprobs(const void* hidden, const void* W_full, const 
                                   int top_n, float* logprob, float* entropy, float* lse, int32_t* top_ids,
                                   float* top_logprobs, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * 4-bit rows (the NVFP4 format of mtp_draft_head_argmax_nvfp4): made from rows
+ * of numbers, turned back, and multiplied with one another.  The source pages
+ * name the format ("为什么生产推理我默认 vLLM" §3) and not how rows get into
+ * it; a 4-bit head is made by these calls, and an engine multiplies 4-bit
+ * activations with 4-bit weights.
+ *
+ * Tiled layout, which the product reads: records of 128 rows x 256 elements,
+ * ceil(H / 256) of them per 128 rows, at byte 18432 * ((row / 128) * ceil(H /
+ * 256) + element / 256).  Of line r = row % 128 and block k = (element % 256) /
+ * 16 a record holds
+ *   [r*128 + ((k/2) ^ (r%8))*16 + (k%2)*8, +8): the 8 code bytes (element 2i in
+ *       the low half of byte i);
+ *   [16384 + (k/4)*512 + (r%32)*16 + (r/32)*4 + k%4]: the scale (e4m3, >= 0).
+ * Blocks past H are zero; lines past the last row may hold anything.
+ * Rows made by these calls may be any call's rows or table: no kernel that
+ * writes them lets the next one start early.
+ * ------------------------------------------------------------------------ */
+
+/* ceil(rows / 128) * ceil(H / 256) * 18432; 0 unless rows >= 1 and 16 <= H <= 65536, H % 16 == 0. */
+VH_API size_t vh_nvfp4_tiles_bytes(int rows, int H);
+
+/*
+ * T rows of width H to 4 bits:
+ *     g = tensor_scale, or for each row fp32(max|row| / 2688) -> row_scales
+ *     s = max|block| / (6 g) as e4m3,  c = x / (s g) as e2m1
+ * per block of 16, both to the nearest with ties to even, saturating at 448
+ * and 6, and decided as the exact quotients are; c is 0 where s is, and a zero
+ * has no sign.  With a tensor scale a block with an infinite or NaN element
+ * has scale NaN (0x7F) and codes 0; with row scales its row has row scale NaN,
+ * scales and codes 0.
+ *
+ *  x           device, dtype [T][H], x_stride >= H elements between rows
+ *  tensor_scale  > 0, finite; ignored when row_scales is given
+ *  codes       device, uint8 [T][H/2] (out), 8-byte aligned; or, with scales
+ *              NULL, the tiled layout (vh_nvfp4_tiles_bytes(T, H) bytes, 16-byte aligned)
+ *  scales      device, uint8 [T][H/16] (out), or NULL
+ *  row_scales  device, fp32 [T] (out), or NULL
+ *  T >= 1; 16 <= H <= 65536, H % 16 == 0
+ * The outputs may not overlap x.
+ */
+VH_API vh_status vh_nvfp4_quantize(const void* x, int dtype, int T, int H, int64_t x_stride, float tensor_scale,
+                                   uint8_t* codes, uint8_t* scales, float* row_scales, void* stream);
+
+/* Row-major codes [V][H/2] (8-byte aligned) and scales [V][H/16] -> the tiled layout (16-byte aligned,
+ * vh_nvfp4_tiles_bytes(V, H) bytes, else VH_ERR_WORKSPACE), whose lines past V are zero. */
+VH_API vh_status vh_nvfp4_tile(const uint8_t* codes, const uint8_t* scales, int V, int H, uint8_t* tiles,
+                               size_t tiles_bytes, void* stream);
+
+/*
+ * The values of 4-bit rows: y = (code * scale) * g, rounded to dtype once;
+ * code * scale is exact.  A NaN scale gives NaN.
+ *
+ *  codes, scales  as for vh_nvfp4_quantize (scales NULL: the tiled layout)
+ *  g              row_scales [T] (device, fp32), or tensor_scale where that is NULL
+ *  y              device, dtype [T][H] (out), y_stride >= H
+ */
+VH_API vh_status vh_nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int T, int H, float tensor_scale,
+                                     const float* row_scales, int dtype, void* y, int64_t y_stride, void* stream);
+
+/*
+ * Product of two 4-bit matrices in the tiled layout:
+ *     y[t,v] = x_g(t) * w_g(v) * sum_h (code * scale of X)[t,h] * (code * scale of W)[v,h]
+ * on the block-scaled 4-bit tensor cores, fp32 accumulation, one rounding to
+ * dtype.  g is a row's entry of the array, or the number where that is NULL.
+ * W is read before the previous kernel of the stream has finished (see
+ * mtp_draft_head_argmax), X and the arrays after.
+ *
+ *  x        device, tiled [T][H], 16-byte aligned
+ *  w        device, tiled [V][H], 16-byte aligned
+ *  x_scales device, fp32 [T], or NULL;  w_scales device, fp32 [V], or NULL
+ *  x_scale, w_scale  finite; ignored where the array is given
+ *  y        device, dtype [T][V] (out), y_stride >= V elements between rows
+ *  T >= 1;  V >= 1;  16 <= H <= 65536, H % 16 == 0
+ * Should a wait inside the kernel expire (see vh_workspace_error_offset), the
+ * tile concerned is NaN.
+ */
+VH_API vh_status vh_nvfp4_matmul(const uint8_t* x, float x_scale, const float* x_scales, const uint8_t* w, float w_scale,
+                                 const float* w_scales, int T, int V, int H, int dtype, void* y, int64_t y_stride,
+                                 void* stream);
+
+/* ------------------------------------------------------------------------
+ * What a server does to logits before it picks a token, or a trainer to those
+ * of a policy: biases, penalties for repeated tokens, temperature, grammar
+ * masks.  No counterpart in the source pages.
+ *
+ * The R rows belong to S = R / rows_per_seq sequences, rows_per_seq rows after
+ * one another (the k + 1 positions of a verify round, or one).  Every pointer
+ * is a device pointer, and each may be NULL: the rule is then left out.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    const int32_t* history;      /* [S][history_width]: the sequence's tokens, prompt first; ids outside [0,V) are passed over */
+    int64_t history_stride;      /* elements between its rows, >= history_width */
+    int history_width;
+    const int32_t* history_len;  /* [S]: tokens of the row that count (at most history_width); NULL: all.  Both lengths are
+                                    ignored without a history */
+    const int32_t* prompt_len;   /* [S]: the first so many are the prompt's, the others output; NULL: 0 */
+    const int32_t* draft_ids;    /* [S][rows_per_seq - 1]: row j also counts the first j of them as output */
+    const float* repetition;     /* [S] > 0 */
+    const float* frequency;      /* [S] */
+    const float* presence;       /* [S] */
+    const float* temperature;    /* [S]; 0 and less stand for 1 (a greedy sequence) */
+    const int32_t* bias_ids;     /* [S][n_bias]: ids outside [0,V) are passed over, the last entry of an id counts */
+    const float* bias;           /* [S][n_bias] */
+    int n_bias;                  /* 0..65535 */
+    const int32_t* allowed;      /* [R][>= ceil(V/32)]: bit v % 32 of word v / 32 set where token v may follow */
+    int64_t allowed_stride;      /* words between its rows */
+} vh_logits_rules;
+
+/*
+ * For row r of sequence s, with n the occurrences of token v in history and
+ * draft and m those among them in output and draft:
+ *     z = logits[r,v] + bias of v
+ *     z = z > 0 ? z / repetition : z * repetition     where n > 0
+ *     z = z - frequency * m - presence * [m > 0]
+ *     out[r,v] = z / temperature                      -inf where v is not allowed
+ * in fp32, rounded to out's type once.  Not allowed places are not looked at
+ * (NaN there is gone too); a row may have none left.
+ *
+ *  logits     device, dtype [R][V];  out device, out_dtype (dtype or VH_F32) [R][V] (out), may be logits itself
+ *             (same address, stride and type)
+ *  R >= 1, R % rows_per_seq == 0, 1 <= V <= 2^31 - 1024; strides >= V
+ */
+VH_API vh_status vh_logits_process(const void* logits, int dtype, int R, int V, int64_t stride, int rows_per_seq,
+                                   const vh_logits_rules* rules, void* out, int out_dtype, int64_t out_stride,
+                                   void* stream);
+
+/*
+ * Its gradient with respect to the logits:
+ *     dlogits = dout / temperature, divided (z > 0) or multiplied by repetition where n > 0; 0 where v is not allowed
+ * z is logits + bias.  frequency and presence do not matter, nor bias but for
+ * its sign of z.
+ *
+ *  dout, logits  device, dtype [R][V];  dlogits device, dtype [R][V] (out), may be dout itself
+ */
+VH_API vh_status vh_logits_process_grad(const void* dout, const void* logits, int dtype, int R, int V,
+                                        int64_t dout_stride, int64_t logits_stride, int rows_per_seq,
+                                        const vh_logits_rules* rules, void* dlogits, int64_t dlogits_stride,
+                                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -9,7 +9,10 @@ Entry points mirror the C ABI in include/verifyhead.h:
     mtp_draft_head_argmax, mtp_draft_head_argmax_nvfp4,
     spec_verify_greedy (spec_verify_greedy_path), vh_workspace_bytes,
     vh_add_rmsnorm (add_rmsnorm, add_rmsnorm_q8, add_rmsnorm_grad),
-    vh_logits_logprobs (logits_logprobs, logits_logprobs_grad), vh_head_logprobs (head_logprobs).
+    vh_logits_logprobs (logits_logprobs, logits_logprobs_grad), vh_head_logprobs (head_logprobs),
+    vh_nvfp4_quantize (nvfp4_quantize, nvfp4_quantize_tiles), vh_nvfp4_tile (nvfp4_tile),
+    vh_nvfp4_dequantize (nvfp4_dequantize, nvfp4_dequantize_tiles), vh_nvfp4_matmul (nvfp4_matmul),
+    vh_logits_process (logits_process, logits_process_grad).
 """
 from __future__ import annotations
 
@@ -51,7 +54,8 @@ EXPORTS = (
     "mtp_draft_head_argmax_nvfp4_packed", "spec_verify_greedy_nvfp4_packed",
     "vh_add_rmsnorm", "vh_add_rmsnorm_grad", "vh_add_rmsnorm_grad_workspace_bytes", "vh_logits_logprobs",
     "vh_logits_logprobs_workspace_bytes", "vh_logits_logprobs_grad", "vh_head_logprobs",
-    "vh_head_logprobs_workspace_bytes",
+    "vh_head_logprobs_workspace_bytes", "vh_nvfp4_tiles_bytes", "vh_nvfp4_quantize", "vh_nvfp4_tile",
+    "vh_nvfp4_dequantize", "vh_nvfp4_matmul", "vh_logits_process", "vh_logits_process_grad",
 )
 
 
@@ -104,6 +108,15 @@ def debug_library():
         yield _debug_lib
     finally:
         _use_debug = prev
+
+
+class LogitsRules(ctypes.Structure):
+    """vh_logits_rules."""
+    _fields_ = [("history", ctypes.c_void_p), ("history_stride", ctypes.c_int64), ("history_width", ctypes.c_int),
+                ("history_len", ctypes.c_void_p), ("prompt_len", ctypes.c_void_p), ("draft_ids", ctypes.c_void_p),
+                ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("temperature", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("n_bias", ctypes.c_int), ("allowed", ctypes.c_void_p), ("allowed_stride", ctypes.c_int64)]
 
 
 def _declare(L):
@@ -164,6 +177,21 @@ def _declare(L):
     L.vh_head_logprobs_workspace_bytes.argtypes = [i32, i32, i32]
     L.vh_head_logprobs.restype = i32
     L.vh_head_logprobs.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.vh_nvfp4_tiles_bytes.restype = sz
+    L.vh_nvfp4_tiles_bytes.argtypes = [i32, i32]
+    L.vh_nvfp4_quantize.restype = i32
+    L.vh_nvfp4_quantize.argtypes = [vp, i32, i32, i32, i64, f32, vp, vp, vp, vp]
+    L.vh_nvfp4_tile.restype = i32
+    L.vh_nvfp4_tile.argtypes = [vp, vp, i32, i32, vp, sz, vp]
+    L.vh_nvfp4_dequantize.restype = i32
+    L.vh_nvfp4_dequantize.argtypes = [vp, vp, i32, i32, f32, vp, i32, vp, i64, vp]
+    L.vh_nvfp4_matmul.restype = i32
+    L.vh_nvfp4_matmul.argtypes = [vp, f32, vp, vp, f32, vp, i32, i32, i32, i32, vp, i64, vp]
+    rules = ctypes.POINTER(LogitsRules)
+    L.vh_logits_process.restype = i32
+    L.vh_logits_process.argtypes = [vp, i32, i32, i32, i64, i32, rules, vp, i32, i64, vp]
+    L.vh_logits_process_grad.restype = i32
+    L.vh_logits_process_grad.argtypes = [vp, vp, i32, i32, i32, i64, i64, i32, rules, vp, i64, vp]
     L.spec_verify_greedy_path.restype = i32
     L.spec_verify_greedy_path.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp, i32]
 
@@ -482,7 +510,8 @@ def _compiled_calls():
             _compiled = False
         else:
             for name in ("vh_add_rmsnorm", "vh_add_rmsnorm_grad", "vh_logits_logprobs", "vh_logits_logprobs_grad",
-                         "vh_head_logprobs"):
+                         "vh_head_logprobs", "vh_nvfp4_tiles_bytes", "vh_nvfp4_quantize", "vh_nvfp4_dequantize",
+                         "vh_nvfp4_matmul", "vh_logits_process", "vh_logits_process_grad"):
                 m.bind(name, ctypes.cast(getattr(L, name), ctypes.c_void_p).value)
             _compiled = m
     return _compiled
@@ -809,3 +838,290 @@ def head_logprobs(hidden, W_full, tokens, top_n: int = 0, logprob=None, entropy=
     st = lib().vh_head_logprobs(hidden.data_ptr(), W_full.data_ptr(), tp, R, H, V, top_n, *at, _stream_on(stream, dev))
     _check(st, "head_logprobs")
     return _logprob_results(outs, tokens)
+
+
+# ----------------------------------------------------------------------------
+# 4-bit rows.  As above, nothing here is recorded by autograd.
+
+
+def vh_nvfp4_tiles_bytes(rows: int, H: int) -> int:
+    """Bytes of a 4-bit matrix [rows, H] in the tiled layout."""
+    _int32(rows, H)
+    return int(lib().vh_nvfp4_tiles_bytes(rows, H))
+
+
+def _scale(scale, name, dev, rows):
+    """(number, address) of a tensor scale (a number) or row scales (fp32 [rows])."""
+    if isinstance(scale, _torch().Tensor):
+        return 0.0, _vector(scale, name, dev, rows, _f32)
+    return float(scale), None
+
+
+def _bytes(t, name, dev, shape):
+    """Checks a contiguous uint8 CUDA tensor of that shape (or of at least that many bytes, where it is a number)."""
+    _place(t, name, dev)
+    fits = t.numel() >= shape if isinstance(shape, int) else t.shape == shape
+    if t.dtype != _torch().uint8 or not t.is_contiguous() or not fits:
+        raise ValueError(f"{name}: contiguous uint8 {shape if isinstance(shape, tuple) else f'of {shape} bytes'} wanted")
+    return t.data_ptr()
+
+
+def _quantize(where, x, tensor_scale, codes, scales, row_scales, stream):
+    dev = _device(x)
+    dt = _dtype(x, "x")
+    stride = _rows(x, "x", dev, x.shape, x.dtype)
+    T, H = x.shape
+    _int32(T, H)
+    cp = _bytes(codes, "codes", dev, (T, H // 2)) if scales is not None else _bytes(codes, "tiles", dev, vh_nvfp4_tiles_bytes(T, H))
+    sp = _bytes(scales, "scales", dev, (T, H // 16)) if scales is not None else None
+    rp = None
+    if tensor_scale is None:
+        rp = _vector(row_scales, "row_scales", dev, T, _f32)
+    elif row_scales is not None:
+        raise ValueError("row_scales are the output of a call without a tensor scale")
+    st = lib().vh_nvfp4_quantize(x.data_ptr(), dt, T, H, stride, 0.0 if tensor_scale is None else float(tensor_scale), cp, sp,
+                                 rp, _stream_on(stream, dev))
+    _check(st, where)
+
+
+def nvfp4_quantize(x, tensor_scale=None, codes=None, scales=None, row_scales=None, stream=None):
+    """Rows x [T,H] (fp32 / bf16 / fp16, may be strided, H % 16 == 0) to block-scaled 4 bits with a tensor scale (a number),
+    or with a scale of its own for each row: codes [T,H/2] uint8, scales [T,H/16] uint8 (E4M3), as the *_nvfp4 calls take
+    them with a tensor scale.  -> (codes, scales, row_scales [T] fp32 or None)"""
+    if stream is None and codes is not None and scales is not None:
+        m = _compiled_calls()
+        if m:
+            st = m.nvfp4_quantize(x, tensor_scale, codes, scales, row_scales)
+            if st <= 0:
+                _check(st, "nvfp4_quantize")
+                return codes, scales, row_scales
+    torch = _torch()
+    _device(x)
+    if x.dim() != 2:
+        raise ValueError("x: shape mismatch")
+    T, H = x.shape
+    with _allocating(stream):
+        codes = torch.empty(T, H // 2, dtype=torch.uint8, device=x.device) if codes is None else codes
+        scales = torch.empty(T, H // 16, dtype=torch.uint8, device=x.device) if scales is None else scales
+        if row_scales is None and tensor_scale is None:
+            row_scales = torch.empty(T, dtype=torch.float32, device=x.device)
+    _quantize("nvfp4_quantize", x, tensor_scale, codes, scales, row_scales, stream)
+    return codes, scales, row_scales
+
+
+def nvfp4_quantize_tiles(x, tensor_scale=None, tiles=None, row_scales=None, stream=None):
+    """nvfp4_quantize into the tiled layout that nvfp4_matmul takes.  -> (tiles, row_scales [T] fp32 or None)"""
+    if stream is None and tiles is not None:
+        m = _compiled_calls()
+        if m:
+            st = m.nvfp4_quantize(x, tensor_scale, tiles, None, row_scales)
+            if st <= 0:
+                _check(st, "nvfp4_quantize_tiles")
+                return tiles, row_scales
+    torch = _torch()
+    _device(x)
+    if x.dim() != 2:
+        raise ValueError("x: shape mismatch")
+    T, H = x.shape
+    with _allocating(stream):
+        tiles = torch.empty(vh_nvfp4_tiles_bytes(T, H), dtype=torch.uint8, device=x.device) if tiles is None else tiles
+        if row_scales is None and tensor_scale is None:
+            row_scales = torch.empty(T, dtype=torch.float32, device=x.device)
+    _quantize("nvfp4_quantize_tiles", x, tensor_scale, tiles, None, row_scales, stream)
+    return tiles, row_scales
+
+
+def nvfp4_tile(codes, scales, tiles=None, stream=None):
+    """codes [V,H/2] uint8, scales [V,H/16] uint8 (row-major) -> the tiled copy that nvfp4_matmul takes.  Done once for a
+    weight (not the layout of nvfp4_pack, which serves the heads' argmax)."""
+    torch = _torch()
+    dev = _device(codes)
+    if codes.dim() != 2:
+        raise ValueError("codes: shape mismatch")
+    V, H = codes.shape[0], codes.shape[1] * 2
+    _int32(V, H)
+    cp, sp = _bytes(codes, "codes", dev, (V, H // 2)), _bytes(scales, "scales", dev, (V, H // 16))
+    n = vh_nvfp4_tiles_bytes(V, H)
+    if tiles is None:
+        with _allocating(stream):
+            tiles = torch.empty(n, dtype=torch.uint8, device=codes.device)
+    st = lib().vh_nvfp4_tile(cp, sp, V, H, _bytes(tiles, "tiles", dev, n), tiles.numel(), _stream_on(stream, dev))
+    _check(st, "nvfp4_tile")
+    return tiles
+
+
+def _dequantize(where, codes, scales, T, H, scale, out, dtype, stream):
+    dev = _device(codes)
+    _int32(T, H)
+    cp = _bytes(codes, "codes", dev, (T, H // 2)) if scales is not None else _bytes(codes, "tiles", dev, vh_nvfp4_tiles_bytes(T, H))
+    sp = _bytes(scales, "scales", dev, (T, H // 16)) if scales is not None else None
+    if out is None:
+        with _allocating(stream):
+            out = _torch().empty(T, H, dtype=dtype or _torch().bfloat16, device=codes.device)
+    elif dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out: {dtype} wanted, not {out.dtype}")
+    g, gp = _scale(scale, "scale", dev, T)
+    st = lib().vh_nvfp4_dequantize(cp, sp, T, H, g, gp, _dtype(out, "out"), out.data_ptr(),
+                                   _rows(out, "out", dev, (T, H), out.dtype), _stream_on(stream, dev))
+    _check(st, where)
+    return out
+
+
+def nvfp4_dequantize(codes, scales, scale, out=None, dtype=None, stream=None):
+    """Values of 4-bit rows, code * block scale * scale: codes [T,H/2], scales [T,H/16] uint8, scale a number or the row
+    scales [T] fp32; out [T,H] fp32 / bf16 / fp16 (bf16 where neither out nor dtype is given).  -> out"""
+    if stream is None and out is not None and dtype is None:
+        m = _compiled_calls()
+        if m:
+            st = m.nvfp4_dequantize(codes, scales, scale, out)
+            if st <= 0:
+                _check(st, "nvfp4_dequantize")
+                return out
+    _device(codes)
+    if codes.dim() != 2 or scales is None:
+        raise ValueError("codes, scales: shape mismatch")
+    return _dequantize("nvfp4_dequantize", codes, scales, codes.shape[0], codes.shape[1] * 2, scale, out, dtype, stream)
+
+
+def nvfp4_dequantize_tiles(tiles, scale, T: int, H: int, out=None, dtype=None, stream=None):
+    """nvfp4_dequantize from the tiled layout of a [T,H] matrix (its gradient's product takes the values).  -> out"""
+    return _dequantize("nvfp4_dequantize_tiles", tiles, None, T, H, scale, out, dtype, stream)
+
+
+def nvfp4_matmul(x_tiles, x_scale, w_tiles, w_scale, T: int, V: int, H: int, out=None, dtype=None, stream=None):
+    """out[t,v] = sum over h of X[t,h] W[v,h] of two 4-bit matrices in the tiled layout, X [T,H] (nvfp4_quantize_tiles) and W
+    [V,H] (nvfp4_tile, nvfp4_quantize_tiles); each scale is a number or the row scales (fp32 [T], [V]).  out [T,V] fp32 /
+    bf16 / fp16, rows may be strided (bf16 where neither out nor dtype is given): logits of a 4-bit head, say.  -> out"""
+    if stream is None and out is not None and dtype is None:
+        m = _compiled_calls()
+        if m:
+            st = m.nvfp4_matmul(x_tiles, x_scale, w_tiles, w_scale, T, V, H, out)
+            if st <= 0:
+                _check(st, "nvfp4_matmul")
+                return out
+    dev = _device(x_tiles)
+    _int32(T, V, H)
+    xp = _bytes(x_tiles, "x_tiles", dev, vh_nvfp4_tiles_bytes(T, H))
+    wp = _bytes(w_tiles, "w_tiles", dev, vh_nvfp4_tiles_bytes(V, H))
+    if out is None:
+        with _allocating(stream):
+            out = _torch().empty(T, V, dtype=dtype or _torch().bfloat16, device=x_tiles.device)
+    elif dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out: {dtype} wanted, not {out.dtype}")
+    xg, xgp = _scale(x_scale, "x_scale", dev, T)
+    wg, wgp = _scale(w_scale, "w_scale", dev, V)
+    st = lib().vh_nvfp4_matmul(xp, xg, xgp, wp, wg, wgp, T, V, H, _dtype(out, "out"), out.data_ptr(),
+                               _rows(out, "out", dev, (T, V), out.dtype), _stream_on(stream, dev))
+    _check(st, "nvfp4_matmul")
+    return out
+
+
+# ----------------------------------------------------------------------------
+# Processing of logits.
+
+_RULES = ("history", "history_len", "prompt_len", "draft_ids", "repetition", "frequency", "presence", "bias_ids", "bias",
+          "allowed", "temperature")
+
+
+def _rows_or_none(t, name, dev, rows, dtype, least=0):
+    """(address, elements between rows, width) of a 2-D tensor of that many rows, or of none."""
+    if t is None:
+        return None, 0, 0
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < least:
+        raise ValueError(f"{name}: shape mismatch")
+    return t.data_ptr(), _rows(t, name, dev, t.shape, dtype), t.shape[1]
+
+
+def _rules(dev, R, V, rules):
+    """(vh_logits_rules, rows per sequence) of the rules given, all by the name of the call's argument."""
+    S = next((len(rules[k]) for k in _RULES if k != "allowed" and rules[k] is not None), R)
+    if S < 1 or R % S != 0:
+        raise ValueError(f"{R} rows are not a whole number for each of {S} sequences")
+    per = R // S
+    r = LogitsRules()
+    r.history, r.history_stride, r.history_width = _rows_or_none(rules["history"], "history", dev, S, _i32)
+    for name, dtype in (("history_len", _i32), ("prompt_len", _i32), ("repetition", _f32), ("frequency", _f32),
+                        ("presence", _f32), ("temperature", _f32)):
+        setattr(r, name, _vector(rules[name], name, dev, S, dtype))
+    d = rules["draft_ids"]
+    if d is not None and d.shape != (S, per - 1):
+        raise ValueError(f"draft_ids: ({S}, {per - 1}) wanted")
+    r.draft_ids = _vector(d, "draft_ids", dev, S * (per - 1), _i32)
+    ids, bias = rules["bias_ids"], rules["bias"]
+    if (ids is None) != (bias is None) or (ids is not None and (ids.dim() != 2 or ids.shape != bias.shape or len(ids) != S)):
+        raise ValueError("bias_ids, bias: shape mismatch")
+    r.n_bias = ids.shape[1] if ids is not None else 0
+    r.bias_ids, r.bias = _vector(ids, "bias_ids", dev, S * r.n_bias, _i32), _vector(bias, "bias", dev, S * r.n_bias, _f32)
+    r.allowed, r.allowed_stride, _ = _rows_or_none(rules["allowed"], "allowed", dev, R, _i32, (V + 31) // 32)
+    return r, per
+
+
+def logits_process(logits, history=None, history_len=None, prompt_len=None, draft_ids=None, repetition=None, frequency=None,
+                   presence=None, bias_ids=None, bias=None, allowed=None, temperature=None, out=None, stream=None):
+    """Biases, penalties for repeated tokens, temperature and grammar masks on logits [R,V] (fp32 / bf16 / fp16, rows may be
+    strided), whose rows are R / S after one another for each of S sequences (a verify round's k + 1 positions, or one):
+        z = logits + bias;  z / repetition or (z <= 0) z * repetition for tokens in the history;
+        z - frequency * n - presence * [n > 0], n the times a token has been output;  z / temperature;  -inf where not allowed
+    history [S,L] int32 (the prompt's tokens first; ids outside [0,V) are passed over), history_len, prompt_len [S] int32;
+    draft_ids [S,R/S-1] int32: row j also counts the first j; repetition, frequency, presence, temperature [S] fp32
+    (temperature 0: greedy, as 1); bias_ids [S,n] int32 with bias [S,n] fp32 (the last entry of an id counts); allowed
+    [R,>=ceil(V/32)] int32, bit v % 32 of word v / 32.  Every rule may be None.
+    out: logits' type or fp32, may be `logits` itself.  -> out"""
+    if stream is None and out is not None:
+        m = _compiled_calls()
+        if m:
+            st = m.logits_process(logits, history, history_len, prompt_len, draft_ids, repetition, frequency, presence, bias_ids,
+                                  bias, allowed, temperature, out)
+            if st <= 0:
+                _check(st, "logits_process")
+                return out
+    dev = _device(logits)
+    dt = _dtype(logits, "logits")
+    shape = logits.shape
+    stride = _rows(logits, "logits", dev, shape, logits.dtype)
+    R, V = shape
+    _int32(R, V)
+    rules = dict(zip(_RULES, (history, history_len, prompt_len, draft_ids, repetition, frequency, presence, bias_ids, bias,
+                              allowed, temperature)))
+    r, per = _rules(dev, R, V, rules)
+    if out is None:
+        with _allocating(stream):
+            out = _empty_rows(logits)
+    if out.dtype != logits.dtype and out.dtype != _f32:
+        raise ValueError(f"out: {logits.dtype} or float32 wanted, not {out.dtype}")
+    st = lib().vh_logits_process(logits.data_ptr(), dt, R, V, stride, per, ctypes.byref(r), out.data_ptr(), _dtypes[out.dtype],
+                                 _rows(out, "out", dev, shape, out.dtype), _stream_on(stream, dev))
+    _check(st, "logits_process")
+    return out
+
+
+def logits_process_grad(dout, logits, history=None, history_len=None, prompt_len=None, draft_ids=None, repetition=None,
+                        frequency=None, presence=None, bias_ids=None, bias=None, allowed=None, temperature=None, dlogits=None,
+                        stream=None):
+    """Gradient of logits_process with respect to the logits, from dout [R,V] of their type (0 where not allowed); dlogits
+    may be `dout` itself.  The other arguments as there.  -> dlogits"""
+    if stream is None and dlogits is not None:
+        m = _compiled_calls()
+        if m:
+            st = m.logits_process_grad(dout, logits, history, history_len, prompt_len, draft_ids, repetition, frequency, presence,
+                                       bias_ids, bias, allowed, temperature, dlogits)
+            if st <= 0:
+                _check(st, "logits_process_grad")
+                return dlogits
+    dev = _device(logits)
+    dt = _dtype(logits, "logits")
+    shape, dtype = logits.shape, logits.dtype
+    stride = _rows(logits, "logits", dev, shape, dtype)
+    R, V = shape
+    _int32(R, V)
+    rules = dict(zip(_RULES, (history, history_len, prompt_len, draft_ids, repetition, frequency, presence, bias_ids, bias,
+                              allowed, temperature)))
+    r, per = _rules(dev, R, V, rules)
+    if dlogits is None:
+        with _allocating(stream):
+            dlogits = _empty_rows(logits)
+    st = lib().vh_logits_process_grad(dout.data_ptr(), logits.data_ptr(), dt, R, V, _rows(dout, "dout", dev, shape, dtype),
+                                      stride, per, ctypes.byref(r), dlogits.data_ptr(),
+                                      _rows(dlogits, "dlogits", dev, shape, dtype), _stream_on(stream, dev))
+    _check(st, "logits_process_grad")
+    return dlogits

@@ -8,6 +8,7 @@
 #include <cmath>
 
 #include "../../include/verifyhead.h"
+#include "vh_capi.h"
 #include "vh_kernels.h"
 #include "vh_row_kernels.h"
 #include "vh_verify.h"
@@ -23,27 +24,12 @@ constexpr int kTcFp4Rows = 16;  // hidden rows per tensor-core 4-bit draft launc
 constexpr int kMmaFp4Rows = 8;  // hidden rows per warp-level-MMA 4-bit launch
 constexpr int kPackedRows = 16;  // hidden rows per pass over a tiled 4-bit head
 constexpr int kMaxNormH = 1 << 24;              // width of a normed row
-constexpr int kMaxLogprobV = 2147483647 - 1023;  // vocabulary of the log probabilities: tile ends stay in 31 bits
-inline bool known_dtype(int d) { return d == VH_F32 || d == VH_BF16 || d == VH_F16; }
-inline uintptr_t dtype_size(int d) { return d == VH_F32 ? 4 : 2; }
-inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-vh_status check_device() {
-    static std::atomic<int> ok_cache[64] = {};  // 1: device already checked
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
-        cudaGetLastError();
-        return VH_ERR_DEVICE;
-    }
-    if (dev < 64 && ok_cache[dev].load(std::memory_order_relaxed)) return VH_OK;
-    int major = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess || major < 10) {
-        cudaGetLastError();
-        return VH_ERR_DEVICE;
-    }
-    if (dev < 64) ok_cache[dev].store(1, std::memory_order_relaxed);
-    return VH_OK;
-}
+using vh::aligned;
+using vh::check_device;
+using vh::dtype_size;
+using vh::known_dtype;
+using vh::launch_status;
+constexpr int kMaxLogprobV = vh::kMaxVocab;
 
 vh::Workspace make_ws(void* ws, int /*rows*/) { return vh::ws_view(ws); }
 
@@ -51,12 +37,6 @@ vh::Workspace make_ws(void* ws, int /*rows*/) { return vh::ws_view(ws); }
 // one 16-row pass (H * 32 bytes) within its shared-memory limit (H <= 6144).
 inline bool packed_shape_ok(int H) {
     return H >= 256 && H <= kMaxH && H % 256 == 0 && vh::nvfp4_packed_smem(kPackedRows, H) <= vh::nvfp4_packed_max_smem();
-}
-
-vh_status launch_status(cudaError_t e) {
-    if (e == cudaSuccess) return VH_OK;
-    cudaGetLastError();  // clear a non-sticky launch error
-    return VH_ERR_LAUNCH;
 }
 
 }  // namespace

@@ -1,4 +1,4 @@
-// Argument marshalling of the norm and log-probability calls in compiled code: the checks of the Python binding on
+// Argument marshalling of the norm, log-probability, 4-bit row and logit-processing calls in compiled code: the checks of the Python binding on
 // torch tensors, then the call through the C ABI.  A decode step makes these calls on a handful of rows, where reading
 // a tensor's type, sizes, strides and address from Python takes longer than the kernel (4 x 2048 norm: 6.95 us a
 // call from Python alone, 2.1 us from here).
@@ -23,6 +23,12 @@ decltype(&vh_add_rmsnorm_grad) p_add_rmsnorm_grad;
 decltype(&vh_logits_logprobs) p_logits_logprobs;
 decltype(&vh_logits_logprobs_grad) p_logits_logprobs_grad;
 decltype(&vh_head_logprobs) p_head_logprobs;
+decltype(&vh_nvfp4_tiles_bytes) p_nvfp4_tiles_bytes;
+decltype(&vh_nvfp4_quantize) p_nvfp4_quantize;
+decltype(&vh_nvfp4_dequantize) p_nvfp4_dequantize;
+decltype(&vh_nvfp4_matmul) p_nvfp4_matmul;
+decltype(&vh_logits_process) p_logits_process;
+decltype(&vh_logits_process_grad) p_logits_process_grad;
 
 struct Unusual {};  // thrown on the way out to "1"
 
@@ -254,6 +260,162 @@ PyObject* head_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// A contiguous uint8 matrix.
+uint8_t* bytes(const Call& c, PyObject* o, int64_t rows, int64_t width) {
+    const at::Tensor& t = tensor(o);
+    c.here(t);
+    if (t.scalar_type() != at::kByte || t.dim() != 2 || t.size(0) != rows || t.size(1) != width || !t.is_contiguous())
+        throw Unusual();
+    return static_cast<uint8_t*>(t.data_ptr());
+}
+// The tiled layout of a matrix [rows][H].
+uint8_t* tiles(const Call& c, PyObject* o, int rows, int H) {
+    const at::Tensor& t = tensor(o);
+    c.here(t);
+    if (t.scalar_type() != at::kByte || !t.is_contiguous() || t.numel() < (int64_t)p_nvfp4_tiles_bytes(rows, H)) throw Unusual();
+    return static_cast<uint8_t*>(t.data_ptr());
+}
+// A tensor scale (a number) or row scales.
+struct Scale {
+    float number = 0.0f;
+    const float* rows = nullptr;
+    Scale(const Call& c, PyObject* o, int64_t n) {
+        if (THPVariable_Check(o))
+            rows = static_cast<const float*>(c.vector(o, n, at::kFloat));
+        else
+            number = as_float(o);
+    }
+};
+
+// x, tensor_scale, codes or tiles, scales or None, row_scales
+PyObject* nvfp4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return call(n, 5, [&]() -> int {
+        const at::Tensor& x = tensor(a[0]);
+        const Call c(x);
+        if (x.dim() != 2 || (a[1] == Py_None) != (a[4] != Py_None)) throw Unusual();
+        const int T = as_int(x.size(0)), H = as_int(x.size(1));
+        int64_t xs;
+        void* xp = c.rows(x, T, H, x.scalar_type(), &xs);
+        uint8_t* sp = a[3] != Py_None ? bytes(c, a[3], T, H / 16) : nullptr;
+        uint8_t* cp = sp ? bytes(c, a[2], T, H / 2) : tiles(c, a[2], T, H);
+        float* rp = static_cast<float*>(c.vector(a[4], T, at::kFloat));
+        return launch(p_nvfp4_quantize, xp, row_type(x.scalar_type()), T, H, xs, rp ? 0.0f : as_float(a[1]), cp, sp, rp, c.stream);
+    });
+}
+
+// codes, scales, scale, out
+PyObject* nvfp4_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return call(n, 4, [&]() -> int {
+        const at::Tensor& y = tensor(a[3]);
+        const Call c(y);
+        if (y.dim() != 2) throw Unusual();
+        const int T = as_int(y.size(0)), H = as_int(y.size(1));
+        int64_t ys;
+        void* yp = c.rows(y, T, H, y.scalar_type(), &ys);
+        if (H % 16 != 0) throw Unusual();
+        const Scale g(c, a[2], T);
+        return launch(p_nvfp4_dequantize, bytes(c, a[0], T, H / 2), bytes(c, a[1], T, H / 16), T, H, g.number, g.rows,
+                      row_type(y.scalar_type()), yp, ys, c.stream);
+    });
+}
+
+// x_tiles, x_scale, w_tiles, w_scale, T, V, H, out
+PyObject* nvfp4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return call(n, 8, [&]() -> int {
+        const at::Tensor& y = tensor(a[7]);
+        const Call c(y);
+        const int T = as_count(a[4]), V = as_count(a[5]), H = as_count(a[6]);
+        if (y.dim() != 2) throw Unusual();
+        int64_t ys;
+        void* yp = c.rows(y, T, V, y.scalar_type(), &ys);
+        const Scale gx(c, a[1], T), gw(c, a[3], V);
+        return launch(p_nvfp4_matmul, tiles(c, a[0], T, H), gx.number, gx.rows, tiles(c, a[2], V, H), gw.number, gw.rows, T, V, H,
+                      row_type(y.scalar_type()), yp, ys, c.stream);
+    });
+}
+
+// The rules of a call, from a[0] on: history, history_len, prompt_len, draft_ids, repetition, frequency, presence, bias_ids,
+// bias, allowed, temperature.
+struct Rules {
+    vh_logits_rules r = {};
+    int per_seq;
+    Rules(const Call& c, PyObject* const* a, int64_t R, int64_t V) {
+        int64_t S = R;
+        for (int i = 0; i < 11; ++i)
+            if (i != 9 && a[i] != Py_None) {
+                const at::Tensor& t = tensor(a[i]);
+                if (t.dim() < 1) throw Unusual();
+                S = t.size(0);
+                break;
+            }
+        if (S < 1 || R % S != 0) throw Unusual();
+        per_seq = as_int(R / S);
+        if (a[0] != Py_None) {
+            const at::Tensor& h = tensor(a[0]);
+            if (h.dim() != 2) throw Unusual();
+            r.history_width = as_int(h.size(1));
+            r.history = static_cast<const int32_t*>(c.rows(h, S, h.size(1), at::kInt, &r.history_stride));
+        }
+        r.history_len = static_cast<const int32_t*>(c.vector(a[1], S, at::kInt));
+        r.prompt_len = static_cast<const int32_t*>(c.vector(a[2], S, at::kInt));
+        if (a[3] != Py_None && (tensor(a[3]).dim() != 2 || tensor(a[3]).size(0) != S)) throw Unusual();
+        r.draft_ids = static_cast<const int32_t*>(c.vector(a[3], S * (per_seq - 1), at::kInt));
+        r.repetition = static_cast<const float*>(c.vector(a[4], S, at::kFloat));
+        r.frequency = static_cast<const float*>(c.vector(a[5], S, at::kFloat));
+        r.presence = static_cast<const float*>(c.vector(a[6], S, at::kFloat));
+        if ((a[7] == Py_None) != (a[8] == Py_None)) throw Unusual();
+        if (a[7] != Py_None) {
+            const at::Tensor& ids = tensor(a[7]);
+            const at::Tensor& b = tensor(a[8]);
+            if (ids.dim() != 2 || b.dim() != 2 || ids.size(0) != S || b.size(0) != S) throw Unusual();
+            r.n_bias = as_int(ids.size(1));
+            r.bias_ids = static_cast<const int32_t*>(c.vector(a[7], S * r.n_bias, at::kInt));
+            r.bias = static_cast<const float*>(c.vector(a[8], S * r.n_bias, at::kFloat));
+        }
+        if (a[9] != Py_None) {
+            const at::Tensor& m = tensor(a[9]);
+            if (m.dim() != 2 || m.size(1) < (V + 31) / 32) throw Unusual();
+            r.allowed = static_cast<const int32_t*>(c.rows(m, R, m.size(1), at::kInt, &r.allowed_stride));
+        }
+        r.temperature = static_cast<const float*>(c.vector(a[10], S, at::kFloat));
+    }
+};
+
+// logits, the rules, out
+PyObject* logits_process(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return call(n, 13, [&]() -> int {
+        const at::Tensor& x = tensor(a[0]);
+        const at::Tensor& y = tensor(a[12]);
+        const Call c(x);
+        if (x.dim() != 2) throw Unusual();
+        const int64_t R = x.size(0), V = x.size(1);
+        int64_t xs, ys;
+        void* xp = c.rows(x, R, V, x.scalar_type(), &xs);
+        void* yp = c.rows(y, R, V, y.scalar_type(), &ys);
+        if (y.scalar_type() != x.scalar_type() && y.scalar_type() != at::kFloat) throw Unusual();
+        const Rules r(c, a + 1, R, V);
+        return launch(p_logits_process, xp, row_type(x.scalar_type()), as_int(R), as_int(V), xs, r.per_seq, &r.r, yp,
+                      row_type(y.scalar_type()), ys, c.stream);
+    });
+}
+
+// dout, logits, the rules, dlogits
+PyObject* logits_process_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return call(n, 14, [&]() -> int {
+        const at::Tensor& x = tensor(a[1]);
+        const Call c(x);
+        if (x.dim() != 2) throw Unusual();
+        const int64_t R = x.size(0), V = x.size(1);
+        int64_t gs, xs, ds;
+        void* gp = c.rows(tensor(a[0]), R, V, x.scalar_type(), &gs);
+        void* xp = c.rows(x, R, V, x.scalar_type(), &xs);
+        void* dp = c.rows(tensor(a[13]), R, V, x.scalar_type(), &ds);
+        const Rules r(c, a + 2, R, V);
+        return launch(p_logits_process_grad, gp, xp, row_type(x.scalar_type()), as_int(R), as_int(V), gs, xs, r.per_seq, &r.r, dp,
+                      ds, c.stream);
+    });
+}
+
 // name, address
 PyObject* bind(PyObject*, PyObject* args) {
     const char* name;
@@ -270,6 +432,18 @@ PyObject* bind(PyObject*, PyObject* args) {
         p_logits_logprobs_grad = reinterpret_cast<decltype(p_logits_logprobs_grad)>(p);
     else if (!std::strcmp(name, "vh_head_logprobs"))
         p_head_logprobs = reinterpret_cast<decltype(p_head_logprobs)>(p);
+    else if (!std::strcmp(name, "vh_nvfp4_tiles_bytes"))
+        p_nvfp4_tiles_bytes = reinterpret_cast<decltype(p_nvfp4_tiles_bytes)>(p);
+    else if (!std::strcmp(name, "vh_nvfp4_quantize"))
+        p_nvfp4_quantize = reinterpret_cast<decltype(p_nvfp4_quantize)>(p);
+    else if (!std::strcmp(name, "vh_nvfp4_dequantize"))
+        p_nvfp4_dequantize = reinterpret_cast<decltype(p_nvfp4_dequantize)>(p);
+    else if (!std::strcmp(name, "vh_nvfp4_matmul"))
+        p_nvfp4_matmul = reinterpret_cast<decltype(p_nvfp4_matmul)>(p);
+    else if (!std::strcmp(name, "vh_logits_process"))
+        p_logits_process = reinterpret_cast<decltype(p_logits_process)>(p);
+    else if (!std::strcmp(name, "vh_logits_process_grad"))
+        p_logits_process_grad = reinterpret_cast<decltype(p_logits_process_grad)>(p);
     else
         return PyErr_Format(PyExc_ValueError, "no entry point %s", name);
     Py_RETURN_NONE;
@@ -284,6 +458,11 @@ PyMethodDef methods[] = {
     {"logits_logprobs", fast(logits_logprobs), METH_FASTCALL, nullptr},
     {"logits_logprobs_grad", fast(logits_logprobs_grad), METH_FASTCALL, nullptr},
     {"head_logprobs", fast(head_logprobs), METH_FASTCALL, nullptr},
+    {"nvfp4_quantize", fast(nvfp4_quantize), METH_FASTCALL, nullptr},
+    {"nvfp4_dequantize", fast(nvfp4_dequantize), METH_FASTCALL, nullptr},
+    {"nvfp4_matmul", fast(nvfp4_matmul), METH_FASTCALL, nullptr},
+    {"logits_process", fast(logits_process), METH_FASTCALL, nullptr},
+    {"logits_process_grad", fast(logits_process_grad), METH_FASTCALL, nullptr},
     {"bind", bind, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -1,4 +1,5 @@
-// Launchers of the operators on both sides of the head (add_rmsnorm.cu, logprobs.cu, head_logprobs.cu).
+// Launchers of the operators on both sides of the head (add_rmsnorm.cu, logprobs.cu, head_logprobs.cu, logits_process.cu)
+// and of those on 4-bit rows (nvfp4_rows.cu, nvfp4_matmul.cu).
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -76,5 +77,50 @@ struct HeadLogprobArgs {
 };
 size_t head_logprobs_ws_bytes(int R, int V, int top_n);
 cudaError_t launch_head_logprobs(const HeadLogprobArgs& a, cudaStream_t s);
+
+// Rows to 4 bits (nvfp4_rows.cu), H % 16 == 0.  scales null: `codes` is the tiled layout (vh_nvfp4_tiles.h).
+struct Nvfp4QuantArgs {
+    const void* x;
+    long long x_stride;
+    int T, H;
+    float tensor_scale;  // when row_scales is null
+    uint8_t *codes, *scales;
+    float* row_scales;
+};
+cudaError_t launch_nvfp4_quantize(const Nvfp4QuantArgs& a, int dtype, cudaStream_t s);
+
+struct Nvfp4DequantArgs {
+    const uint8_t *codes, *scales;
+    int T, H;
+    float tensor_scale;
+    const float* row_scales;
+    void* y;
+    long long y_stride;
+};
+cudaError_t launch_nvfp4_dequantize(const Nvfp4DequantArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_nvfp4_tile(const uint8_t* codes, const uint8_t* scales, int V, int H, uint8_t* tiles, cudaStream_t s);
+
+// Product of two tiled 4-bit matrices (nvfp4_matmul.cu): y[t][v] = x_scale(t) w_scale(v) sum_h X[t,h] W[v,h].
+struct Nvfp4MatmulArgs {
+    const uint8_t *x, *w;
+    float x_scale, w_scale;               // when the arrays are null
+    const float *x_scales, *w_scales;
+    int T, V, H;
+    void* y;
+    long long y_stride;
+};
+cudaError_t launch_nvfp4_matmul(const Nvfp4MatmulArgs& a, int dtype, cudaStream_t s);
+
+// Processing of logits (logits_process.cu).  `in` are the logits, or the gradient of the processed ones; `logits` is
+// read by the gradient alone.
+struct ProcessArgs {
+    const void *in, *logits;
+    void* out;
+    long long in_stride, logits_stride, out_stride;
+    int R, V, per_seq;
+    vh_logits_rules rules;
+};
+cudaError_t launch_logits_process(const ProcessArgs& a, int dtype, int out_dtype, cudaStream_t s);
+cudaError_t launch_logits_process_grad(const ProcessArgs& a, int dtype, cudaStream_t s);
 
 }  // namespace vh
