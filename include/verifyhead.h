@@ -663,7 +663,8 @@ VH_API vh_status vh_logits_process(const void* logits, int dtype, int R, int V, 
  * z is logits + bias.  frequency and presence do not matter, nor bias but for
  * its sign of z.
  *
- *  dout, logits  device, dtype [R][V];  dlogits device, dtype [R][V] (out), may be dout itself
+ *  dout, logits  device, dtype [R][V];  dlogits device, dtype [R][V] (out), may be dout itself (same address and
+ *                stride), not logits
  */
 VH_API vh_status vh_logits_process_grad(const void* dout, const void* logits, int dtype, int R, int V,
                                         int64_t dout_stride, int64_t logits_stride, int rows_per_seq,

@@ -46,7 +46,7 @@ def rules(vh, **kw):
 
 
 def process(vh, **kw):
-    a = dict(x=P, dtype=1, R=6, V=100, xs=100, per=3, rules=None, y=P, yt=1, ys=100, stream=None)
+    a = dict(x=P, dtype=1, R=6, V=100, xs=100, per=3, rules=None, y=2 * P, yt=1, ys=100, stream=None)
     r = {k: kw.pop(k) for k in list(kw) if k not in a}
     a.update(kw)
     if "rules" not in kw:
@@ -55,7 +55,7 @@ def process(vh, **kw):
 
 
 def process_grad(vh, **kw):
-    a = dict(d=P, x=P, dtype=1, R=6, V=100, dys=100, xs=100, per=3, rules=None, y=P, ys=100, stream=None)
+    a = dict(d=P, x=2 * P, dtype=1, R=6, V=100, dys=100, xs=100, per=3, rules=None, y=3 * P, ys=100, stream=None)
     r = {k: kw.pop(k) for k in list(kw) if k not in a}
     a.update(kw)
     if "rules" not in kw:
@@ -91,6 +91,8 @@ def test_shape(vh):
         assert process(vh, **kw) == vh.VH_ERR_SHAPE, kw
         assert process_grad(vh, **kw) == vh.VH_ERR_SHAPE, kw
     assert process(vh, yt=2) == vh.VH_ERR_SHAPE
+    assert process(vh, y=P, ys=101) == vh.VH_ERR_SHAPE and process(vh, y=P, yt=0) == vh.VH_ERR_SHAPE
+    assert process_grad(vh, y=2 * P) == vh.VH_ERR_SHAPE and process_grad(vh, y=P, ys=101) == vh.VH_ERR_SHAPE
     assert process_grad(vh, dys=99) == vh.VH_ERR_SHAPE
 
 

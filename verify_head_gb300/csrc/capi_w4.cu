@@ -128,6 +128,7 @@ vh_status vh_logits_process(const void* logits, int dtype, int R, int V, int64_t
         return VH_ERR_SHAPE;
     const vh_status rt = check_rules(*rules, R, V, rows_per_seq);
     if (rt != VH_OK) return rt;
+    if (out == logits && (out_dtype != dtype || (R > 1 && out_stride != stride))) return VH_ERR_SHAPE;
     if (!aligned(logits, dtype_size(dtype)) || !aligned(out, dtype_size(out_dtype))) return VH_ERR_ALIGN;
     const vh_status st = check_device();
     if (st != VH_OK) return st;
@@ -153,6 +154,7 @@ vh_status vh_logits_process_grad(const void* dout, const void* logits, int dtype
         return VH_ERR_SHAPE;
     const vh_status rt = check_rules(*rules, R, V, rows_per_seq);
     if (rt != VH_OK) return rt;
+    if (dlogits == logits || (dlogits == dout && R > 1 && dlogits_stride != dout_stride)) return VH_ERR_SHAPE;
     const uintptr_t sz = dtype_size(dtype);
     if (!aligned(dout, sz) || !aligned(logits, sz) || !aligned(dlogits, sz)) return VH_ERR_ALIGN;
     const vh_status st = check_device();
