@@ -69,21 +69,40 @@ __host__ __device__ constexpr uint32_t idesc_nvf4(int M, int N) {
            | ((uint32_t)(M >> 7) << 27);  // M / 128
 }
 
+template <int CTAS>
 __device__ __forceinline__ void mma_nvf4(uint32_t tmem_d, unsigned long long adesc, unsigned long long bdesc, uint32_t idesc,
                                          uint32_t scale_a, uint32_t scale_b, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(tmem_d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"(accumulate)
-        : "memory");
+    if constexpr (CTAS == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(tmem_d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(tmem_d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"(accumulate)
+            : "memory");
 }
 
 // 32 lines of 16 bytes (512 in a row) to 4 columns of each quarter of the TMEM lanes.
-__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t saddr) {
-    const unsigned long long d = (unsigned long long)((saddr >> 4) & 0x3FFFu)  // no swizzle: 8 lines of 16 bytes, then
-                                 | (unsigned long long)(128u >> 4) << 32       // the next 8 lines
-                                 | 1ull << 46;
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+__device__ __forceinline__ unsigned long long scale_desc(uint32_t saddr) {
+    return (unsigned long long)((saddr >> 4) & 0x3FFFu)  // no swizzle: 8 lines of 16 bytes, then
+           | (unsigned long long)(128u >> 4) << 32       // the next 8 lines
+           | 1ull << 46;
+}
+template <int CTAS>
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, unsigned long long desc) {
+    if constexpr (CTAS == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else  // in both CTAs, each from its own shared memory
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0u;
 }
 
 template <int NMAX>
@@ -173,39 +192,49 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
                 mbar_drain(&bars->full[j % STAGES], (j / STAGES) & 1u);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t it = 0, local = 0;
-            bool ok = true;
-            for (long long tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x, ++local) {
-                const uint32_t idesc = idesc_nvf4(kTileM, cols((int)(tile % a.n_x)));
-                const uint32_t buf = local & 1u;
-                if (!mbar_wait(&bars->tmem_empty[buf], ((local >> 1) & 1u) ^ 1u, &bars->err)) break;
+        // The whole warp runs the loop, so that addresses and descriptors stay in uniform registers; one lane issues.  (With the
+        // loop in one lane every instruction's operands were moved there first: 12 instructions took 1,400 cycles a stage.)
+        const bool leader = elect_one();
+        const uint32_t base = smem_u32(smem);
+        uint32_t it = 0, local = 0;
+        bool ok = true;
+        for (long long tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x, ++local) {
+            const uint32_t idesc = idesc_nvf4(kTileM, cols((int)(tile % a.n_x)));
+            const uint32_t buf = local & 1u;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars->tmem_empty[buf], ((local >> 1) & 1u) ^ 1u, &bars->err))) break;
+            tc_fence_after();
+            for (int kt = 0; kt < a.records; ++kt, ++it) {
+                const int s = it % STAGES;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars->full[s], (it / STAGES) & 1u, &bars->err))) { ok = false; break; }
                 tc_fence_after();
-                for (int kt = 0; kt < a.records; ++kt, ++it) {
-                    const int s = it % STAGES;
-                    if (!mbar_wait(&bars->full[s], (it / STAGES) & 1u, &bars->err)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t sw = smem_u32(smem + (size_t)s * C::kStage), sx = sw + kTileBytes;
-                    const uint32_t tw = tmem_base + kScaleCol + s * kScaleCols, tx = tw + 16;
-                    const int steps = min(4, (a.H - kt * kTileElems + 63) / 64);
+                const uint32_t sw = base + s * C::kStage, sx = sw + kTileBytes;
+                const uint32_t tw = tmem_base + kScaleCol + s * kScaleCols, tx = tw + 16, td = tmem_base + buf * 128u;
+                const unsigned long long dw = smem_desc_sw128(sw), dx = smem_desc_sw128(sx);
+                const unsigned long long gw = scale_desc(sw + kTileCodes), gx = scale_desc(sx + NMAX * 128);
+                const int steps = min(4, (a.H - kt * kTileElems + 63) / 64);
+                if (leader) {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         if (ks < steps) {
-                            scales_to_tmem(tw + ks * 4, sw + kTileCodes + ks * 512);
-                            scales_to_tmem(tx + ks * 4, sx + NMAX * 128 + ks * 512);
+                            scales_to_tmem<1>(tw + ks * 4, gw + ks * 32);
+                            scales_to_tmem<1>(tx + ks * 4, gx + ks * 32);
                         }
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         if (ks < steps)
-                            mma_nvf4(tmem_base + buf * 128u, smem_desc_sw128(sw + ks * 32), smem_desc_sw128(sx + ks * 32), idesc,
-                                     tw + ks * 4, tx + ks * 4, (kt > 0 || ks > 0) ? 1u : 0u);
+                            mma_nvf4<1>(td, dw + ks * 2, dx + ks * 2, idesc, tw + ks * 4, tx + ks * 4, (kt > 0 || ks > 0) ? 1u : 0u);
                     mma_commit(&bars->empty[s]);
                 }
-                if (ok) mma_commit(&bars->tmem_full[buf]);
+                __syncwarp();
             }
+            if (ok && leader) mma_commit(&bars->tmem_full[buf]);
+            __syncwarp();
+        }
+        if (leader) {
             mma_commit(&bars->mma_done);
             mbar_drain(&bars->mma_done, 0u);
         }
+        __syncwarp();
     } else {
         rows_wait();
         const int quarter = warp & 3, half = (warp - 2) >> 2;
@@ -247,6 +276,201 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// More rows of X: CTA pairs (cta_group::2) on 256 rows of W x 256 rows of X, two records, or up to 128 at X's end, where each
+// CTA has half the lines of the last record.  Each CTA stages its record of W, its lines of X and the scales of both records; the
+// leader issues; each CTA's TMEM has the accumulators of its own rows of W and the scales of all rows of X, 32 rows to a column
+// and a record's in four columns (tcgen05.cp writes four at a time, at a multiple of four).  Per stage a CTA takes in 38 KiB for 512 cycles of MMAs, a little more than an SM is given by L2 (64 bytes a cycle).
+// Two accumulators of 256 columns would leave the scales no room: there is one, and the epilogue takes all of it into registers
+// (128 a thread) before it hands it back and begins to write.
+//
+// The records come by tensor maps over the buffer's bytes, since those copies may signal the leader's barrier.
+
+constexpr int kStages2 = 5;
+constexpr int kScales2 = 256, kScaleCols2 = 48;  // columns: behind the accumulator; per stage 4 x 4 of W, 4 x 8 of X
+constexpr int kStageB2 = kTileBytes + kTileCodes + 2 * kTileScales;
+constexpr int kMapRow = 256;                      // bytes of a row of the tensor maps
+static_assert(kScales2 + kStages2 * kScaleCols2 <= kTmemCols, "scales of every stage");
+constexpr size_t kSmem2 = 1024 + (size_t)kStages2 * kStageB2 + sizeof(Bars);
+
+template <typename TO>
+__global__ void __launch_bounds__(kThreadsM, 1)
+    k_matmul_pair(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_codes,
+                  const __grid_constant__ CUtensorMap map_scales, const Args a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // stage: W (codes, scales), codes of X, scales of both records of X
+    Bars* bars = reinterpret_cast<Bars*>(smem + (size_t)kStages2 * kStageB2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const long long n_tiles = (long long)a.n_w * a.n_x;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages2; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        mbar_init(&bars->tmem_full[0], 1);
+        mbar_init(&bars->tmem_empty[0], 2 * kEpiWarps);  // of both CTAs
+        mbar_init(&bars->mma_done, 1);
+        bars->err = 0u;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync();  // both CTAs' barriers are initialised before any remote use
+    tc_fence_after();
+    const uint32_t tmem_base = bars->tmem_base;
+    // rows of X of a tile, as the MMA takes them: two records, or some lines of one
+    auto cols = [&](int tx) { return a.T - tx * 256 > kTileRows ? 256 : (a.T - tx * 256 + 31) / 32 * 32; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // W is read before the previous kernel is waited for, X after.
+            const unsigned long long pol_w = a.n_x > 1 ? policy_evict_last() : policy_evict_first(), pol_x = policy_evict_last();
+            uint32_t it = 0;
+            bool ok = true, waited = false;
+            auto load_x = [&](uint32_t j, int tx, int kt) {
+                const int s = j % kStages2;
+                const uint32_t bar = map_to_rank(smem_u32(&bars->full[s]), 0);
+                uint8_t* to = smem + (size_t)s * kStageB2 + kTileBytes;
+                auto row = [&](int r) { return ((2 * tx + r) * a.records + kt) * (kTileBytes / kMapRow); };  // r: of the two records
+                const int n = cols(tx);  // of one record: the other half of its lines, and what lies behind them
+                tma_load_2d_pair(to, &map_codes, bar, 0, n == 256 ? row((int)rank) : row(0) + (int)rank * (n / 2 * 128 / kMapRow), pol_x);
+                tma_load_2d_pair(to + kTileCodes, &map_scales, bar, 0, row(0) + kTileCodes / kMapRow, pol_x);
+                tma_load_2d_pair(to + kTileCodes + kTileScales, &map_scales, bar, 0, row(1) + kTileCodes / kMapRow, pol_x);
+            };
+            auto release_first_ring = [&](uint32_t n) {
+                rows_wait();
+                rows_fence_async();
+                for (uint32_t j = 0; j < n; ++j) {
+                    const long long tile = pair + (long long)(j / a.records) * pairs;
+                    load_x(j, (int)(tile % a.n_x), (int)(j % a.records));
+                }
+                waited = true;
+            };
+            for (long long tile = pair; tile < n_tiles && ok; tile += pairs) {
+                const int tw = (int)(tile / a.n_x) * 2 + (int)rank, tx = (int)(tile % a.n_x);
+                for (int kt = 0; kt < a.records; ++kt, ++it) {
+                    const int s = it % kStages2;
+                    if (!mbar_wait(&bars->empty[s], ((it / kStages2) & 1u) ^ 1u, &bars->err)) { ok = false; break; }
+                    if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], 2u * kStageB2);
+                    tma_load_2d_pair(smem + (size_t)s * kStageB2, &map_w, map_to_rank(smem_u32(&bars->full[s]), 0), 0,
+                                     (tw * a.records + kt) * (kTileBytes / kMapRow), pol_w);
+                    if (waited)
+                        load_x(it, tx, kt);
+                    else if (it + 1 == (uint32_t)kStages2)
+                        release_first_ring(it + 1);
+                }
+            }
+            if (!waited) release_first_ring(it);
+            if (rank == 0)  // the leader's barriers see both CTAs' loads
+                for (uint32_t j = (it > (uint32_t)kStages2 ? it - kStages2 : 0); j < it; ++j)
+                    mbar_drain(&bars->full[j % kStages2], (j / kStages2) & 1u);
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const bool leader = elect_one();
+            const uint32_t base = smem_u32(smem);
+            uint32_t it = 0, local = 0;
+            bool ok = true;
+            for (long long tile = pair; tile < n_tiles && ok; tile += pairs, ++local) {
+                const uint32_t idesc = idesc_nvf4(2 * kTileM, cols((int)(tile % a.n_x)));
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars->tmem_empty[0], (local & 1u) ^ 1u, &bars->err))) break;
+                tc_fence_after();
+                for (int kt = 0; kt < a.records; ++kt, ++it) {
+                    const int s = it % kStages2;
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars->full[s], (it / kStages2) & 1u, &bars->err))) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sw = base + s * kStageB2, sx = sw + kTileBytes;
+                    const uint32_t tw = tmem_base + kScales2 + s * kScaleCols2, tx = tw + 16;
+                    const unsigned long long dw = smem_desc_sw128(sw), dx = smem_desc_sw128(sx);
+                    const unsigned long long gw = scale_desc(sw + kTileCodes), gx = scale_desc(sx + kTileCodes);
+                    const int steps = min(4, (a.H - kt * kTileElems + 63) / 64);
+                    if (leader) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            if (ks < steps) {
+                                scales_to_tmem<2>(tw + ks * 4, gw + ks * 32);
+                                scales_to_tmem<2>(tx + ks * 8, gx + ks * 32);
+                                scales_to_tmem<2>(tx + ks * 8 + 4, gx + kTileScales / 16 + ks * 32);
+                            }
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            if (ks < steps)
+                                mma_nvf4<2>(tmem_base, dw + ks * 2, dx + ks * 2, idesc, tw + ks * 4, tx + ks * 8,
+                                            (kt > 0 || ks > 0) ? 1u : 0u);
+                        mma_commit_pair(&bars->empty[s]);
+                    }
+                    __syncwarp();
+                }
+                if (ok && leader) mma_commit_pair(&bars->tmem_full[0]);
+                __syncwarp();
+            }
+            if (leader) {
+                mma_commit_pair(&bars->mma_done);
+                mbar_drain(&bars->mma_done, 0u);
+            }
+            __syncwarp();
+        }
+    } else {
+        rows_wait();
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t empty = map_to_rank(smem_u32(&bars->tmem_empty[0]), 0);
+        uint32_t local = 0;
+        bool ok = true;
+        for (long long tile = pair; tile < n_tiles; tile += pairs, ++local) {
+            const int tw = (int)(tile / a.n_x) * 2 + (int)rank, tx = (int)(tile % a.n_x);
+            const int v = tw * kTileM + quarter * 32 + lane, t0 = tx * 256;
+            const int blocks = cols(tx) / 32;  // this warp has half, half + 2, ..
+            const float gw = a.w_scales != nullptr ? (v < a.V ? a.w_scales[v] : 0.0f) : a.w_scale;
+            float gx[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int t = t0 + (2 * g + half) * 32 + lane;
+                gx[g] = a.x_scales != nullptr ? (t < a.T ? a.x_scales[t] : 0.0f) : a.x_scale;
+            }
+            if (ok) ok = mbar_wait(&bars->tmem_full[0], local & 1u, &bars->err);
+            tc_fence_after();
+            float acc[4][32];
+            const uint32_t at = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 32);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                if (2 * g + half < blocks) tmem_ld32(at + g * 64u, acc[g]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(empty);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int t = t0 + (2 * g + half) * 32;
+                if (2 * g + half >= blocks || t >= a.T) break;
+                TO* y = static_cast<TO*>(a.y) + (long long)t * a.y_stride + v;
+                const int n = min(32, a.T - t);
+                const float gt = ok ? gx[g] : quiet_nan();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float f = acc[g][j] * __shfl_sync(0xFFFFFFFFu, gt, j) * gw;
+                    if (j < n && v < a.V) y[(long long)j * a.y_stride] = from_f32<TO>(f);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // no CTA leaves while its peer may still signal or read it
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------
+
 static int sm_count() {
     static std::atomic<int> cache[64] = {};
     int dev = 0;
@@ -280,6 +504,71 @@ static cudaError_t run_n(Args a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+// A buffer of records as rows of kMapRow bytes, copied `box` rows at a time; past its end zeros.
+static bool byte_map(CUtensorMap* m, const void* base, size_t bytes, int box) {
+    auto enc = get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)kMapRow, (cuuint64_t)(bytes / kMapRow)};
+    cuuint64_t strides[1] = {(cuuint64_t)kMapRow};
+    cuuint32_t boxes[2] = {(cuuint32_t)kMapRow, (cuuint32_t)box};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, boxes, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTA pairs that are resident at once, per device.
+template <typename TO>
+static int resident_pairs() {
+    static std::atomic<int> cache[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    int n = cache[dev & 63].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (cudaFuncSetAttribute(k_matmul_pair<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem2) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
+    cfg.blockDim = dim3(kThreadsM);
+    cfg.dynamicSmemBytes = kSmem2;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, k_matmul_pair<TO>, &cfg) != cudaSuccess) return 0;
+    cache[dev & 63].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+template <typename TO>
+static cudaError_t run_pair(Args a, int pairs, cudaStream_t s) {
+    a.n_w = (int)(((long long)a.V + 2 * kTileM - 1) / (2 * kTileM));
+    a.n_x = (int)(((long long)a.T + 255) / 256);
+    alignas(64) CUtensorMap mw, mc, ms;
+    if (!byte_map(&mw, a.w, nvfp4_tiles_bytes(a.V, a.H), kTileBytes / kMapRow) ||
+        !byte_map(&mc, a.x, nvfp4_tiles_bytes(a.T, a.H), kTileCodes / kMapRow) ||
+        !byte_map(&ms, a.x, nvfp4_tiles_bytes(a.T, a.H), kTileScales / kMapRow))
+        return cudaErrorNotSupported;
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_matmul_pair<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem2);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * std::min<long long>((long long)a.n_w * a.n_x, pairs)));
+    cfg.blockDim = dim3(kThreadsM);
+    cfg.dynamicSmemBytes = kSmem2;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_matmul_pair<TO>, mw, mc, ms, a);
+}
+
 template <typename TO>
 static cudaError_t run(const Nvfp4MatmulArgs& m, cudaStream_t s) {
     Args a{};
@@ -295,7 +584,11 @@ static cudaError_t run(const Nvfp4MatmulArgs& m, cudaStream_t s) {
     a.records = tiles_per_row(m.H);
     a.y = m.y;
     a.y_stride = m.y_stride;
-    return a.T <= 32 ? run_n<TO, 32>(a, s) : run_n<TO, 128>(a, s);
+    if (a.T <= 32) return run_n<TO, 32>(a, s);
+    if (a.T <= kTileRows) return run_n<TO, 128>(a, s);
+    // rows of tiles of bytes / 256 in 31 bits (549 GB)
+    const int pairs = resident_pairs<TO>();
+    return pairs > 0 ? run_pair<TO>(a, pairs, s) : run_n<TO, 128>(a, s);
 }
 
 }  // namespace mm4
