@@ -6,7 +6,10 @@
 // lie together), without tensor maps.  The scales go from there to TMEM by tcgen05.cp, each ring stage to columns of its
 // own: they are written again only when the stage's MMAs have been committed.
 //
-// Epilogue: an accumulator lane is a row of W and a column a row of X, so a warp's 32 lanes write 32 neighbours of a row of y.
+// Epilogue: an accumulator lane is a row of W and a column a row of X.  A warp turns its 32 x 32 blocks in shared memory and
+// writes 64 or 128 bytes of each of 32 rows of y in 16-byte pieces; where y's rows are not aligned for that, its 32 lanes write 32
+// neighbours of a row.  (One row after the other for all, the rows' scales by shuffles: 256 x 248320 x 2048 took 113 us, and
+// 104 with a quarter of the contraction: the epilogue set the pace.)
 //
 // Every wait is bounded; on expiry the CTA's flag is set, the tiles concerned become NaN, copies in flight are waited for, and
 // TMEM is freed.
@@ -32,8 +35,10 @@ using ptx::policy_evict_first;
 using ptx::policy_evict_last;
 
 constexpr int kTileM = kTileRows;
-constexpr int kEpiWarps = 8;  // two per quarter of the TMEM lanes, on alternate blocks of 32 rows of X
-constexpr int kThreadsM = 32 * (2 + kEpiWarps);
+constexpr int kEpiWarps = 8;  // two per quarter of the TMEM lanes, on every other block of 32 rows of X
+constexpr int kShare = kEpiWarps / 4;
+constexpr int kXWarp = 2 + kEpiWarps;  // asks for X
+constexpr int kThreadsM = 32 * (kXWarp + 1);
 constexpr int kMaxStages = 8;
 constexpr int kTmemCols = 512;
 constexpr int kScaleCol = 256;   // behind two accumulators of 128 columns
@@ -57,8 +62,10 @@ struct Args {
     int T, V, H;
     int records;  // per row of records
     int n_w, n_x; // tiles of W and of X
+    int split;    // CTAs that share a tile's records (a cluster), with up to 32 rows of X
     void* y;
     long long y_stride;
+    bool wide;    // y's rows are 16-byte aligned
 };
 
 // Instruction descriptor, kind::mxf4nvf4: e2m1 A and B, e4m3 scales, K = 64, both K-major.
@@ -99,19 +106,117 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, unsigned long lon
     else  // in both CTAs, each from its own shared memory
         asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
+// Arrival that orders no memory: the accumulators have been read when it is made.  (With release semantics at cluster scope it
+// waits for the warp's stores of the tile before.)
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0u;
 }
 
+constexpr int kTurnBytes = 32 * 32 * 4;  // a turned block, per epilogue warp
+constexpr int kEpiBytes = kEpiWarps * kTurnBytes;
+
+// 32 lanes x 32 columns of fp32 from TMEM, without waiting for them; and the wait, before which nothing uses them.
+__device__ __forceinline__ void tmem_ask32(uint32_t taddr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+template <int G>
+__device__ __forceinline__ void tmem_wait(float (&v)[G][32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[g][i]));
+}
+
+// A warp's block of y: rows t.. (n of them), columns v0.. (nv of them); lane = column, acc[j] row t + j, whose scale lane j has.
+// Turned in shared memory: of odd rows the 16-byte halves of each 32 bytes are swapped, so that eight lanes read two rows' 16-byte
+// pieces 32 bytes apart from all banks.
+template <typename TO>
+__device__ __forceinline__ void write_block(const float (&acc)[32], float gx, float gw, TO* y, long long stride, int n, int nv,
+                                            bool wide, float* turn) {
+    const int lane = threadIdx.x & 31;
+    if (wide && nv == 32) {
+        constexpr int LANES = 2 * (int)sizeof(TO);     // of a row: 16 bytes of y each
+        constexpr int ROWS = 32 / LANES, E = 16 / (int)sizeof(TO);
+        const int row = lane / LANES, piece = lane % LANES;
+        TO* to = y + row * stride + piece * E;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) turn[j * 32 + (lane ^ ((j & 1) << 2))] = acc[j] * gw;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; i += ROWS) {
+            const int r = i + row;
+            const float g = __shfl_sync(0xFFFFFFFFu, gx, r);
+            RawVec<TO, E> o;
+#pragma unroll
+            for (int h = 0; h < E / 4; ++h) {
+                const float4 q = *reinterpret_cast<const float4*>(turn + r * 32 + ((piece * E + h * 4) ^ ((r & 1) << 2)));
+                if constexpr (sizeof(TO) == 4) {
+                    o.u[0] = __float_as_uint(q.x * g);
+                    o.u[1] = __float_as_uint(q.y * g);
+                    o.u[2] = __float_as_uint(q.z * g);
+                    o.u[3] = __float_as_uint(q.w * g);
+                } else {
+                    o.set2(2 * h, q.x * g, q.y * g);
+                    o.set2(2 * h + 1, q.z * g, q.w * g);
+                }
+            }
+            if (r < n) o.store(to);
+            to += ROWS * stride;
+        }
+        __syncwarp();
+    } else {
+        TO* to = y + lane;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float f = acc[j] * gw * __shfl_sync(0xFFFFFFFFu, gx, j);
+            if (j < n && lane < nv) *to = from_f32<TO>(f);
+            to += stride;
+        }
+    }
+}
+
+// The scales that a warp's blocks of a tile want: asked for a tile ahead.  First row of W v0, first row of X t0; the warp has blocks
+// share, share + kShare, .. of 32 rows of X.
+template <int G>
+struct TileScales {
+    float gx[G], gw;
+    __device__ __forceinline__ void ask(const Args& a, int v0, int t0, int share) {
+        const int lane = threadIdx.x & 31;
+        gw = a.w_scales != nullptr ? (v0 + lane < a.V ? a.w_scales[v0 + lane] : 0.0f) : a.w_scale;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int t = t0 + (kShare * g + share) * 32 + lane;
+            gx[g] = a.x_scales != nullptr ? (t < a.T ? a.x_scales[t] : 0.0f) : a.x_scale;
+        }
+    }
+};
+
 template <int NMAX>
 struct Config {
     static constexpr int kStageX = NMAX * 128 + kTileScales;
     static constexpr int kStage = kTileBytes + kStageX;
-    static constexpr int kStages = std::min(kMaxStages, (226 * 1024 - 2048) / kStage);
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + sizeof(Bars);
+    static constexpr int kStages = std::min(kMaxStages, (226 * 1024 - 2048 - kEpiBytes) / kStage);
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kEpiBytes + sizeof(Bars);
 };
+
+// Which CTA of a cluster of `split` adds up a quarter of a tile's rows of W, and the quarter's place there.
+__device__ __forceinline__ int owner_of(int quarter, int split) { return split == 2 ? quarter >> 1 : quarter; }
+__device__ __forceinline__ int slot_of(int quarter, int split) { return split == 2 ? quarter & 1 : 0; }
+constexpr int kMaxSplit = 8;
+static_assert(kMaxSplit * kTurnBytes <= kEpiBytes, "partial sums of a quarter from every CTA, in place of the turned blocks");
 
 template <typename TO, int NMAX>
 __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
@@ -120,13 +225,19 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // stage s: W codes and scales, X codes (NMAX lines) and scales
-    Bars* bars = reinterpret_cast<Bars*>(smem + (size_t)STAGES * C::kStage);
+    uint8_t* turn = smem + (size_t)STAGES * C::kStage;
+    Bars* bars = reinterpret_cast<Bars*>(turn + kEpiBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long n_tiles = (long long)a.n_w * a.n_x;
+    // With few tiles a cluster shares the records of one; its partial sums meet below.
+    const int split = NMAX == 32 ? a.split : 1;
+    const int rank = split > 1 ? (int)cluster_rank() : 0;
+    const int k0 = (int)((long long)a.records * rank / split), k1 = (int)((long long)a.records * (rank + 1) / split);
+    const long long first_tile = blockIdx.x / split, step = gridDim.x / split;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->full[s], 2);  // W and X are asked for by a warp each
             mbar_init(&bars->empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -150,47 +261,44 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
     // rows of X of tile `tx`, as the MMA takes them
     auto cols = [&](int tx) { return min(NMAX, (a.T - tx * NMAX + 15) / 16 * 16); };
 
-    if (warp == 0) {
-        if (lane == 0) {
-            // W is read before the previous kernel is waited for, X after.
-            const unsigned long long pol_w = a.n_x > 1 ? policy_evict_last() : policy_evict_first(), pol_x = policy_evict_last();
-            uint32_t it = 0;
-            bool ok = true, waited = false;
-            auto load_x = [&](uint32_t j, int tx, int kt) {
-                const int s = j % STAGES;
-                uint8_t* to = smem + (size_t)s * C::kStage + kTileBytes;
-                // NMAX of a record's 128 lines, and all of its scales
-                const uint8_t* from = a.x + ((size_t)(tx * NMAX / kTileRows) * a.records + kt) * kTileBytes;
-                bulk_load(to, from + (tx * NMAX % kTileRows) * 128, cols(tx) * 128, &bars->full[s], pol_x);
-                bulk_load(to + NMAX * 128, from + kTileCodes, kTileScales, &bars->full[s], pol_x);
-            };
-            auto release_first_ring = [&](uint32_t n) {  // all of one tile of X, or of several: by their order
-                rows_wait();
-                rows_fence_async();
-                for (uint32_t j = 0; j < n; ++j) {
-                    const long long tile = blockIdx.x + (long long)(j / a.records) * gridDim.x;
-                    load_x(j, (int)(tile % a.n_x), (int)(j % a.records));
-                }
-                waited = true;
-            };
-            for (long long tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
-                const int tw = (int)(tile / a.n_x), tx = (int)(tile % a.n_x);
-                for (int kt = 0; kt < a.records; ++kt, ++it) {
-                    const int s = it % STAGES;
-                    if (!mbar_wait(&bars->empty[s], ((it / STAGES) & 1u) ^ 1u, &bars->err)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&bars->full[s], (uint32_t)(kTileBytes + cols(tx) * 128 + kTileScales));
-                    bulk_load(smem + (size_t)s * C::kStage, a.w + ((size_t)tw * a.records + kt) * kTileBytes, kTileBytes,
-                              &bars->full[s], pol_w);
-                    if (waited)
-                        load_x(it, tx, kt);
-                    else if (it + 1 == (uint32_t)STAGES)
-                        release_first_ring(it + 1);
-                }
-            }
-            if (!waited) release_first_ring(it);
-            for (uint32_t j = (it > (uint32_t)STAGES ? it - STAGES : 0); j < it; ++j)
-                mbar_drain(&bars->full[j % STAGES], (j / STAGES) & 1u);
+    if (warp == 0 || warp == kXWarp) {
+        // As with the issue of MMAs below, the whole warp runs the loop.  W is read before the previous kernel is waited for.
+        const bool leader = elect_one(), is_w = warp == 0;
+        const unsigned long long policy = is_w && a.n_x == 1 ? policy_evict_first() : policy_evict_last();
+        if (!is_w) {
+            rows_wait();
+            rows_fence_async();
         }
+        uint32_t it = 0;
+        bool ok = true;
+        for (long long tile = first_tile; tile < n_tiles && ok; tile += step) {
+            const int tw = (int)(tile / a.n_x), tx = (int)(tile % a.n_x);
+            const uint32_t x_bytes = (uint32_t)cols(tx) * 128u;
+            // of X, NMAX of a record's 128 lines, and all of its scales
+            const uint8_t* from = is_w ? a.w + (size_t)tw * a.records * kTileBytes : a.x + (size_t)(tx * NMAX / kTileRows) * a.records * kTileBytes;
+            from += (size_t)k0 * kTileBytes;
+            const int line = is_w ? 0 : tx * NMAX % kTileRows * 128;
+            for (int kt = k0; kt < k1; ++kt, ++it, from += kTileBytes) {
+                const int s = it % STAGES;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars->empty[s], ((it / STAGES) & 1u) ^ 1u, &bars->err))) { ok = false; break; }
+                uint8_t* to = smem + (size_t)s * C::kStage;
+                if (leader) {
+                    if (is_w) {
+                        mbar_arrive_expect_tx(&bars->full[s], kTileBytes);
+                        bulk_load(to, from, kTileBytes, &bars->full[s], policy);
+                    } else {
+                        mbar_arrive_expect_tx(&bars->full[s], x_bytes + kTileScales);
+                        bulk_load(to + kTileBytes, from + line, x_bytes, &bars->full[s], policy);
+                        bulk_load(to + kTileBytes + NMAX * 128, from + kTileCodes, kTileScales, &bars->full[s], policy);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        // copies in flight, should the kernel end early
+        if (is_w && leader)
+            for (uint32_t j = (it > (uint32_t)STAGES ? it - STAGES : 0); j < it; ++j) mbar_drain(&bars->full[j % STAGES], (j / STAGES) & 1u);
+        __syncwarp();
     } else if (warp == 1) {
         // The whole warp runs the loop, so that addresses and descriptors stay in uniform registers; one lane issues.  (With the
         // loop in one lane every instruction's operands were moved there first: 12 instructions took 1,400 cycles a stage.)
@@ -198,12 +306,12 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
         const uint32_t base = smem_u32(smem);
         uint32_t it = 0, local = 0;
         bool ok = true;
-        for (long long tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x, ++local) {
+        for (long long tile = first_tile; tile < n_tiles && ok; tile += step, ++local) {
             const uint32_t idesc = idesc_nvf4(kTileM, cols((int)(tile % a.n_x)));
             const uint32_t buf = local & 1u;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars->tmem_empty[buf], ((local >> 1) & 1u) ^ 1u, &bars->err))) break;
             tc_fence_after();
-            for (int kt = 0; kt < a.records; ++kt, ++it) {
+            for (int kt = k0; kt < k1; ++kt, ++it) {
                 const int s = it % STAGES;
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars->full[s], (it / STAGES) & 1u, &bars->err))) { ok = false; break; }
                 tc_fence_after();
@@ -222,7 +330,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         if (ks < steps)
-                            mma_nvf4<1>(td, dw + ks * 2, dx + ks * 2, idesc, tw + ks * 4, tx + ks * 4, (kt > 0 || ks > 0) ? 1u : 0u);
+                            mma_nvf4<1>(td, dw + ks * 2, dx + ks * 2, idesc, tw + ks * 4, tx + ks * 4, (kt > k0 || ks > 0) ? 1u : 0u);
                     mma_commit(&bars->empty[s]);
                 }
                 __syncwarp();
@@ -237,35 +345,69 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
         __syncwarp();
     } else {
         rows_wait();
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int quarter = warp & 3, share = (warp - 2) >> 2;
+        constexpr int G = (NMAX + 32 * kShare - 1) / (32 * kShare);  // blocks per warp
         uint32_t local = 0;
         bool ok = true;
-        for (long long tile = blockIdx.x; tile < n_tiles; tile += gridDim.x, ++local) {
+        TileScales<G> now, next;
+        auto ask = [&](long long tile, TileScales<G>& to) {
+            if (tile < n_tiles) to.ask(a, (int)(tile / a.n_x) * kTileM + quarter * 32, (int)(tile % a.n_x) * NMAX, share);
+        };
+        ask(first_tile, next);
+        for (long long tile = first_tile; tile < n_tiles; tile += step, ++local) {
             const uint32_t buf = local & 1u;
-            const int tw = (int)(tile / a.n_x), tx = (int)(tile % a.n_x);
-            const int v = tw * kTileM + quarter * 32 + lane, t0 = tx * NMAX;
-            const float gw = a.w_scales != nullptr ? (v < a.V ? a.w_scales[v] : 0.0f) : a.w_scale;
+            const int v0 = (int)(tile / a.n_x) * kTileM + quarter * 32, tx = (int)(tile % a.n_x), t0 = tx * NMAX;
             const int blocks = (cols(tx) + 31) / 32;
+            now = next;
+            ask(tile + step, next);
             if (ok) ok = mbar_wait(&bars->tmem_full[buf], (local >> 1) & 1u, &bars->err);
             tc_fence_after();
-            for (int g = half; g < blocks; g += 2) {
-                const int t = t0 + g * 32;
-                float acc[32];
-                tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * 128u + g * 32u, acc);
-                float gx = a.x_scale;
-                if (a.x_scales != nullptr) gx = t + lane < a.T ? a.x_scales[t + lane] : 0.0f;
-                if (!ok) gx = quiet_nan();
-                TO* y = static_cast<TO*>(a.y) + (long long)t * a.y_stride + v;
-                const int n = min(32, a.T - t);
+            float acc[G][32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float f = acc[j] * __shfl_sync(0xFFFFFFFFu, gx, j) * gw;
-                    if (j < n && v < a.V) y[(long long)j * a.y_stride] = from_f32<TO>(f);
-                }
-            }
+            for (int g = 0; g < G; ++g)
+                if (kShare * g + share < blocks)
+                    tmem_ask32(tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * 128u + (kShare * g + share) * 32u, acc[g]);
+            tmem_wait(acc);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->tmem_empty[buf]);
+            if (NMAX == 32 && split > 1) {
+                // to the CTA that adds this quarter up
+                if (share == 0) {
+                    const uint32_t to = map_to_rank(smem_u32(turn), (uint32_t)owner_of(quarter, split)) +
+                                        (uint32_t)((slot_of(quarter, split) * split + rank) * kTurnBytes + lane * 4);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < a.T)
+                            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + j * 128), "f"(ok ? acc[0][j] : quiet_nan()) : "memory");
+                }
+                continue;
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int t = t0 + (kShare * g + share) * 32;
+                if (kShare * g + share < blocks && t < a.T && v0 < a.V)
+                    write_block(acc[g], ok ? now.gx[g] : quiet_nan(), now.gw, static_cast<TO*>(a.y) + t * a.y_stride + v0, a.y_stride,
+                                min(32, a.T - t), min(32, a.V - v0), a.wide, reinterpret_cast<float*>(turn + (warp - 2) * kTurnBytes));
+            }
+        }
+    }
+    if (NMAX == 32 && split > 1) {
+        __syncwarp();
+        cluster_sync();  // every CTA's sums are where they are added
+        const int quarter = warp & 3;
+        if (warp >= 2 && warp < 6 && owner_of(quarter, split) == rank) {
+            const float* from = reinterpret_cast<const float*>(turn + slot_of(quarter, split) * split * kTurnBytes) + lane;
+            const int v0 = (int)first_tile * kTileM + quarter * 32;
+            TileScales<1> scales;
+            scales.ask(a, v0, 0, 0);
+#pragma unroll 4
+            for (int j = 0; j < a.T; ++j) {  // in the order of the ranks
+                float f = from[j * 32];
+                for (int r = 1; r < split; ++r) f += from[r * (kTurnBytes / 4) + j * 32];
+                f = f * scales.gw * __shfl_sync(0xFFFFFFFFu, scales.gx[0], j);
+                if (v0 + lane < a.V) static_cast<TO*>(a.y)[(long long)j * a.y_stride + v0 + lane] = from_f32<TO>(f);
+            }
         }
     }
     tc_fence_before();
@@ -277,37 +419,45 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// More rows of X: CTA pairs (cta_group::2) on 256 rows of W x 256 rows of X, two records, or up to 128 at X's end, where each
-// CTA has half the lines of the last record.  Each CTA stages its record of W, its lines of X and the scales of both records; the
-// leader issues; each CTA's TMEM has the accumulators of its own rows of W and the scales of all rows of X, 32 rows to a column
-// and a record's in four columns (tcgen05.cp writes four at a time, at a multiple of four).  Per stage a CTA takes in 38 KiB for 512 cycles of MMAs, a little more than an SM is given by L2 (64 bytes a cycle).
-// Two accumulators of 256 columns would leave the scales no room: there is one, and the epilogue takes all of it into registers
-// (128 a thread) before it hands it back and begins to write.
+// Many rows of X: CTA pairs (cta_group::2) on 256 rows of W x two records of X, or some lines of one at X's end.  Each CTA stages
+// its record of W, half of the tile's lines of X (of two records one each) and the scales of all of them; the leader issues; each
+// CTA's TMEM has the accumulators of its own rows of W and the scales of all rows of X, 32 rows to a column and a record's in four
+// columns (tcgen05.cp writes four at a time, at a multiple of four).
+//
+// A stage is 38 KiB per CTA for 512 cycles of MMAs, a little more than an SM is given by L2 (64 bytes a cycle): 0.39 us, 5.9
+// PFLOP/s.  Two accumulators of 256 columns would leave the scales no room: there is one, and the epilogue takes all of it into
+// registers (128 a thread) before it hands it back and begins to write; every tile waits for that, about 2.6 us with the writing
+// that the next tile's MMAs do not hide.  (Pairs on one record, with two accumulators: 4096 x 8192 x 8192 138 us, 88 with two;
+// 256 x 248320 x 2048 84 and 87; what one CTA per tile does as well.)
 //
 // The records come by tensor maps over the buffer's bytes, since those copies may signal the leader's barrier.
 
+constexpr int kMapRow = 256;  // bytes of a row of the tensor maps
+constexpr int kCols2 = 2 * kTileRows;  // rows of X of a tile
+constexpr int kStage2 = kTileBytes + kTileCodes + 2 * kTileScales;
 constexpr int kStages2 = 5;
 constexpr int kScales2 = 256, kScaleCols2 = 48;  // columns: behind the accumulator; per stage 4 x 4 of W, 4 x 8 of X
-constexpr int kStageB2 = kTileBytes + kTileCodes + 2 * kTileScales;
-constexpr int kMapRow = 256;                      // bytes of a row of the tensor maps
-static_assert(kScales2 + kStages2 * kScaleCols2 <= kTmemCols, "scales of every stage");
-constexpr size_t kSmem2 = 1024 + (size_t)kStages2 * kStageB2 + sizeof(Bars);
+constexpr size_t kSmem2 = 1024 + (size_t)kStages2 * kStage2 + kEpiBytes + sizeof(Bars);
+static_assert(kScales2 + kStages2 * kScaleCols2 <= kTmemCols && kStages2 <= kMaxStages && kStage2 % 1024 == 0, "room");
+static_assert(kSmem2 <= 227 * 1024, "shared memory");
 
 template <typename TO>
 __global__ void __launch_bounds__(kThreadsM, 1)
     k_matmul_pair(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_codes,
                   const __grid_constant__ CUtensorMap map_scales, const Args a) {
+    constexpr int STAGES = kStages2, kStage = kStage2;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    // stage: W (codes, scales), codes of X, scales of both records of X
-    Bars* bars = reinterpret_cast<Bars*>(smem + (size_t)kStages2 * kStageB2);
+    // stage: W (codes, scales), codes of X, scales of X
+    uint8_t* turn = smem + (size_t)STAGES * kStage;
+    Bars* bars = reinterpret_cast<Bars*>(turn + kEpiBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const long long n_tiles = (long long)a.n_w * a.n_x;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages2; ++s) {
-            mbar_init(&bars->full[s], 1);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&bars->full[s], 2);  // W and X are asked for by a warp each
             mbar_init(&bars->empty[s], 1);
         }
         mbar_init(&bars->tmem_full[0], 1);
@@ -326,53 +476,51 @@ __global__ void __launch_bounds__(kThreadsM, 1)
     cluster_sync();  // both CTAs' barriers are initialised before any remote use
     tc_fence_after();
     const uint32_t tmem_base = bars->tmem_base;
-    // rows of X of a tile, as the MMA takes them: two records, or some lines of one
-    auto cols = [&](int tx) { return a.T - tx * 256 > kTileRows ? 256 : (a.T - tx * 256 + 31) / 32 * 32; };
+    // rows of X of a tile, as the MMA takes them: two records, or some lines of one, half of them in each CTA
+    auto cols = [&](int tx) {
+        const int left = a.T - tx * kCols2;
+        return left > kTileRows ? 256 : (left + 31) / 32 * 32;
+    };
 
-    if (warp == 0) {
-        if (lane == 0) {
-            // W is read before the previous kernel is waited for, X after.
-            const unsigned long long pol_w = a.n_x > 1 ? policy_evict_last() : policy_evict_first(), pol_x = policy_evict_last();
-            uint32_t it = 0;
-            bool ok = true, waited = false;
-            auto load_x = [&](uint32_t j, int tx, int kt) {
-                const int s = j % kStages2;
-                const uint32_t bar = map_to_rank(smem_u32(&bars->full[s]), 0);
-                uint8_t* to = smem + (size_t)s * kStageB2 + kTileBytes;
-                auto row = [&](int r) { return ((2 * tx + r) * a.records + kt) * (kTileBytes / kMapRow); };  // r: of the two records
-                const int n = cols(tx);  // of one record: the other half of its lines, and what lies behind them
-                tma_load_2d_pair(to, &map_codes, bar, 0, n == 256 ? row((int)rank) : row(0) + (int)rank * (n / 2 * 128 / kMapRow), pol_x);
-                tma_load_2d_pair(to + kTileCodes, &map_scales, bar, 0, row(0) + kTileCodes / kMapRow, pol_x);
-                tma_load_2d_pair(to + kTileCodes + kTileScales, &map_scales, bar, 0, row(1) + kTileCodes / kMapRow, pol_x);
-            };
-            auto release_first_ring = [&](uint32_t n) {
-                rows_wait();
-                rows_fence_async();
-                for (uint32_t j = 0; j < n; ++j) {
-                    const long long tile = pair + (long long)(j / a.records) * pairs;
-                    load_x(j, (int)(tile % a.n_x), (int)(j % a.records));
-                }
-                waited = true;
-            };
-            for (long long tile = pair; tile < n_tiles && ok; tile += pairs) {
-                const int tw = (int)(tile / a.n_x) * 2 + (int)rank, tx = (int)(tile % a.n_x);
-                for (int kt = 0; kt < a.records; ++kt, ++it) {
-                    const int s = it % kStages2;
-                    if (!mbar_wait(&bars->empty[s], ((it / kStages2) & 1u) ^ 1u, &bars->err)) { ok = false; break; }
-                    if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], 2u * kStageB2);
-                    tma_load_2d_pair(smem + (size_t)s * kStageB2, &map_w, map_to_rank(smem_u32(&bars->full[s]), 0), 0,
-                                     (tw * a.records + kt) * (kTileBytes / kMapRow), pol_w);
-                    if (waited)
-                        load_x(it, tx, kt);
-                    else if (it + 1 == (uint32_t)kStages2)
-                        release_first_ring(it + 1);
-                }
-            }
-            if (!waited) release_first_ring(it);
-            if (rank == 0)  // the leader's barriers see both CTAs' loads
-                for (uint32_t j = (it > (uint32_t)kStages2 ? it - kStages2 : 0); j < it; ++j)
-                    mbar_drain(&bars->full[j % kStages2], (j / kStages2) & 1u);
+    if (warp == 0 || warp == kXWarp) {
+        const bool leader = elect_one(), is_w = warp == 0;
+        const unsigned long long policy = is_w && a.n_x == 1 ? policy_evict_first() : policy_evict_last();
+        if (!is_w) {
+            rows_wait();
+            rows_fence_async();
         }
+        const uint32_t full0 = map_to_rank(smem_u32(&bars->full[0]), 0);  // the leader's; 8 bytes on the next
+        uint32_t it = 0;
+        bool ok = true;
+        for (long long tile = pair; tile < n_tiles && ok; tile += pairs) {
+            const int tw = (int)(tile / a.n_x) * 2 + (int)rank, tx = (int)(tile % a.n_x);
+            const int n = cols(tx);
+            int row_w = tw * a.records * (kTileBytes / kMapRow), row_x = 2 * tx * a.records * (kTileBytes / kMapRow);
+            // of one record: the CTA's half of its lines, and what lies behind them
+            const int codes = (int)rank * (n == 256 ? a.records * (kTileBytes / kMapRow) : n / 2 * 128 / kMapRow);
+            for (int kt = 0; kt < a.records; ++kt, ++it, row_w += kTileBytes / kMapRow, row_x += kTileBytes / kMapRow) {
+                const int s = it % STAGES;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars->empty[s], ((it / STAGES) & 1u) ^ 1u, &bars->err))) { ok = false; break; }
+                uint8_t* to = smem + (size_t)s * kStage;
+                const uint32_t bar = full0 + s * 8u;
+                if (leader) {
+                    if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], 2u * (is_w ? kTileBytes : kStage - kTileBytes));
+                    if (is_w) {
+                        tma_load_2d_pair(to, &map_w, bar, 0, row_w, policy);
+                    } else {
+                        tma_load_2d_pair(to + kTileBytes, &map_codes, bar, 0, row_x + codes, policy);
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            tma_load_2d_pair(to + kTileBytes + kTileCodes + r * kTileScales, &map_scales, bar, 0,
+                                             row_x + (r * a.records) * (kTileBytes / kMapRow) + kTileCodes / kMapRow, policy);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (rank == 0 && is_w && leader)  // the leader's barriers see both CTAs' loads
+            for (uint32_t j = (it > (uint32_t)STAGES ? it - STAGES : 0); j < it; ++j) mbar_drain(&bars->full[j % STAGES], (j / STAGES) & 1u);
+        __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
             const bool leader = elect_one();
@@ -384,10 +532,10 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars->tmem_empty[0], (local & 1u) ^ 1u, &bars->err))) break;
                 tc_fence_after();
                 for (int kt = 0; kt < a.records; ++kt, ++it) {
-                    const int s = it % kStages2;
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars->full[s], (it / kStages2) & 1u, &bars->err))) { ok = false; break; }
+                    const int s = it % STAGES;
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars->full[s], (it / STAGES) & 1u, &bars->err))) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t sw = base + s * kStageB2, sx = sw + kTileBytes;
+                    const uint32_t sw = base + s * kStage, sx = sw + kTileBytes;
                     const uint32_t tw = tmem_base + kScales2 + s * kScaleCols2, tx = tw + 16;
                     const unsigned long long dw = smem_desc_sw128(sw), dx = smem_desc_sw128(sx);
                     const unsigned long long gw = scale_desc(sw + kTileCodes), gx = scale_desc(sx + kTileCodes);
@@ -397,8 +545,9 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                         for (int ks = 0; ks < 4; ++ks)
                             if (ks < steps) {
                                 scales_to_tmem<2>(tw + ks * 4, gw + ks * 32);
-                                scales_to_tmem<2>(tx + ks * 8, gx + ks * 32);
-                                scales_to_tmem<2>(tx + ks * 8 + 4, gx + kTileScales / 16 + ks * 32);
+#pragma unroll
+                                for (int r = 0; r < 2; ++r)
+                                    scales_to_tmem<2>(tx + (ks * 2 + r) * 4, gx + r * (kTileScales / 16) + ks * 32);
                             }
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
@@ -420,43 +569,39 @@ __global__ void __launch_bounds__(kThreadsM, 1)
         }
     } else {
         rows_wait();
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int quarter = warp & 3, share = (warp - 2) >> 2;
         const uint32_t empty = map_to_rank(smem_u32(&bars->tmem_empty[0]), 0);
+        constexpr int G = kCols2 / (32 * kShare);  // blocks of 32 columns per warp
         uint32_t local = 0;
         bool ok = true;
+        TileScales<G> now, next;
+        auto ask = [&](long long tile, TileScales<G>& to) {
+            if (tile < n_tiles)
+                to.ask(a, ((int)(tile / a.n_x) * 2 + (int)rank) * kTileM + quarter * 32, (int)(tile % a.n_x) * kCols2, share);
+        };
+        ask(pair, next);
         for (long long tile = pair; tile < n_tiles; tile += pairs, ++local) {
-            const int tw = (int)(tile / a.n_x) * 2 + (int)rank, tx = (int)(tile % a.n_x);
-            const int v = tw * kTileM + quarter * 32 + lane, t0 = tx * 256;
-            const int blocks = cols(tx) / 32;  // this warp has half, half + 2, ..
-            const float gw = a.w_scales != nullptr ? (v < a.V ? a.w_scales[v] : 0.0f) : a.w_scale;
-            float gx[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int t = t0 + (2 * g + half) * 32 + lane;
-                gx[g] = a.x_scales != nullptr ? (t < a.T ? a.x_scales[t] : 0.0f) : a.x_scale;
-            }
+            const int v0 = ((int)(tile / a.n_x) * 2 + (int)rank) * kTileM + quarter * 32, tx = (int)(tile % a.n_x), t0 = tx * kCols2;
+            const int blocks = cols(tx) / 32;  // this warp has share, share + kShare, ..
+            now = next;
+            ask(tile + pairs, next);
             if (ok) ok = mbar_wait(&bars->tmem_full[0], local & 1u, &bars->err);
             tc_fence_after();
-            float acc[4][32];
-            const uint32_t at = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 32);
+            float acc[G][32];
+            const uint32_t at = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(share * 32);
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-                if (2 * g + half < blocks) tmem_ld32(at + g * 64u, acc[g]);
+            for (int g = 0; g < G; ++g)
+                if (kShare * g + share < blocks) tmem_ask32(at + g * (32u * kShare), acc[g]);
+            tmem_wait(acc);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(empty);
+            if (lane == 0) mbar_arrive_relaxed(empty);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int t = t0 + (2 * g + half) * 32;
-                if (2 * g + half >= blocks || t >= a.T) break;
-                TO* y = static_cast<TO*>(a.y) + (long long)t * a.y_stride + v;
-                const int n = min(32, a.T - t);
-                const float gt = ok ? gx[g] : quiet_nan();
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float f = acc[g][j] * __shfl_sync(0xFFFFFFFFu, gt, j) * gw;
-                    if (j < n && v < a.V) y[(long long)j * a.y_stride] = from_f32<TO>(f);
-                }
+            for (int g = 0; g < G; ++g) {
+                const int t = t0 + (kShare * g + share) * 32;
+                if (kShare * g + share < blocks && t < a.T && v0 < a.V)
+                    write_block(acc[g], ok ? now.gx[g] : quiet_nan(), now.gw, static_cast<TO*>(a.y) + t * a.y_stride + v0, a.y_stride,
+                                min(32, a.T - t), min(32, a.V - v0), a.wide, reinterpret_cast<float*>(turn + (warp - 2) * kTurnBytes));
             }
         }
     }
@@ -470,6 +615,8 @@ __global__ void __launch_bounds__(kThreadsM, 1)
 }
 
 // ---------------------------------------------------------------------------
+
+static long long tiles_of(int n, int per) { return ((long long)n + per - 1) / per; }
 
 static int sm_count() {
     static std::atomic<int> cache[64] = {};
@@ -489,18 +636,25 @@ static cudaError_t run_n(Args a, cudaStream_t s) {
     auto kernel = k_matmul<TO, NMAX>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    a.n_w = (int)(((long long)a.V + kTileM - 1) / kTileM);
-    a.n_x = (int)(((long long)a.T + NMAX - 1) / NMAX);
+    a.n_w = (int)tiles_of(a.V, kTileM);
+    a.n_x = (int)tiles_of(a.T, NMAX);
+    const long long tiles = (long long)a.n_w * a.n_x;
+    // Clusters while there are SMs for all of them, and two records or more for each CTA.
+    a.split = 1;
+    while (NMAX == 32 && a.split < kMaxSplit && tiles * a.split * 2 <= sm_count() && a.records >= a.split * 4) a.split *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<long long>((long long)a.n_w * a.n_x, sm_count()));
+    cfg.gridDim = dim3((unsigned)(a.split > 1 ? tiles * a.split : std::min<long long>(tiles, sm_count())));
     cfg.blockDim = dim3(kThreadsM);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
@@ -543,8 +697,8 @@ static int resident_pairs() {
 
 template <typename TO>
 static cudaError_t run_pair(Args a, int pairs, cudaStream_t s) {
-    a.n_w = (int)(((long long)a.V + 2 * kTileM - 1) / (2 * kTileM));
-    a.n_x = (int)(((long long)a.T + 255) / 256);
+    a.n_w = (int)tiles_of(a.V, 2 * kTileM);
+    a.n_x = (int)tiles_of(a.T, kCols2);
     alignas(64) CUtensorMap mw, mc, ms;
     if (!byte_map(&mw, a.w, nvfp4_tiles_bytes(a.V, a.H), kTileBytes / kMapRow) ||
         !byte_map(&mc, a.x, nvfp4_tiles_bytes(a.T, a.H), kTileCodes / kMapRow) ||
@@ -584,11 +738,16 @@ static cudaError_t run(const Nvfp4MatmulArgs& m, cudaStream_t s) {
     a.records = tiles_per_row(m.H);
     a.y = m.y;
     a.y_stride = m.y_stride;
+    a.wide = reinterpret_cast<uintptr_t>(m.y) % 16 == 0 && (m.T == 1 || m.y_stride * sizeof(TO) % 16 == 0);
     if (a.T <= 32) return run_n<TO, 32>(a, s);
     if (a.T <= kTileRows) return run_n<TO, 128>(a, s);
-    // rows of tiles of bytes / 256 in 31 bits (549 GB)
+    // One CTA per 128 x 128 rows, or pairs: by what a tile costs (us, measured: see k_matmul_pair) and the waves of tiles.
+    const long long w = tiles_of(a.V, kTileM), x = tiles_of(a.T, kTileRows);
     const int pairs = resident_pairs<TO>();
-    return pairs > 0 ? run_pair<TO>(a, pairs, s) : run_n<TO, 128>(a, s);
+    auto waves = [](long long tiles, int at_once) { return (float)((tiles + at_once - 1) / at_once); };
+    const float one = waves(w * x, sm_count()) * (a.records * 0.325f + 0.9f);
+    const float two = pairs > 0 ? waves(tiles_of(a.V, 2 * kTileM) * tiles_of(a.T, kCols2), pairs) * (a.records * 0.39f + 2.6f) : one;
+    return two < one ? run_pair<TO>(a, pairs, s) : run_n<TO, 128>(a, s);
 }
 
 }  // namespace mm4
