@@ -572,6 +572,7 @@ __global__ void __launch_bounds__(kThreadsM, 1)
         const int quarter = warp & 3, share = (warp - 2) >> 2;
         const uint32_t empty = map_to_rank(smem_u32(&bars->tmem_empty[0]), 0);
         constexpr int G = kCols2 / (32 * kShare);  // blocks of 32 columns per warp
+        static_assert(G == 4, "two and two");
         uint32_t local = 0;
         bool ok = true;
         TileScales<G> now, next;
@@ -587,21 +588,29 @@ __global__ void __launch_bounds__(kThreadsM, 1)
             ask(tile + pairs, next);
             if (ok) ok = mbar_wait(&bars->tmem_full[0], local & 1u, &bars->err);
             tc_fence_after();
-            float acc[G][32];
             const uint32_t at = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(share * 32);
+            // two blocks at a time: four do not fit the registers, and there is no first-level cache left to spill to
+#pragma unroll 1
+            for (int g0 = 0; g0 < G; g0 += 2) {
+                float acc[2][32];
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-                if (kShare * g + share < blocks) tmem_ask32(at + g * (32u * kShare), acc[g]);
-            tmem_wait(acc);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_relaxed(empty);
+                for (int g = 0; g < 2; ++g)
+                    if (kShare * (g0 + g) + share < blocks) tmem_ask32(at + (g0 + g) * (32u * kShare), acc[g]);
+                tmem_wait(acc);
+                if (g0 + 2 >= G) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_relaxed(empty);
+                }
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const int t = t0 + (kShare * g + share) * 32;
-                if (kShare * g + share < blocks && t < a.T && v0 < a.V)
-                    write_block(acc[g], ok ? now.gx[g] : quiet_nan(), now.gw, static_cast<TO*>(a.y) + t * a.y_stride + v0, a.y_stride,
-                                min(32, a.T - t), min(32, a.V - v0), a.wide, reinterpret_cast<float*>(turn + (warp - 2) * kTurnBytes));
+                for (int g = 0; g < 2; ++g) {
+                    const int block = kShare * (g0 + g) + share, t = t0 + block * 32;
+                    if (block < blocks && t < a.T && v0 < a.V)
+                        write_block(acc[g], ok ? now.gx[g] : quiet_nan(), now.gw, static_cast<TO*>(a.y) + t * a.y_stride + v0, a.y_stride,
+                                    min(32, a.T - t), min(32, a.V - v0), a.wide, reinterpret_cast<float*>(turn + (warp - 2) * kTurnBytes));
+                }
+                now.gx[0] = now.gx[2];
+                now.gx[1] = now.gx[3];
             }
         }
     }
@@ -741,13 +750,14 @@ static cudaError_t run(const Nvfp4MatmulArgs& m, cudaStream_t s) {
     a.wide = reinterpret_cast<uintptr_t>(m.y) % 16 == 0 && (m.T == 1 || m.y_stride * sizeof(TO) % 16 == 0);
     if (a.T <= 32) return run_n<TO, 32>(a, s);
     if (a.T <= kTileRows) return run_n<TO, 128>(a, s);
-    // One CTA per 128 x 128 rows, or pairs: by what a tile costs (us, measured: see k_matmul_pair) and the waves of tiles.
+    // One CTA per 128 x 128 rows, or pairs: by what a tile takes (us, measured) and the waves of tiles.  A tile takes its
+    // contraction and the wait for the accumulators, or the writing of the one before, whichever is longer.
     const long long w = tiles_of(a.V, kTileM), x = tiles_of(a.T, kTileRows);
     const int pairs = resident_pairs<TO>();
     auto waves = [](long long tiles, int at_once) { return (float)((tiles + at_once - 1) / at_once); };
-    const float one = waves(w * x, sm_count()) * (a.records * 0.325f + 0.9f);
-    const float two = pairs > 0 ? waves(tiles_of(a.V, 2 * kTileM) * tiles_of(a.T, kCols2), pairs) * (a.records * 0.39f + 2.6f) : one;
-    return two < one ? run_pair<TO>(a, pairs, s) : run_n<TO, 128>(a, s);
+    const float one = waves(w * x, sm_count()) * std::max(1.75f, a.records * 0.325f + 0.7f);
+    const float two = waves(tiles_of(a.V, 2 * kTileM) * tiles_of(a.T, kCols2), std::max(pairs, 1)) * std::max(4.9f, a.records * 0.39f + 1.6f) + 2.5f;
+    return pairs > 0 && two < one ? run_pair<TO>(a, pairs, s) : run_n<TO, 128>(a, s);
 }
 
 }  // namespace mm4
