@@ -426,8 +426,8 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
 //
 // A stage is 38 KiB per CTA for 512 cycles of MMAs, a little more than an SM is given by L2 (64 bytes a cycle): 0.39 us, 5.9
 // PFLOP/s.  Two accumulators of 256 columns would leave the scales no room: there is one, and the epilogue takes all of it into
-// registers (128 a thread) before it hands it back and begins to write; every tile waits for that, about 2.6 us with the writing
-// that the next tile's MMAs do not hide.  (Pairs on one record, with two accumulators: 4096 x 8192 x 8192 138 us, 88 with two;
+// registers, in two halves, the second before it hands it back; every tile waits for that and the writing of the first, about
+// 2.2 us.  (Pairs on one record, with two accumulators: 4096 x 8192 x 8192 138 us, 88 with two;
 // 256 x 248320 x 2048 84 and 87; what one CTA per tile does as well.)
 //
 // The records come by tensor maps over the buffer's bytes, since those copies may signal the leader's barrier.
@@ -756,7 +756,7 @@ static cudaError_t run(const Nvfp4MatmulArgs& m, cudaStream_t s) {
     const int pairs = resident_pairs<TO>();
     auto waves = [](long long tiles, int at_once) { return (float)((tiles + at_once - 1) / at_once); };
     const float one = waves(w * x, sm_count()) * std::max(1.75f, a.records * 0.325f + 0.7f);
-    const float two = waves(tiles_of(a.V, 2 * kTileM) * tiles_of(a.T, kCols2), std::max(pairs, 1)) * std::max(4.9f, a.records * 0.39f + 1.6f) + 2.5f;
+    const float two = waves(tiles_of(a.V, 2 * kTileM) * tiles_of(a.T, kCols2), std::max(pairs, 1)) * std::max(3.3f, a.records * 0.39f + 2.2f) + 2.0f;
     return pairs > 0 && two < one ? run_pair<TO>(a, pairs, s) : run_n<TO, 128>(a, s);
 }
 
