@@ -6,31 +6,34 @@
 // Almost every token of the vocabulary is neither biased nor in the history:
 // its place is one product with 1 / temperature (two units in the last place
 // of fp32 at most, instead of a division's half).  The others are marked
-// places.  There are CTAs of two kinds:
+// places.  Rows stream through by slots of 16 aligned bytes; a slot with no
+// allowed place is not read.
 //
-// - Dense: some rows of one sequence over a chunk of the vocabulary stream
-//   through by slots of 16 aligned bytes; a slot with no allowed place is not
-//   read.
-// - Sparse: the marked places of the same rows.  A table in shared memory
-//   counts each token (whole numbers: the order of the atomics does not
-//   matter), then each place of the table is read, changed and written.  It is
-//   a hash table with room for all tokens that may come; for histories past its
-//   size several CTAs have a range of the vocabulary each, with a place for
-//   every token.
+// Large calls: one kernel streams every place (k_process_stream), and a second
+// one (k_process_marked), which builds its tables while the first ends, writes
+// the marked places over it.  A table in shared memory counts each token of
+// the history, drafted and biased ones among them (whole numbers: the order of
+// the atomics does not matter), then each place of the table is read, changed
+// and written.  It is a hash table with room for all tokens that may come; for
+// histories past its size several CTAs have a range of the vocabulary each,
+// with a place for every token.
 //
-// Usually the dense CTAs write every place, and the sparse ones, a kernel that
-// builds its tables while the dense one ends, write theirs over it.  Where the
-// output is the input, what they read must not have been written: the dense
-// CTAs then look through the history too and leave the marked places of their
-// chunk, a bitmap, out of their stores, so that no place is written by two
-// threads or read after another wrote it, in whatever order they run.  Calls of
-// few rows, where a launch counts, go that way too; for all calls it would cost
-// more, since the bitmap's slots are stored element by element (gradient of
-// 2048 x 65536 bf16 with histories of 512: 158 us, 111 in two kernels).
+// Small calls, where a launch counts, and outputs that are the inputs, whose
+// marked places the first kernel would have lost: one kernel (k_process).  A
+// CTA has some rows of one sequence over a chunk of the vocabulary.  It looks
+// through the history, its first slots of logits already on their way, and
+// counts the tokens of its chunk, 16 bits each unless a history is longer than
+// that counts, with a bitmap of the marked places; those are changed in their
+// slot's registers, so that every slot is read and written once, by one
+// thread.  Most warps have a marked place in some lane and wait for it: 256 x
+// 248320 bf16 with histories of 4096 94 us this way, 58 in two kernels; 4 x
+// 248320 fp32 5.4 us, 8.3 in two.
 //
 // Bound: memory (the logits once in and once out).  256 x 248320 bf16: 43 us
-// without a history (255 MB: 0.89 of the copy rate), 48 with 512 tokens, 58 with
-// 4096; the gradient of 2048 x 65536: 89 (0.90) and, with 512 tokens, 111.
+// without a history (255 MB: 0.89 of the copy rate), 45 with 512 tokens, 58 with
+// 4096: of each marked place the logit is read again and the output's sector
+// filled and written again, long after the stream has left L2.  The gradient of
+// 2048 x 65536: 89 us (0.90) and, with 512 tokens, 110.
 #include <algorithm>
 
 #include "vh_row_kernels.h"
@@ -40,40 +43,42 @@ namespace vh {
 namespace proc {
 
 constexpr int kThreadsP = 256;
-// Threads of the sparse CTAs where they are a launch of their own: few tokens and many sequences (256; 2048 sequences of 512
-// tokens: 111 us, 121 with 512 threads), up to kShort tokens (512; 64 sequences of 2900 tokens: 61 us, 134 with 256), more.
+constexpr int kSlotBytes = 16;   // of logits per thread and load (256 x 248320 bf16 42.6 us; 32 bytes 45.4)
+constexpr int kStreamSlots = 4;  // slots per thread, all asked for at once: where every place is written,
+constexpr int kUnroll = 2;       // and in k_process (four: as fast or slower)
+constexpr int kMaxRows = 8;      // of a sequence per CTA
+// Calls of up to so many CTAs of k_process_stream take k_process (4 x 248320 fp32, 244: 5.4 us, 8.3 in two kernels; 129 x 40001,
+// 645: 13.7 and 16.6; 16 x 248320, 976: 10.0 and 9.4).
+constexpr int kOneLaunch = 800;
+constexpr int kChunk = 8192;     // places of a CTA of k_process at most (a multiple of 128)
+constexpr int kPerSm = 4;        // of them
+constexpr int kMostNarrow = 32767;  // tokens that 16-bit counts hold, beside the prompt's bit
+constexpr uint32_t kInPrompt = 0x80000000u;
+constexpr uint32_t kDrafted = 0x40000000u;
+// Threads of k_process_marked: few tokens and many sequences (256; 2048 sequences of 512 tokens: 111 us, 121 with 512 threads), up
+// to kShort tokens (512; 64 sequences of 2900 tokens: 61 us, 134 with 256), more.
 constexpr int kThreadsFew = 256, kThreadsShort = 512, kThreadsLong = 1024;
 constexpr int kFew = 768;
 constexpr int kManyCtas = 304;
-// CTAs with every place up to which both kinds are one launch although the output is another one (4 x 248320 fp32, 244 CTAs:
-// 6.1 us, 8.3 in two launches; 129 x 40001, 645 CTAs: 14.6 and 16.6; 16 x 248320, 976 CTAs: 10.0 and 9.4).
-constexpr int kOneLaunch = 800;
-constexpr uint32_t kInPrompt = 0x80000000u;
-constexpr uint32_t kDrafted = 0x40000000u;
-// 16-byte slots, four per thread, where every place is written: 256 x 248320 bf16 42.6 us; 32-byte ones 45.4 to 46.3.
-constexpr int kSlotBytes = 16;
-constexpr int kUnroll = 4;
-constexpr int kMaxChunk = 32768;       // places of a dense CTA (a multiple of 128) at most
 // A hash table is at most 3/4 full and has 12 bytes per place: token, count, bias entry, list; a table by tokens has 8.
-constexpr int kShort = 3072;           // tokens up to which sparse CTAs are small: tables of 48 KiB
-constexpr int kHashed = 12288;         // tokens of the largest hash table
-constexpr int kRange = 24576;          // places of a table by tokens
+constexpr int kShort = 4096 / 4 * 3;  // tokens up to which several CTAs with a table fit an SM (48 KiB)
+constexpr int kHashed = 12288;   // tokens of the largest hash table
+constexpr int kRange = 24576;    // places of a table by tokens
 constexpr int kHashBytes = 12, kRangeBytes = 8;
 constexpr size_t kMostShort = (size_t)kShort / 3 * 4 * kHashBytes;
 constexpr size_t kMostLong = (size_t)kRange * kRangeBytes;
-static_assert(kMostLong >= (size_t)kHashed / 3 * 4 * kHashBytes && kMostShort >= (size_t)(kMaxChunk / 32 + 4) * 4, "one limit each");
+static_assert(kMostLong >= (size_t)kHashed / 3 * 4 * kHashBytes, "one limit for both kinds of table");
 
 struct Args {
     const void *in, *logits;
     void* out;
     long long in_stride, logits_stride, out_stride;
     int V, per_seq;
-    int rows, groups;    // rows of a sequence per CTA, and CTAs for them
-    int chunk, chunks;   // dense: places per CTA, and CTAs for the vocabulary
-    int table;           // sparse: places of the table (0: no place is marked)
-    bool hashed;         // a hash table, of a power of two
-    int range, parts;    // sparse: tokens of a table by tokens; CTAs that share a sequence's marked places
-    unsigned int sparse; // CTAs of the sparse kind, the first ones of the launch
+    int rows, groups;   // rows of a sequence per CTA, and CTAs for them
+    int chunk, chunks;  // k_process: places per CTA, and CTAs for the vocabulary
+    int table;          // k_process_marked: places of the table
+    bool hashed;        // a hash table, of a power of two
+    int range, parts;   // tokens of a table by tokens; CTAs that share a sequence's marked places
     vh_logits_rules r;
 };
 
@@ -85,6 +90,296 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* words, long long at,
     return n < 32 ? b & ((1u << n) - 1u) : b;
 }
 __device__ __forceinline__ bool bit_at(const uint32_t* words, long long at) { return ((words[at >> 5] >> (at & 31)) & 1u) != 0u; }
+
+// A row from place c0 on; its slots begin `shift` elements before an aligned place.
+template <typename T, typename TO>
+struct Row {
+    static constexpr int VEC = kSlotBytes / (int)sizeof(T);
+    const T* x;
+    TO* y;
+    const T* logits;
+    const uint32_t* ok;  // of the whole row
+    int shift;
+    __device__ __forceinline__ Row(const Args& a, long long row, long long c0) {
+        x = static_cast<const T*>(a.in) + row * a.in_stride + c0;
+        y = static_cast<TO*>(a.out) + row * a.out_stride + c0;
+        logits = static_cast<const T*>(a.logits) + row * a.logits_stride + c0;
+        ok = a.r.allowed != nullptr ? reinterpret_cast<const uint32_t*>(a.r.allowed) + row * a.r.allowed_stride : nullptr;
+        shift = (int)((reinterpret_cast<uintptr_t>(x) & (kSlotBytes - 1)) / sizeof(T));
+    }
+};
+
+// What a CTA knows of its chunk's tokens.  WIDE: counts of 32 bits, else of 16, two to a word; the highest bit is the prompt's.
+template <bool WIDE>
+struct Marks {
+    uint32_t* count;
+    uint32_t* bits;    // [chunk / 32], and a word that bits_at reads past them
+    uint16_t* entry;   // bias entry + 1 (null: no biases)
+    int words;
+    __host__ __device__ static constexpr size_t bytes(int chunk, bool biased) {
+        return (size_t)chunk * ((WIDE ? 4 : 2) + (biased ? 2 : 0)) + (size_t)(chunk / 32 + 4) * 4;  // a multiple of 16
+    }
+    __device__ __forceinline__ Marks(uint32_t* base, int chunk, bool biased) {
+        count = base;
+        bits = base + (WIDE ? chunk : chunk / 2);
+        words = chunk / 32;
+        entry = biased ? reinterpret_cast<uint16_t*>(bits + words + 4) : nullptr;
+    }
+    __device__ __forceinline__ void mark(int at) const { atomicOr(bits + (at >> 5), 1u << (at & 31)); }
+    __device__ __forceinline__ void add(int at, bool prompt) const {
+        uint32_t* w = count + (WIDE ? at : at >> 1);
+        const int sh = WIDE ? 0 : (at & 1) * 16;
+        if (prompt)
+            atomicOr(w, (WIDE ? 0x80000000u : 0x8000u) << sh);
+        else
+            atomicAdd(w, 1u << sh);
+        mark(at);
+    }
+    // The last entry of an id counts: the larger one, in its half of a word.
+    __device__ __forceinline__ void bias(int at, int i) const {
+        uint32_t* w = reinterpret_cast<uint32_t*>(entry) + (at >> 1);
+        const int sh = (at & 1) * 16;
+        uint32_t old = *w;
+        while (((old >> sh) & 0xFFFFu) < (uint32_t)(i + 1)) {
+            const uint32_t was = atomicCAS(w, old, (old & ~(0xFFFFu << sh)) | (uint32_t)(i + 1) << sh);
+            if (was == old) break;
+            old = was;
+        }
+        mark(at);
+    }
+    // Occurrences in output, and whether the prompt has the token.
+    __device__ __forceinline__ uint32_t get(int at, bool& prompt) const {
+        const uint32_t c = WIDE ? count[at] : (count[at >> 1] >> ((at & 1) * 16)) & 0xFFFFu;
+        prompt = (c & (WIDE ? 0x80000000u : 0x8000u)) != 0u;
+        return c & (WIDE ? 0x7FFFFFFFu : 0x7FFFu);
+    }
+};
+
+// What one sequence's rows share.
+struct Rules {
+    float rep, freq, pres, inv_temp;
+    const float* bias;
+    const int* draft;  // of the CTA's rows (shared memory), null: none
+};
+
+// A marked place of row j (of the CTA's), `v` its logit, or its gradient with `z` the logit.
+template <bool GRAD, bool WIDE>
+__device__ __forceinline__ float apply(const Rules& u, const Marks<WIDE>& c, int at, long long token, int j, float z, float v) {
+    const uint32_t e = c.entry != nullptr ? c.entry[at] : 0u;
+    if (e != 0u) z += u.bias[e - 1u];
+    bool seen;
+    uint32_t m = c.get(at, seen);
+    if (u.draft != nullptr)
+        for (int i = 0; i < j; ++i) m += u.draft[i] == token;
+    seen = seen || m > 0u;
+    float r = GRAD ? v : z;
+    if (seen) r = z > 0.0f ? __fdiv_rn(r, u.rep) : r * u.rep;
+    if (!GRAD && m > 0u) r = __fsub_rn(__fsub_rn(r, __fmul_rn(u.freq, (float)m)), u.pres);
+    return r * u.inv_temp;
+}
+
+// The slot at element e0 (counted from the Row's c0) of a row that has elements [lo, n).
+template <typename T, typename TO, bool GRAD>
+struct Slot {
+    static constexpr int VEC = Row<T, TO>::VEC;
+    RawVec<T, VEC> in;
+    uint32_t allow;
+    __device__ __forceinline__ void load(const Row<T, TO>& r, int e0, int lo, int n, long long c0, long long last_word) {
+        allow = (1u << VEC) - 1u;
+        if (e0 >= lo && e0 + VEC <= n) {
+            if (r.ok != nullptr) allow = bits_at(r.ok, c0 + e0, VEC, last_word);
+            if (allow != 0u) in.load(r.x + e0);
+        }
+    }
+    __device__ __forceinline__ float pick(int i) const {  // element i, by selects
+        const uint32_t u0 = in.u[0], u1 = in.u[1], u2 = in.u[2], u3 = in.u[3];
+        const int k = sizeof(T) == 4 ? i : i >> 1;
+        const uint32_t lo = (k & 1) ? u1 : u0, hi = (k & 1) ? u3 : u2, w = (k & 2) ? hi : lo;
+        if constexpr (sizeof(T) == 4) {
+            return __uint_as_float(w);
+        } else {
+            const unsigned short h = (unsigned short)(w >> ((i & 1) * 16));
+            return to_f32(*reinterpret_cast<const T*>(&h));
+        }
+    }
+    // marked(first element, number) -> bits; change(element, logit of the row or gradient) -> value.
+    template <typename M, typename C>
+    __device__ __forceinline__ void store(const Row<T, TO>& r, int e0, int lo, int n, long long c0, float scale, M marked,
+                                          C change) const {
+        constexpr int VO = kVecOf<TO>;
+        const float masked = GRAD ? 0.0f : neg_inf();
+        if (e0 >= n) return;
+        if (e0 >= lo && e0 + VEC <= n) {
+            float v[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = (allow >> i) & 1u ? in.get(i) * scale : masked;
+            uint32_t todo = marked(e0, VEC) & allow;
+            while (todo != 0u) {
+                const int i = __ffs((int)todo) - 1;
+                todo &= todo - 1u;
+                const float c = change(e0 + i, pick(i));
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) v[k] = k == i ? c : v[k];
+            }
+            if ((reinterpret_cast<uintptr_t>(r.y + e0) & 15) == 0) {
+#pragma unroll
+                for (int i = 0; i < VEC; i += VO) {
+                    RawVec<TO, VO> o;
+                    if constexpr (sizeof(TO) == 4) {
+#pragma unroll
+                        for (int q = 0; q < VO; ++q) o.u[q] = __float_as_uint(v[i + q]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < VO / 2; ++q) o.set2(q, v[i + 2 * q], v[i + 2 * q + 1]);
+                    }
+                    o.store(r.y + e0 + i);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) r.y[e0 + i] = from_f32<TO>(v[i]);
+            }
+        } else {  // the ends
+#pragma unroll 1
+            for (int e = max(e0, lo); e < min(e0 + VEC, n); ++e) {
+                float v = masked;
+                if (r.ok == nullptr || bit_at(r.ok, c0 + e)) {
+                    v = to_f32(r.x[e]);
+                    v = marked(e, 1) != 0u ? change(e, v) : v * scale;
+                }
+                r.y[e] = from_f32<TO>(v);
+            }
+        }
+    }
+};
+
+// Every place, a few slots per thread, all asked for before anything else; k_process_marked follows where places are marked.
+template <typename T, typename TO, bool GRAD>
+__global__ void __launch_bounds__(kThreadsP) k_process_stream(const Args a, int chunks, bool more) {
+    constexpr int VEC = Row<T, TO>::VEC;
+    constexpr int kStep = kThreadsP * VEC;
+    rows_wait();
+    if (more) rows_launch_dependents();
+    const long long row = blockIdx.x / chunks;
+    const long long c0 = (long long)(blockIdx.x % chunks) * (kStep * kStreamSlots);  // the slots begin `shift` before it
+    const Row<T, TO> r(a, row, c0);
+    const int lo = c0 > 0 ? -r.shift : 0, n = (int)min(a.V - c0, (long long)kStep * kStreamSlots);
+    const int e0 = (int)threadIdx.x * VEC - r.shift;
+    const long long last_word = ((long long)a.V + 31) / 32 - 1;
+    Slot<T, TO, GRAD> s[kStreamSlots];
+#pragma unroll
+    for (int k = 0; k < kStreamSlots; ++k) s[k].load(r, e0 + k * kStep, lo, n, c0, last_word);
+    const float temp = a.r.temperature != nullptr ? a.r.temperature[row / a.per_seq] : 1.0f;
+    const float inv_temp = temp > 0.0f ? __fdiv_rn(1.0f, temp) : 1.0f;
+#pragma unroll
+    for (int k = 0; k < kStreamSlots; ++k)
+        s[k].store(r, e0 + k * kStep, lo, n, c0, inv_temp, [](int, int) { return 0u; }, [](int, float v) { return v; });
+}
+
+template <typename T, typename TO, bool GRAD, bool WIDE>
+__global__ void __launch_bounds__(kThreadsP, kPerSm) k_process(const Args a) {
+    extern __shared__ __align__(16) uint32_t s_words[];
+    __shared__ int s_draft[kMaxRows];
+    constexpr int VEC = Row<T, TO>::VEC;
+    constexpr int kStep = kThreadsP * VEC;
+    rows_wait();
+    const unsigned int part = blockIdx.x / a.chunks;
+    const int seq = (int)(part / a.groups);
+    const int j0 = (int)(part % a.groups) * a.rows, j1 = min(j0 + a.rows, a.per_seq);
+    const long long c0 = (long long)(blockIdx.x % a.chunks) * a.chunk;
+    const int n = (int)min((long long)a.chunk, a.V - c0);
+    const long long last_word = ((long long)a.V + 31) / 32 - 1;
+    const int tid = threadIdx.x;
+    const bool biased = a.r.bias_ids != nullptr;
+    const Marks<WIDE> c(s_words, a.chunk, biased);
+
+    // The first slots, and everything that one look needs, are asked for before the rest begins.
+    Row<T, TO> r(a, (long long)seq * a.per_seq + j0, c0);
+    Slot<T, TO, GRAD> s[kUnroll];
+    int e = tid * VEC - r.shift;
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) s[k].load(r, e + k * kStep, 0, n, c0, last_word);
+    constexpr int BATCH = 4;
+    const int32_t* h = a.r.history != nullptr ? a.r.history + (size_t)seq * a.r.history_stride : nullptr;
+    int t[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) t[k] = h != nullptr && tid + k * kThreadsP < a.r.history_width ? h[tid + k * kThreadsP] : -1;
+    const int len = h == nullptr ? 0 : a.r.history_len != nullptr ? min(a.r.history_len[seq], a.r.history_width) : a.r.history_width;
+    const int prompt = h != nullptr && a.r.prompt_len != nullptr ? a.r.prompt_len[seq] : 0;
+    const int32_t* bias_ids = biased ? a.r.bias_ids + (size_t)seq * a.r.n_bias : nullptr;
+    const int first_bias = biased && tid < a.r.n_bias ? bias_ids[tid] : -1;
+    const int32_t* draft = a.r.draft_ids != nullptr && a.per_seq > 1 ? a.r.draft_ids + (size_t)seq * (a.per_seq - 1) : nullptr;
+
+    for (int i = tid; i < (int)(Marks<WIDE>::bytes(a.chunk, biased) / 16); i += kThreadsP)
+        reinterpret_cast<uint4*>(s_words)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (draft != nullptr && tid < j1 - 1 - j0) s_draft[tid] = draft[j0 + tid];
+    __syncthreads();
+    // The place of a token in the chunk, or -1.
+    auto place = [&](int token) {
+        const long long at = (long long)token - c0;
+        return at >= 0 && at < n ? (int)at : -1;
+    };
+    for (int base = tid; base < len; base += kThreadsP * BATCH) {
+        int next[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int i = base + (k + BATCH) * kThreadsP;
+            next[k] = i < len ? h[i] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int i = base + k * kThreadsP, at = place(t[k]);
+            if (i < len && at >= 0) c.add(at, i < prompt);
+            t[k] = next[k];
+        }
+    }
+    if (biased)
+        for (int i = tid; i < a.r.n_bias; i += kThreadsP) {
+            const int at = place(i == tid ? first_bias : bias_ids[i]);
+            if (at >= 0) c.bias(at, i);
+        }
+    if (draft != nullptr)
+        for (int i = tid; i < j1 - 1; i += kThreadsP) {
+            const int at = place(draft[i]);
+            if (at < 0) continue;
+            if (i < j0)
+                c.add(at, false);  // before all of the CTA's rows
+            else
+                c.mark(at);
+        }
+    Rules u;
+    u.rep = a.r.repetition != nullptr ? a.r.repetition[seq] : 1.0f;
+    u.freq = a.r.frequency != nullptr ? a.r.frequency[seq] : 0.0f;
+    u.pres = a.r.presence != nullptr ? a.r.presence[seq] : 0.0f;
+    const float temp = a.r.temperature != nullptr ? a.r.temperature[seq] : 1.0f;
+    u.inv_temp = temp > 0.0f ? __fdiv_rn(1.0f, temp) : 1.0f;
+    u.bias = biased ? a.r.bias + (size_t)seq * a.r.n_bias : nullptr;
+    u.draft = draft != nullptr ? s_draft : nullptr;
+    __syncthreads();
+
+    int j = j0;
+    while (true) {
+        auto store = [&](const Slot<T, TO, GRAD>& slot, int at_e) {
+            slot.store(r, at_e, 0, n, c0, u.inv_temp, [&](int at, int count) { return bits_at(c.bits, at, count, c.words); },
+                       [&](int at, float v) {
+                           const float z = GRAD ? to_f32(r.logits[at]) : v;
+                           return apply<GRAD, WIDE>(u, c, at, c0 + at, j - j0, z, v);
+                       });
+        };
+        store(s[0], e);
+        store(s[1], e + kStep);
+        static_assert(kUnroll == 2, "as written out here");
+        e += kUnroll * kStep;
+        if (e - tid * VEC >= n) {  // the row's last slots: the same for all threads
+            if (++j == j1) break;
+            r = Row<T, TO>(a, (long long)seq * a.per_seq + j, c0);
+            e = tid * VEC - r.shift;
+        }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) s[k].load(r, e + k * kStep, 0, n, c0, last_word);
+    }
+}
+
+// ---------------------------------------------------------------------------
 
 // The rows of a sequence that a CTA has, and what they share.
 struct Unit {
@@ -136,117 +431,6 @@ struct Unit {
     }
 };
 
-// ---------------------------------------------------------------------------
-
-// A row from place c0 on; slot i: elements [i * VEC - shift, +VEC).
-template <typename T, typename TO>
-struct Row {
-    static constexpr int VEC = kSlotBytes / (int)sizeof(T);
-    const T* x;
-    TO* y;
-    const uint32_t* ok;  // of the whole row
-    int shift;
-    __device__ __forceinline__ Row(const Args& a, long long row, long long c0) {
-        x = static_cast<const T*>(a.in) + row * a.in_stride + c0;
-        y = static_cast<TO*>(a.out) + row * a.out_stride + c0;
-        ok = a.r.allowed != nullptr ? reinterpret_cast<const uint32_t*>(a.r.allowed) + row * a.r.allowed_stride : nullptr;
-        shift = (int)((reinterpret_cast<uintptr_t>(x) & (kSlotBytes - 1)) / sizeof(T));
-    }
-};
-
-// The slot at element e0 (counted from the Row's c0) of a row that has elements [lo, n).
-template <typename T, typename TO, bool GRAD>
-struct Slot {
-    static constexpr int VEC = Row<T, TO>::VEC;
-    RawVec<T, VEC> in;
-    uint32_t allow;
-    __device__ __forceinline__ void load(const Row<T, TO>& r, int e0, int lo, int n, long long c0, long long last_word) {
-        allow = (1u << VEC) - 1u;
-        if (e0 >= lo && e0 + VEC <= n) {
-            if (r.ok != nullptr) allow = bits_at(r.ok, c0 + e0, VEC, last_word);
-            if (allow != 0u) in.load(r.x + e0);
-        }
-    }
-    // marked: places that are left out (null: none), of so many words and one more.
-    __device__ __forceinline__ void store(const Row<T, TO>& r, int e0, int lo, int n, long long c0, float scale,
-                                          const uint32_t* marked, int words) const {
-        constexpr int VO = kVecOf<TO>;
-        const float masked = GRAD ? 0.0f : neg_inf();
-        if (e0 >= n) return;
-        if (e0 >= lo && e0 + VEC <= n) {
-            const uint32_t skip = marked != nullptr ? bits_at(marked, e0, VEC, words) : 0u;
-            auto value = [&](int i) { return (allow >> i) & 1u ? in.get(i) * scale : masked; };
-            if (skip == 0u && (reinterpret_cast<uintptr_t>(r.y + e0) & 15) == 0) {
-#pragma unroll
-                for (int i = 0; i < VEC; i += VO) {
-                    RawVec<TO, VO> o;
-                    if constexpr (sizeof(TO) == 4) {
-#pragma unroll
-                        for (int q = 0; q < VO; ++q) o.u[q] = __float_as_uint(value(i + q));
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < VO / 2; ++q) o.set2(q, value(i + 2 * q), value(i + 2 * q + 1));
-                    }
-                    o.store(r.y + e0 + i);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    if (!((skip >> i) & 1u)) r.y[e0 + i] = from_f32<TO>(value(i));
-            }
-        } else {  // the ends
-#pragma unroll 1
-            for (int e = max(e0, lo); e < min(e0 + VEC, n); ++e)
-                if (marked == nullptr || !bit_at(marked, e))
-                    r.y[e] = from_f32<TO>(r.ok == nullptr || bit_at(r.ok, c0 + e) ? to_f32(r.x[e]) * scale : masked);
-        }
-    }
-};
-
-// Some rows of a sequence over a chunk, marked places left out.
-template <typename T, typename TO, bool GRAD>
-__device__ __forceinline__ void dense_but_marked(const Args& a, unsigned int block, uint32_t* marked) {
-    const Unit u(a, block / a.chunks);
-    const long long c0 = (long long)(block % a.chunks) * a.chunk;
-    const int n = (int)min((long long)a.chunk, a.V - c0);
-    const long long last_word = ((long long)a.V + 31) / 32 - 1;
-    const int tid = threadIdx.x;
-    const int words = a.chunk / 32;
-    constexpr int VEC = Row<T, TO>::VEC;
-    constexpr int kStep = kThreadsP * VEC;
-    Slot<T, TO, GRAD> s[2];  // one on its way while the other is stored
-    Row<T, TO> r(a, (long long)u.seq * a.per_seq + u.j0, c0);
-    s[0].load(r, tid * VEC - r.shift, 0, n, c0, last_word);
-    const int first = u.first_bias(a);
-    for (int i = tid; i <= words; i += kThreadsP) marked[i] = 0u;
-    __syncthreads();
-    auto mark = [&](int token) {
-        const long long at = (long long)token - c0;
-        if (at >= 0 && at < n) atomicOr(marked + (at >> 5), 1u << (at & 31));
-    };
-    u.history<kThreadsP>(a, [&](int token, bool) { mark(token); });
-    u.biases<kThreadsP>(a, first, [&](int token, int) { mark(token); });
-    if (u.draft != nullptr)
-        for (int i = tid; i < u.j1 - 1; i += kThreadsP) mark(__ldcg(u.draft + i));
-    __syncthreads();
-    for (int j = u.j0; j < u.j1; ++j) {
-        int e = tid * VEC - r.shift;
-        if (j > u.j0) {
-            r = Row<T, TO>(a, (long long)u.seq * a.per_seq + j, c0);
-            e = tid * VEC - r.shift;
-            s[0].load(r, e, 0, n, c0, last_word);
-        }
-        for (; e < n; e += 2 * kStep) {
-            s[1].load(r, e + kStep, 0, n, c0, last_word);
-            s[0].store(r, e, 0, n, c0, u.inv_temp, marked, words);
-            s[0].load(r, e + 2 * kStep, 0, n, c0, last_word);
-            s[1].store(r, e + kStep, 0, n, c0, u.inv_temp, marked, words);
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------
-
 struct Table {
     uint32_t* count;  // occurrences in output, kInPrompt, kDrafted
     uint16_t* entry;  // bias entry + 1
@@ -272,10 +456,12 @@ struct Table {
     __device__ __forceinline__ bool taken(int p) const { return key != nullptr ? key[p] != 0u : (count[p] != 0u || entry[p] != 0u); }
 };
 
-// LATE: what is read up to the logits is read past the first-level cache, before the previous kernel (the dense one, which has
-// waited for its predecessors before it let this one start) has ended.
-template <typename T, typename TO, bool GRAD, int THREADS, bool LATE>
-__device__ __forceinline__ void sparse(const Args& a, unsigned int block, uint32_t* smem) {
+// The marked places of some rows of a sequence.  Up to the wait this runs before the previous kernel has ended (the one that streams
+// the rows, which had waited for its own predecessors before it let this one start), and reads past the first-level cache.
+template <typename T, typename TO, bool GRAD, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_process_marked(const Args a) {
+    extern __shared__ __align__(16) uint32_t smem[];
+    const unsigned int block = blockIdx.x;
     __shared__ int s_taken;
     const float masked = GRAD ? 0.0f : neg_inf();
     const Unit u(a, block / a.parts);
@@ -338,7 +524,7 @@ __device__ __forceinline__ void sparse(const Args& a, unsigned int block, uint32
         if (taken) t.list[first + __popc(all & ((1u << (tid & 31)) - 1u))] = (uint16_t)(p0 + (tid & 31));
     }
     __syncthreads();
-    if constexpr (LATE) rows_wait();
+    rows_wait();
     constexpr int UNROLL = 4;  // places with their reads in flight
     for (int i0 = tid; i0 < s_taken; i0 += THREADS * UNROLL) {
         int token[UNROLL];
@@ -388,102 +574,11 @@ __device__ __forceinline__ void sparse(const Args& a, unsigned int block, uint32
     }
 }
 
-// Every place of a row, a few slots per thread, all asked for before anything else; the sparse kernel follows where there
-// are marked ones.
-template <typename T, typename TO, bool GRAD>
-__global__ void __launch_bounds__(kThreadsP) k_process(const Args a, int chunks) {
-    constexpr int VEC = Row<T, TO>::VEC;
-    constexpr int kStep = kThreadsP * VEC;
-    rows_wait();
-    if (a.table > 0) rows_launch_dependents();
-    const long long row = blockIdx.x / chunks;
-    const long long c0 = (long long)(blockIdx.x % chunks) * (kStep * kUnroll);  // the slots begin `shift` before it
-    const Row<T, TO> r(a, row, c0);
-    const int lo = c0 > 0 ? -r.shift : 0, n = (int)min(a.V - c0, (long long)kStep * kUnroll);
-    const int e0 = (int)threadIdx.x * VEC - r.shift;
-    const long long last_word = ((long long)a.V + 31) / 32 - 1;
-    Slot<T, TO, GRAD> s[kUnroll];
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) s[k].load(r, e0 + k * kStep, lo, n, c0, last_word);
-    const float temp = a.r.temperature != nullptr ? a.r.temperature[row / a.per_seq] : 1.0f;
-    const float inv_temp = temp > 0.0f ? __fdiv_rn(1.0f, temp) : 1.0f;
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) s[k].store(r, e0 + k * kStep, lo, n, c0, inv_temp, nullptr, 0);
-}
-template <typename T, typename TO, bool GRAD, int THREADS>
-__global__ void __launch_bounds__(THREADS) k_process_marked(const Args a) {
-    extern __shared__ __align__(16) uint32_t s_words[];
-    sparse<T, TO, GRAD, THREADS, true>(a, blockIdx.x, s_words);
-}
-
-// Both kinds in one launch, marked places left to the sparse ones.
-template <typename T, typename TO, bool GRAD>
-__global__ void __launch_bounds__(kThreadsP) k_process_apart(const Args a) {
-    extern __shared__ __align__(16) uint32_t s_words[];
-    rows_wait();
-    if (blockIdx.x < a.sparse)
-        sparse<T, TO, GRAD, kThreadsP, false>(a, blockIdx.x, s_words);
-    else
-        dense_but_marked<T, TO, GRAD>(a, blockIdx.x - a.sparse, s_words);
-}
-template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kThreadsLong) k_process_marked_first(const Args a) {
-    extern __shared__ __align__(16) uint32_t s_words[];
-    rows_wait();
-    sparse<T, T, GRAD, kThreadsLong, false>(a, blockIdx.x, s_words);
-}
-
 static int cut(long long n, long long by) { return (int)((n + by - 1) / by); }
-
-// How the work is cut.
-struct Plan {
-    int chunks;       // per row, where every place is written
-    long long whole;  // CTAs then
-    long long dense;  // CTAs that leave marked places out
-    long long sparse;
-    long long marks;  // places, at most
-    bool small;       // the sparse ones
-    size_t bitmap, table;
-    // size: of a logit
-    Plan(Args& a, int S, int size) {
-        const long long per = (long long)kThreadsP * kUnroll * (kSlotBytes / size);
-        chunks = cut((long long)a.V + kSlotBytes / size - 1, per);  // up to a slot less one begins before the row
-        whole = (long long)S * a.per_seq * chunks;
-        constexpr int kResident = 152 * 4;
-        // rows of a sequence share a table as long as the machine is filled
-        a.rows = std::min(a.per_seq, 8);
-        while (a.rows > 1 && (long long)S * cut(a.per_seq, a.rows) * cut(a.V, 4096) < kResident) a.rows = (a.rows + 1) / 2;
-        a.groups = cut(a.per_seq, a.rows);
-        // chunks of even size: some waves of CTAs, or one
-        const long long units = (long long)S * a.groups;
-        const long long wanted = std::max<long long>(1, std::min<long long>(cut(a.V, 8192) * units >= 4 * kResident ? 4 * kResident / units : kResident / units, cut(a.V, 1024)));
-        a.chunks = (int)std::max<long long>(cut(a.V, kMaxChunk), wanted);
-        a.chunk = cut(cut(a.V, a.chunks), 128) * 128;
-        a.chunks = cut(a.V, a.chunk);
-        dense = units * a.chunks;
-        marks = (a.r.history != nullptr ? a.r.history_width : 0) + (a.r.bias_ids != nullptr ? a.r.n_bias : 0) +
-                                (a.r.draft_ids != nullptr ? a.per_seq - 1ll : 0);
-        const long long most = std::min<long long>(marks, a.V);
-        sparse = 0;
-        small = most <= kShort;
-        bitmap = (size_t)(a.chunk / 32 + 4) * 4;
-        table = 0;
-        a.table = 0;
-        if (most > 0) {
-            a.hashed = most <= kHashed;
-            a.table = a.hashed ? 128 : kRange;
-            while (a.hashed && a.table * 3ll < most * 4) a.table *= 2;
-            a.range = kRange;
-            // a few hundred places per CTA while there are SMs left
-            a.parts = a.hashed ? (int)std::max<long long>(1, std::min<long long>({most / 256, 152 / units, 8})) : cut(a.V, kRange);
-            sparse = units * a.parts;
-            table = (size_t)a.table * (a.hashed ? kHashBytes : kRangeBytes);
-        }
-    }
-};
 
 template <typename... P, typename... A>
 static cudaError_t launch(void (*kernel)(P...), long long ctas, int threads, size_t smem, size_t most, cudaStream_t s, A... args) {
+    if (ctas > 2147483647ll) return cudaErrorInvalidValue;
     if (most > 0) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
         if (e != cudaSuccess) return e;
@@ -516,31 +611,47 @@ static cudaError_t run(const ProcessArgs& p, cudaStream_t s) {
     if (a.r.n_bias == 0) a.r.bias_ids = nullptr;
     if (a.r.history_width == 0) a.r.history = nullptr;
     if (a.per_seq == 1) a.r.draft_ids = nullptr;
-    const Plan plan(a, p.R / p.per_seq, (int)sizeof(T));
-    if (std::max(plan.whole, plan.dense + plan.sparse) > 2147483647ll) return cudaErrorInvalidValue;
-    cudaError_t e;
-    const bool in_place = p.out == p.in;
-    if (a.table == 0) return launch(k_process<T, TO, GRAD>, plan.whole, kThreadsP, 0, 0, s, a, plan.chunks);
-    if (plan.small && (in_place || plan.whole <= kOneLaunch)) {
-        a.sparse = (unsigned int)plan.sparse;
-        return launch(k_process_apart<T, TO, GRAD>, plan.sparse + plan.dense, kThreadsP, std::max(plan.bitmap, plan.table), kMostShort,
-                      s, a);
+    constexpr int VEC = kSlotBytes / (int)sizeof(T);
+    const int S = p.R / p.per_seq;
+    const bool biased = a.r.bias_ids != nullptr;
+    const long long drafts = a.r.draft_ids != nullptr ? a.per_seq - 1ll : 0, tokens = (a.r.history != nullptr ? a.r.history_width : 0) + drafts;
+    const long long marks = std::min<long long>(tokens + (biased ? a.r.n_bias : 0), a.V);  // at most
+    const int stream_chunks = cut((long long)a.V + VEC - 1, kThreadsP * kStreamSlots * VEC);  // a slot less one may begin before the row
+    const long long stream = (long long)p.R * stream_chunks;
+    if (marks == 0) return launch(k_process_stream<T, TO, GRAD>, stream, kThreadsP, 0, 0, s, a, stream_chunks, false);
+
+    // The rows of a sequence share a look through its history while the machine is filled.
+    constexpr long long kResident = 152 * kPerSm;
+    a.rows = std::min(a.per_seq, kMaxRows);
+    while (a.rows > 1 && (long long)S * cut(a.per_seq, a.rows) * cut(a.V, 4096) < kResident) a.rows = (a.rows + 1) / 2;
+    a.groups = cut(a.per_seq, a.rows);
+    const long long units = (long long)S * a.groups;
+
+    if (p.out == p.in || stream <= kOneLaunch) {
+        a.chunks = (int)std::max<long long>(cut(a.V, kChunk), std::min<long long>(cut(a.V, 1024), kResident / units));
+        a.chunk = cut(cut(a.V, a.chunks), 128) * 128;
+        a.chunks = cut(a.V, a.chunk);
+        return tokens <= kMostNarrow ? launch(k_process<T, TO, GRAD, false>, units * a.chunks, kThreadsP, Marks<false>::bytes(a.chunk, biased),
+                                              Marks<false>::bytes(kChunk, true), s, a)
+                                     : launch(k_process<T, TO, GRAD, true>, units * a.chunks, kThreadsP, Marks<true>::bytes(a.chunk, biased),
+                                              Marks<true>::bytes(kChunk, true), s, a);
     }
-    if (!in_place) {
-        e = launch(k_process<T, TO, GRAD>, plan.whole, kThreadsP, 0, 0, s, a, plan.chunks);
-        if (e != cudaSuccess) return e;
-        return plan.marks <= kFew && plan.sparse > kManyCtas
-                   ? launch(k_process_marked<T, TO, GRAD, kThreadsFew>, plan.sparse, kThreadsFew, plan.table, kMostShort, s, a)
-               : plan.small
-                   ? launch(k_process_marked<T, TO, GRAD, kThreadsShort>, plan.sparse, kThreadsShort, plan.table, kMostShort, s, a)
-                   : launch(k_process_marked<T, TO, GRAD, kThreadsLong>, plan.sparse, kThreadsLong, plan.table, kMostLong, s, a);
-    }
-    if constexpr (std::is_same<T, TO>::value) {
-        e = launch(k_process_marked_first<T, GRAD>, plan.sparse, kThreadsLong, plan.table, kMostLong, s, a);
-        if (e != cudaSuccess) return e;
-        return launch(k_process_apart<T, T, GRAD>, plan.dense, kThreadsP, plan.bitmap, kMostShort, s, a);
-    }
-    return cudaErrorInvalidValue;
+
+    a.hashed = marks <= kHashed;
+    a.table = a.hashed ? 128 : kRange;
+    while (a.hashed && a.table * 3ll < marks * 4) a.table *= 2;
+    a.range = kRange;
+    // a few hundred places per CTA while there are SMs left
+    a.parts = a.hashed ? (int)std::max<long long>(1, std::min<long long>({marks / 256, 152 / units, 8})) : cut(a.V, kRange);
+    const long long sparse = units * a.parts;
+    if (sparse > 2147483647ll) return cudaErrorInvalidValue;
+    const size_t table = (size_t)a.table * (a.hashed ? kHashBytes : kRangeBytes);
+    const cudaError_t e = launch(k_process_stream<T, TO, GRAD>, stream, kThreadsP, 0, 0, s, a, stream_chunks, true);
+    if (e != cudaSuccess) return e;
+    return marks <= kFew && sparse > kManyCtas
+               ? launch(k_process_marked<T, TO, GRAD, kThreadsFew>, sparse, kThreadsFew, table, kMostShort, s, a)
+           : marks <= kShort ? launch(k_process_marked<T, TO, GRAD, kThreadsShort>, sparse, kThreadsShort, table, kMostShort, s, a)
+                             : launch(k_process_marked<T, TO, GRAD, kThreadsLong>, sparse, kThreadsLong, table, kMostLong, s, a);
 }
 
 }  // namespace proc
