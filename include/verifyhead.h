@@ -43,7 +43,8 @@
  *    early right before a call.  Of this library's calls those that write
  *    rows or lists of ids for general use do not signal early
  *    (vh_add_rmsnorm; dx of vh_add_rmsnorm_grad; dlogits; log probabilities
- *    with alternatives; vh_nvfp4_pack): a table, rows or a list that they
+ *    with alternatives; vh_nvfp4_pack; vh_nvfp4_quantize, _tile, _dequantize
+ *    and _matmul; processed logits): a table, rows or a list that they
  *    write can be the next call's.  The draft and verify kernels signal early:
  *    their ids may be any later call's row_ids or draft_ids, and its cand_ids
  *    after a call or an operation that does not signal.
@@ -568,7 +569,7 @@ VH_API size_t vh_nvfp4_tiles_bytes(int rows, int H);
  *              NULL, the tiled layout (vh_nvfp4_tiles_bytes(T, H) bytes, 16-byte aligned)
  *  scales      device, uint8 [T][H/16] (out), or NULL
  *  row_scales  device, fp32 [T] (out), or NULL
- *  T >= 1; 16 <= H <= 65536, H % 16 == 0
+ *  1 <= T <= 2^31 - 1024 (and so V of vh_nvfp4_tile, T of vh_nvfp4_dequantize); 16 <= H <= 65536, H % 16 == 0
  * The outputs may not overlap x.
  */
 VH_API vh_status vh_nvfp4_quantize(const void* x, int dtype, int T, int H, int64_t x_stride, float tensor_scale,
@@ -603,7 +604,7 @@ VH_API vh_status vh_nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales
  *  x_scales device, fp32 [T], or NULL;  w_scales device, fp32 [V], or NULL
  *  x_scale, w_scale  finite; ignored where the array is given
  *  y        device, dtype [T][V] (out), y_stride >= V elements between rows
- *  T >= 1;  V >= 1;  16 <= H <= 65536, H % 16 == 0
+ *  1 <= T, V <= 2^31 - 1024;  16 <= H <= 65536, H % 16 == 0
  * Should a wait inside the kernel expire (see vh_workspace_error_offset), the
  * tile concerned is NaN.
  */
@@ -623,7 +624,7 @@ VH_API vh_status vh_nvfp4_matmul(const uint8_t* x, float x_scale, const float* x
 typedef struct {
     const int32_t* history;      /* [S][history_width]: the sequence's tokens, prompt first; ids outside [0,V) are passed over */
     int64_t history_stride;      /* elements between its rows, >= history_width */
-    int history_width;
+    int history_width;           /* 0..2^28 */
     const int32_t* history_len;  /* [S]: tokens of the row that count (at most history_width); NULL: all.  Both lengths are
                                     ignored without a history */
     const int32_t* prompt_len;   /* [S]: the first so many are the prompt's, the others output; NULL: 0 */

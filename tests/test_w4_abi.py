@@ -96,6 +96,16 @@ def test_shape(vh):
     assert process_grad(vh, dys=99) == vh.VH_ERR_SHAPE
 
 
+def test_sizes_past_the_counts(vh):
+    """Rows whose numbers would pass 31 bits within a block of threads, and histories whose counts would reach the bits beside
+    them."""
+    n = 2 ** 31 - 1023
+    assert quantize(vh, T=n) == vh.VH_ERR_SHAPE and dequantize(vh, T=n) == vh.VH_ERR_SHAPE
+    assert tile(vh, V=n, n=2 ** 60) == vh.VH_ERR_SHAPE and matmul(vh, T=n) == vh.VH_ERR_SHAPE
+    for call in (process, process_grad):
+        assert call(vh, history_width=2 ** 28 + 1, history_stride=2 ** 29) == vh.VH_ERR_SHAPE
+
+
 def test_alignment(vh):
     for kw in (dict(x=P + 1), dict(codes=P + 4), dict(codes=P + 8, scales=None), dict(rows=P + 2)):
         assert quantize(vh, **kw) == vh.VH_ERR_ALIGN, kw

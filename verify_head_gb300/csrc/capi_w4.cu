@@ -16,13 +16,15 @@ namespace {
 
 constexpr int kMaxWidth = 65536;
 constexpr int kMaxBias = 65535;
+constexpr int kMaxRows = vh::kMaxVocab;       // the rows of a block of threads still count in 32 bits
+constexpr int kMaxHistory = 1 << 28;          // counts of a token, with two bits beside them
 
 inline bool width_ok(int H) { return H >= 16 && H <= kMaxWidth && H % 16 == 0; }
 inline bool scale_ok(float g) { return g > 0.0f && g <= 3.4028234e38f; }
 
 vh_status check_rules(const vh_logits_rules& r, int R, int V, int per_seq) {
     if (per_seq < 1 || R % per_seq != 0) return VH_ERR_SHAPE;
-    if (r.history != nullptr && (r.history_width < 0 || r.history_stride < r.history_width)) return VH_ERR_SHAPE;
+    if (r.history != nullptr && (r.history_width < 0 || r.history_width > kMaxHistory || r.history_stride < r.history_width)) return VH_ERR_SHAPE;
     if ((r.bias_ids == nullptr) != (r.bias == nullptr)) return VH_ERR_NULL;
     if (r.bias_ids != nullptr && (r.n_bias < 0 || r.n_bias > kMaxBias)) return VH_ERR_SHAPE;
     if (r.allowed != nullptr && r.allowed_stride < ((long long)V + 31) / 32) return VH_ERR_SHAPE;
@@ -45,7 +47,7 @@ size_t vh_nvfp4_tiles_bytes(int rows, int H) { return rows < 1 || !width_ok(H) ?
 vh_status vh_nvfp4_quantize(const void* x, int dtype, int T, int H, int64_t x_stride, float tensor_scale, uint8_t* codes,
                             uint8_t* scales, float* row_scales, void* stream) {
     if (!x || !codes) return VH_ERR_NULL;
-    if (!known_dtype(dtype) || T < 1 || !width_ok(H) || x_stride < H) return VH_ERR_SHAPE;
+    if (!known_dtype(dtype) || T < 1 || T > kMaxRows || !width_ok(H) || x_stride < H) return VH_ERR_SHAPE;
     if (!row_scales && !scale_ok(tensor_scale)) return VH_ERR_SHAPE;
     if (!aligned(x, dtype_size(dtype)) || !aligned(codes, scales ? 8 : 16) || !aligned(row_scales, 4)) return VH_ERR_ALIGN;
     const vh_status st = check_device();
@@ -65,7 +67,7 @@ vh_status vh_nvfp4_quantize(const void* x, int dtype, int T, int H, int64_t x_st
 vh_status vh_nvfp4_tile(const uint8_t* codes, const uint8_t* scales, int V, int H, uint8_t* tiles, size_t tiles_bytes,
                         void* stream) {
     if (!codes || !scales || !tiles) return VH_ERR_NULL;
-    if (V < 1 || !width_ok(H)) return VH_ERR_SHAPE;
+    if (V < 1 || V > kMaxRows || !width_ok(H)) return VH_ERR_SHAPE;
     if (!aligned(codes, 8) || !aligned(tiles, 16)) return VH_ERR_ALIGN;
     if (tiles_bytes < vh_nvfp4_tiles_bytes(V, H)) return VH_ERR_WORKSPACE;
     const vh_status st = check_device();
@@ -76,7 +78,7 @@ vh_status vh_nvfp4_tile(const uint8_t* codes, const uint8_t* scales, int V, int 
 vh_status vh_nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int T, int H, float tensor_scale,
                               const float* row_scales, int dtype, void* y, int64_t y_stride, void* stream) {
     if (!codes || !y) return VH_ERR_NULL;
-    if (!known_dtype(dtype) || T < 1 || !width_ok(H) || y_stride < H) return VH_ERR_SHAPE;
+    if (!known_dtype(dtype) || T < 1 || T > kMaxRows || !width_ok(H) || y_stride < H) return VH_ERR_SHAPE;
     if (!row_scales && !(std::fabs(tensor_scale) <= 3.4028234e38f)) return VH_ERR_SHAPE;
     if (!aligned(codes, scales ? 8 : 16) || !aligned(row_scales, 4) || !aligned(y, dtype_size(dtype))) return VH_ERR_ALIGN;
     const vh_status st = check_device();
@@ -96,7 +98,7 @@ vh_status vh_nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int T
 vh_status vh_nvfp4_matmul(const uint8_t* x, float x_scale, const float* x_scales, const uint8_t* w, float w_scale,
                           const float* w_scales, int T, int V, int H, int dtype, void* y, int64_t y_stride, void* stream) {
     if (!x || !w || !y) return VH_ERR_NULL;
-    if (!known_dtype(dtype) || T < 1 || V < 1 || V > vh::kMaxVocab || T > vh::kMaxVocab || !width_ok(H) || y_stride < V)
+    if (!known_dtype(dtype) || T < 1 || V < 1 || V > vh::kMaxVocab || T > kMaxRows || !width_ok(H) || y_stride < V)
         return VH_ERR_SHAPE;
     if ((!x_scales && !(std::fabs(x_scale) <= 3.4028234e38f)) || (!w_scales && !(std::fabs(w_scale) <= 3.4028234e38f)))
         return VH_ERR_SHAPE;
