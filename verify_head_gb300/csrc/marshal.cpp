@@ -1,6 +1,6 @@
-// Argument marshalling of the norm, log-probability, 4-bit row and logit-processing calls in compiled code: the checks of the Python binding on
-// torch tensors, then the call through the C ABI.  A decode step makes these calls on a handful of rows, where reading
-// a tensor's type, sizes, strides and address from Python takes longer than the kernel (4 x 2048 norm: 6.95 us a
+// Argument marshalling of the norm, log-probability, 4-bit row and logit-processing calls in compiled code: the checks
+// of the Python binding on torch tensors, then the call through the C ABI.  A decode step makes these calls on a handful
+// of rows, where reading a tensor's type, sizes, strides and address from Python takes longer than the kernel (4 x 2048 norm: 6.95 us a
 // call from Python alone, 2.1 us from here).
 //
 // Every function returns 0 (done), a negative vh_status, or 1: the arguments are not of the usual kind (an output to

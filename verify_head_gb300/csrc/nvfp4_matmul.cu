@@ -11,6 +11,10 @@
 // neighbours of a row.  (One row after the other for all, the rows' scales by shuffles: 256 x 248320 x 2048 took 113 us, and
 // 104 with a quarter of the contraction: the epilogue set the pace.)
 //
+// Bound: the stream of W for few rows (4 x 248320 x 2048 44.5 us, 0.97 of the copy rate), what L2 gives an SM for many (4096 x 8192 x
+// 8192 88 us, 6.2 PFLOP/s; the pairs below).  Up to 32 rows of X a stage has 32 lines of X and there are eight stages of W, so
+// that enough of it is on its way; with few tiles a cluster shares the records of one (1 x 4096 x 4096 5.8 us, 9.9 with a CTA each).
+//
 // Every wait is bounded; on expiry the CTA's flag is set, the tiles concerned become NaN, copies in flight are waited for, and
 // TMEM is freed.
 #include <algorithm>
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
 // CTA's TMEM has the accumulators of its own rows of W and the scales of all rows of X, 32 rows to a column and a record's in four
 // columns (tcgen05.cp writes four at a time, at a multiple of four).
 //
-// A stage is 38 KiB per CTA for 512 cycles of MMAs, a little more than an SM is given by L2 (64 bytes a cycle): 0.39 us, 5.9
+// A stage is 38 KiB per CTA for 512 cycles of MMAs, a little more than an SM is given by L2 (64 bytes a cycle): 0.39 us, 6.2
 // PFLOP/s.  Two accumulators of 256 columns would leave the scales no room: there is one, and the epilogue takes all of it into
 // registers, in two halves, the second before it hands it back; every tile waits for that and the writing of the first, about
 // 2.2 us.  (Pairs on one record, with two accumulators: 4096 x 8192 x 8192 138 us, 88 with two;
