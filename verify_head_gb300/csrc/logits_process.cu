@@ -18,16 +18,24 @@
 // histories past its size several CTAs have a range of the vocabulary each,
 // with a place for every token.
 //
-// Small calls, where a launch counts, and outputs that are the inputs, whose
-// marked places the first kernel would have lost: one kernel (k_process).  A
-// CTA has some rows of one sequence over a chunk of the vocabulary.  It looks
-// through the history, its first slots of logits already on their way, and
-// counts the tokens of its chunk, 16 bits each unless a history is longer than
-// that counts, with a bitmap of the marked places; those are changed in their
-// slot's registers, so that every slot is read and written once, by one
-// thread.  Most warps have a marked place in some lane and wait for it: 256 x
-// 248320 bf16 with histories of 4096 94 us this way, 58 in two kernels; 4 x
-// 248320 fp32 5.4 us, 8.3 in two.
+// Small calls, where a launch counts: one kernel (k_process_small).  A CTA has
+// some rows of one sequence over a chunk of the vocabulary.  It looks through
+// the history, the slots of a row of logits already on their way, counts the
+// tokens of its chunk in 16 bits each and lists the marked places.  It writes
+// all of a row's places, and after a barrier the listed ones again, shared out
+// over its threads.
+//
+// Outputs that are the inputs, whose marked places would be lost that way, and
+// small calls with long histories: one kernel (k_process) that counts like this
+// and changes a marked place in its slot's registers, so that every slot is
+// read and written once, by one thread.  Most warps have a marked place in some
+// lane and wait for it.
+//
+//     us                                        small    in registers    two kernels
+//     4 x 248320 fp32, history 1500               5.1             5.5            8.3
+//     129 x 40001 fp16 to fp32, masked, 700      11.7            13.3           16.6
+//     4 x 248320 fp32, history 8000              11.9             9.6
+//     256 x 248320 bf16, histories of 4096       69.4            94             58
 //
 // Bound: memory (the logits once in and once out).  256 x 248320 bf16: 43 us
 // without a history (255 MB: 0.89 of the copy rate), 45 with 512 tokens, 58 with
@@ -44,14 +52,18 @@ namespace proc {
 
 constexpr int kThreadsP = 256;
 constexpr int kSlotBytes = 16;   // of logits per thread and load (256 x 248320 bf16 42.6 us; 32 bytes 45.4)
-constexpr int kStreamSlots = 4;  // slots per thread, all asked for at once: where every place is written,
-constexpr int kUnroll = 2;       // and in k_process (four: as fast or slower)
+constexpr int kStreamSlots = 4;  // slots per thread, all asked for at once; in k_process
+constexpr int kUnroll = 2;       // (four: as fast or slower)
 constexpr int kMaxRows = 8;      // of a sequence per CTA
-// Calls of up to so many CTAs of k_process_stream take k_process (4 x 248320 fp32, 244: 5.4 us, 8.3 in two kernels; 129 x 40001,
-// 645: 13.7 and 16.6; 16 x 248320, 976: 10.0 and 9.4).
+// Calls of up to so many CTAs of k_process_stream are small (129 x 40001, 645: above; 16 x 248320, 976: 10.0 us in registers, 9.4 in
+// two kernels), and histories of up to kFewTokens are short (4 x 248320 with 3000: 6.4 us listed, 6.3 in registers; 129 x 40001 with
+// 1500: 12.9 and 14.6, with 3000: 16.6 and 15.9).
 constexpr int kOneLaunch = 800;
-constexpr int kChunk = 8192;     // places of a CTA of k_process at most (a multiple of 128)
-constexpr int kPerSm = 4;        // of them
+constexpr int kFewTokens = 2048;
+constexpr int kPerSm = 4;       // CTAs of k_process
+constexpr int kPerSmSmall = 5;  // and of k_process_small (four: 129 x 40001 12.6 us, in more than one wave; 4 x 248320 5.0)
+constexpr int kChunk = 8192;    // places of a CTA of k_process at most (a multiple of 128)
+constexpr int kBefore = 128;    // places of k_process_small's table before its chunk (a slot's at least, whole words of 16 bytes)
 constexpr int kMostNarrow = 32767;  // tokens that 16-bit counts hold, beside the prompt's bit
 constexpr uint32_t kInPrompt = 0x80000000u;
 constexpr uint32_t kDrafted = 0x40000000u;
@@ -125,7 +137,11 @@ struct Marks {
         words = chunk / 32;
         entry = biased ? reinterpret_cast<uint16_t*>(bits + words + 4) : nullptr;
     }
-    __device__ __forceinline__ void mark(int at) const { atomicOr(bits + (at >> 5), 1u << (at & 31)); }
+    // Whether the place had not been marked.
+    __device__ __forceinline__ bool mark(int at) const {
+        const uint32_t bit = 1u << (at & 31);
+        return (atomicOr(bits + (at >> 5), bit) & bit) == 0u;
+    }
     __device__ __forceinline__ void add(int at, bool prompt) const {
         uint32_t* w = count + (WIDE ? at : at >> 1);
         const int sh = WIDE ? 0 : (at & 1) * 16;
@@ -133,7 +149,6 @@ struct Marks {
             atomicOr(w, (WIDE ? 0x80000000u : 0x8000u) << sh);
         else
             atomicAdd(w, 1u << sh);
-        mark(at);
     }
     // The last entry of an id counts: the larger one, in its half of a word.
     __device__ __forceinline__ void bias(int at, int i) const {
@@ -145,7 +160,6 @@ struct Marks {
             if (was == old) break;
             old = was;
         }
-        mark(at);
     }
     // Occurrences in output, and whether the prompt has the token.
     __device__ __forceinline__ uint32_t get(int at, bool& prompt) const {
@@ -328,23 +342,26 @@ __global__ void __launch_bounds__(kThreadsP, kPerSm) k_process(const Args a) {
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
             const int i = base + k * kThreadsP, at = place(t[k]);
-            if (i < len && at >= 0) c.add(at, i < prompt);
+            if (i < len && at >= 0) {
+                c.add(at, i < prompt);
+                c.mark(at);
+            }
             t[k] = next[k];
         }
     }
     if (biased)
         for (int i = tid; i < a.r.n_bias; i += kThreadsP) {
             const int at = place(i == tid ? first_bias : bias_ids[i]);
-            if (at >= 0) c.bias(at, i);
+            if (at < 0) continue;
+            c.bias(at, i);
+            c.mark(at);
         }
     if (draft != nullptr)
         for (int i = tid; i < j1 - 1; i += kThreadsP) {
             const int at = place(draft[i]);
             if (at < 0) continue;
-            if (i < j0)
-                c.add(at, false);  // before all of the CTA's rows
-            else
-                c.mark(at);
+            if (i < j0) c.add(at, false);  // before all of the CTA's rows
+            c.mark(at);
         }
     Rules u;
     u.rep = a.r.repetition != nullptr ? a.r.repetition[seq] : 1.0f;
@@ -376,6 +393,128 @@ __global__ void __launch_bounds__(kThreadsP, kPerSm) k_process(const Args a) {
         }
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) s[k].load(r, e + k * kStep, 0, n, c0, last_word);
+    }
+}
+
+// Every place of some rows of a sequence, then the marked ones again.  A chunk has as many places as the CTA's threads have slots;
+// as the slots begin `shift` places before it, so does the table.  The slots of the next row are on their way while a row's
+// marked places are written.
+template <typename T, typename TO, bool GRAD>
+__global__ void __launch_bounds__(kThreadsP, kPerSmSmall) k_process_small(const Args a) {
+    extern __shared__ __align__(16) uint32_t s_words[];
+    __shared__ int s_draft[kMaxRows];
+    __shared__ int s_marks;
+    constexpr int VEC = Row<T, TO>::VEC;
+    constexpr int kStep = kThreadsP * VEC;
+    constexpr int kPlaces = kStep * kStreamSlots;
+    rows_wait();
+    const unsigned int part = blockIdx.x / a.chunks;
+    const int seq = (int)(part / a.groups);
+    const int j0 = (int)(part % a.groups) * a.rows, j1 = min(j0 + a.rows, a.per_seq);
+    const long long c0 = (long long)(blockIdx.x % a.chunks) * kPlaces;
+    const long long last_word = ((long long)a.V + 31) / 32 - 1;
+    const int tid = threadIdx.x;
+    const bool biased = a.r.bias_ids != nullptr;
+    const Marks<false> c(s_words, kPlaces + kBefore, biased);
+    uint16_t* list = reinterpret_cast<uint16_t*>(s_words + Marks<false>::bytes(kPlaces + kBefore, biased) / 4);
+    const int lo = c0 > 0 ? -VEC : 0, n = (int)min(a.V - c0, (long long)kPlaces);  // of all rows
+
+    Row<T, TO> r(a, (long long)seq * a.per_seq + j0, c0);
+    Slot<T, TO, GRAD> s[kStreamSlots];
+    int from, to, e;  // the places that the row's slots hold, and the thread's first slot
+    auto load = [&]() {
+        from = c0 > 0 ? -r.shift : 0;
+        to = (int)min(a.V - c0, (long long)kPlaces - r.shift);
+        e = tid * VEC - r.shift;
+#pragma unroll
+        for (int k = 0; k < kStreamSlots; ++k) s[k].load(r, e + k * kStep, from, to, c0, last_word);
+    };
+    load();
+    constexpr int BATCH = 4;
+    const int32_t* h = a.r.history != nullptr ? a.r.history + (size_t)seq * a.r.history_stride : nullptr;
+    int t[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) t[k] = h != nullptr && tid + k * kThreadsP < a.r.history_width ? h[tid + k * kThreadsP] : -1;
+    const int len = h == nullptr ? 0 : a.r.history_len != nullptr ? min(a.r.history_len[seq], a.r.history_width) : a.r.history_width;
+    const int prompt = h != nullptr && a.r.prompt_len != nullptr ? a.r.prompt_len[seq] : 0;
+    const int32_t* bias_ids = biased ? a.r.bias_ids + (size_t)seq * a.r.n_bias : nullptr;
+    const int first_bias = biased && tid < a.r.n_bias ? bias_ids[tid] : -1;
+    const int32_t* draft = a.r.draft_ids != nullptr && a.per_seq > 1 ? a.r.draft_ids + (size_t)seq * (a.per_seq - 1) : nullptr;
+
+    for (int i = tid; i < (int)(Marks<false>::bytes(kPlaces + kBefore, biased) / 16); i += kThreadsP)
+        reinterpret_cast<uint4*>(s_words)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (draft != nullptr && tid < j1 - 1 - j0) s_draft[tid] = draft[j0 + tid];
+    if (tid == 0) s_marks = 0;
+    __syncthreads();
+    // f(place in the table) for a token of the chunk; the first to mark it puts it on the list
+    auto with = [&](int token, auto f) {
+        const long long at = (long long)token - c0;
+        if (at < lo || at >= n) return;
+        const int p = (int)at + kBefore;
+        f(p);
+        if (c.mark(p)) list[atomicAdd(&s_marks, 1)] = (uint16_t)p;
+    };
+    for (int base = tid; base < len; base += kThreadsP * BATCH) {
+        int next[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int i = base + (k + BATCH) * kThreadsP;
+            next[k] = i < len ? h[i] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int i = base + k * kThreadsP;
+            if (i < len) with(t[k], [&](int p) { c.add(p, i < prompt); });
+            t[k] = next[k];
+        }
+    }
+    if (biased)
+        for (int i = tid; i < a.r.n_bias; i += kThreadsP)
+            with(i == tid ? first_bias : bias_ids[i], [&](int p) { c.bias(p, i); });
+    if (draft != nullptr)
+        for (int i = tid; i < j1 - 1; i += kThreadsP)
+            with(draft[i], [&](int p) {
+                if (i < j0) c.add(p, false);  // before all of the CTA's rows
+            });
+    Rules u;
+    u.rep = a.r.repetition != nullptr ? a.r.repetition[seq] : 1.0f;
+    u.freq = a.r.frequency != nullptr ? a.r.frequency[seq] : 0.0f;
+    u.pres = a.r.presence != nullptr ? a.r.presence[seq] : 0.0f;
+    const float temp = a.r.temperature != nullptr ? a.r.temperature[seq] : 1.0f;
+    u.inv_temp = temp > 0.0f ? __fdiv_rn(1.0f, temp) : 1.0f;
+    u.bias = biased ? a.r.bias + (size_t)seq * a.r.n_bias : nullptr;
+    u.draft = draft != nullptr ? s_draft : nullptr;
+    __syncthreads();
+    const int marks = s_marks;
+
+    for (int j = j0; j < j1; ++j) {
+        const Row<T, TO> now = r;
+        const int begin = from, end = to;
+        // a marked place that the row's slots hold, or begin - 1
+        auto place = [&](int k) {
+            const int at = k < marks ? (int)list[k] - kBefore : begin - 1;
+            return at >= begin && at < end && (now.ok == nullptr || bit_at(now.ok, c0 + at)) ? at : begin - 1;
+        };
+        auto value = [&](int at) {
+            const float v = to_f32(now.x[at]);
+            return apply<GRAD, false>(u, c, at + kBefore, c0 + at, j - j0, GRAD ? to_f32(now.logits[at]) : v, v);
+        };
+        const int at = place(tid);
+        float v = 0.0f;
+        if (at >= begin) v = value(at);
+#pragma unroll
+        for (int k = 0; k < kStreamSlots; ++k)
+            s[k].store(now, e + k * kStep, begin, end, c0, u.inv_temp, [](int, int) { return 0u; }, [](int, float x) { return x; });
+        if (j + 1 < j1) {
+            r = Row<T, TO>(a, (long long)seq * a.per_seq + j + 1, c0);
+            load();
+        }
+        __syncthreads();
+        if (at >= begin) now.y[at] = from_f32<TO>(v);
+        for (int k = tid + kThreadsP; k < marks; k += kThreadsP) {
+            const int more = place(k);
+            if (more >= begin) now.y[more] = from_f32<TO>(value(more));
+        }
     }
 }
 
@@ -627,6 +766,13 @@ static cudaError_t run(const ProcessArgs& p, cudaStream_t s) {
     a.groups = cut(a.per_seq, a.rows);
     const long long units = (long long)S * a.groups;
 
+    if (p.out != p.in && stream <= kOneLaunch && tokens <= kFewTokens) {
+        constexpr int kPlaces = kThreadsP * VEC * kStreamSlots, kListed = kPlaces + VEC;
+        a.chunks = stream_chunks;
+        return launch(k_process_small<T, TO, GRAD>, units * a.chunks, kThreadsP,
+                      Marks<false>::bytes(kPlaces + kBefore, biased) + (size_t)std::min<long long>(marks, kListed) * 2,
+                      Marks<false>::bytes(kPlaces + kBefore, true) + kListed * 2, s, a);
+    }
     if (p.out == p.in || stream <= kOneLaunch) {
         a.chunks = (int)std::max<long long>(cut(a.V, kChunk), std::min<long long>(cut(a.V, 1024), kResident / units));
         a.chunk = cut(cut(a.V, a.chunks), 128) * 128;
