@@ -632,7 +632,8 @@ typedef struct {
     const float* repetition;     /* [S] > 0 */
     const float* frequency;      /* [S] */
     const float* presence;       /* [S] */
-    const float* temperature;    /* [S]; 0 and less stand for 1 (a greedy sequence) */
+    const float* temperature;    /* [S]; 0 and less stand for 1 (a greedy sequence); 1 / temperature is at most
+                                    the largest fp32 number */
     const int32_t* bias_ids;     /* [S][n_bias]: ids outside [0,V) are passed over, the last entry of an id counts */
     const float* bias;           /* [S][n_bias] */
     int n_bias;                  /* 0..65535 */

@@ -204,3 +204,22 @@ def test_what_one_call_writes_the_next_reads(vh):
             o.zero_(), i.zero_()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(run(lambda: None), want))
+
+
+@pytest.mark.parametrize("L", [0, 3, 4000])
+@pytest.mark.parametrize("S", [1, 1200])
+def test_temperatures_next_to_zero(vh, L, S):
+    """A temperature whose reciprocal is no fp32 number: 0 stays 0, the others keep their sign and order."""
+    V = 2055
+    x = torch.zeros(S, V, device="cuda")
+    x[:, 1::4], x[:, 2::4] = 1.0, -1.0
+    t = torch.full((S,), 1e-42, device="cuda")
+    r = dict(temperature=t)
+    if L:
+        r.update(history=torch.arange(L, dtype=torch.int32, device="cuda")[None].expand(S, L).contiguous() % V,
+                 repetition=torch.full((S,), 1.5, device="cuda"))
+    y = vh.logits_process(x, **r)
+    assert bool((y[:, 0::4] == 0).all()) and bool((y[:, 3::4] == 0).all())
+    assert bool((y[:, 1::4] > 1e37).all()) and bool((y[:, 2::4] < -1e37).all())
+    d = vh.logits_process_grad(x, x.clone(), **r)
+    assert not bool(torch.isnan(d).any()) and bool((d[:, 0::4] == 0).all())

@@ -103,6 +103,11 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* words, long long at,
 }
 __device__ __forceinline__ bool bit_at(const uint32_t* words, long long at) { return ((words[at >> 5] >> (at & 31)) & 1u) != 0u; }
 
+// Of a temperature; a finite number also where that is below 2^-128, since 0 times it has to be 0.
+__device__ __forceinline__ float inverse(float temp) {
+    return temp > 0.0f ? fminf(__fdiv_rn(1.0f, temp), 3.40282347e38f) : 1.0f;
+}
+
 // A row from place c0 on; its slots begin `shift` elements before an aligned place.
 template <typename T, typename TO>
 struct Row {
@@ -283,7 +288,7 @@ __global__ void __launch_bounds__(kThreadsP) k_process_stream(const Args a, int 
 #pragma unroll
     for (int k = 0; k < kStreamSlots; ++k) s[k].load(r, e0 + k * kStep, lo, n, c0, last_word);
     const float temp = a.r.temperature != nullptr ? a.r.temperature[row / a.per_seq] : 1.0f;
-    const float inv_temp = temp > 0.0f ? __fdiv_rn(1.0f, temp) : 1.0f;
+    const float inv_temp = inverse(temp);
 #pragma unroll
     for (int k = 0; k < kStreamSlots; ++k)
         s[k].store(r, e0 + k * kStep, lo, n, c0, inv_temp, [](int, int) { return 0u; }, [](int, float v) { return v; });
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__(kThreadsP, kPerSm) k_process(const Args a) {
     u.freq = a.r.frequency != nullptr ? a.r.frequency[seq] : 0.0f;
     u.pres = a.r.presence != nullptr ? a.r.presence[seq] : 0.0f;
     const float temp = a.r.temperature != nullptr ? a.r.temperature[seq] : 1.0f;
-    u.inv_temp = temp > 0.0f ? __fdiv_rn(1.0f, temp) : 1.0f;
+    u.inv_temp = inverse(temp);
     u.bias = biased ? a.r.bias + (size_t)seq * a.r.n_bias : nullptr;
     u.draft = draft != nullptr ? s_draft : nullptr;
     __syncthreads();
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(kThreadsP, kPerSmSmall) k_process_small(const 
     u.freq = a.r.frequency != nullptr ? a.r.frequency[seq] : 0.0f;
     u.pres = a.r.presence != nullptr ? a.r.presence[seq] : 0.0f;
     const float temp = a.r.temperature != nullptr ? a.r.temperature[seq] : 1.0f;
-    u.inv_temp = temp > 0.0f ? __fdiv_rn(1.0f, temp) : 1.0f;
+    u.inv_temp = inverse(temp);
     u.bias = biased ? a.r.bias + (size_t)seq * a.r.n_bias : nullptr;
     u.draft = draft != nullptr ? s_draft : nullptr;
     __syncthreads();
@@ -530,7 +535,7 @@ struct Unit {
         j0 = (int)(group % a.groups) * a.rows;
         j1 = min(j0 + a.rows, a.per_seq);
         const float temp = a.r.temperature != nullptr ? __ldcg(a.r.temperature + seq) : 1.0f;
-        inv_temp = temp > 0.0f ? __fdiv_rn(1.0f, temp) : 1.0f;
+        inv_temp = inverse(temp);
         draft = a.r.draft_ids != nullptr && a.per_seq > 1 ? a.r.draft_ids + (size_t)seq * (a.per_seq - 1) : nullptr;
     }
     // f(token, whether it is the prompt's) for every token of the history, over the CTA's threads.  The first tokens are asked
