@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import w4_util as u
-from rows_util import close
+from rows_util import TINY, U, close
 from test_gpu_logits_process import check, check_grad, rows, tolerance
 
 pytestmark = pytest.mark.gpu
@@ -223,3 +223,29 @@ def test_temperatures_next_to_zero(vh, L, S):
     assert bool((y[:, 1::4] > 1e37).all()) and bool((y[:, 2::4] < -1e37).all())
     d = vh.logits_process_grad(x, x.clone(), **r)
     assert not bool(torch.isnan(d).any()) and bool((d[:, 0::4] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("S,m,V,L", [(300, 1, 20011, 5000), (150, 2, 16384, 4200), (40, 2, 70003, 6000)])
+def test_long_histories_of_many_sequences(vh, S, m, V, L, dtype):
+    """Histories of a good part of the vocabulary, on both sides of a twentieth and of 4096 tokens; a few sequences are compared."""
+    g = torch.Generator().manual_seed(S)
+    x = rows(g, S * m, V, dtype, V + 3, 1)
+    r = dict(history=torch.randint(0, V, (S, L), generator=g, dtype=torch.int32).cuda(),
+             prompt_len=torch.randint(0, L, (S,), generator=g, dtype=torch.int32).cuda(),
+             repetition=(0.8 + torch.rand(S, generator=g)).cuda(), frequency=torch.rand(S, generator=g).cuda(),
+             presence=torch.rand(S, generator=g).cuda(), bias_ids=torch.randint(0, V, (S, 40), generator=g, dtype=torch.int32).cuda(),
+             bias=torch.randn(S, 40, generator=g).cuda())
+    if m > 1:
+        r["draft_ids"] = torch.randint(0, V, (S, m - 1), generator=g, dtype=torch.int32).cuda()
+    out = vh.logits_process(x, **r)
+    d = rows(g, S * m, V, dtype, None, 0, 0.1)
+    grad = vh.logits_process_grad(d, x, **r)
+    for s in (0, S // 2, S - 1):
+        some = {k: v[s:s + 1] for k, v in r.items()}
+        at = slice(s * m, (s + 1) * m)
+        rel, floor = tolerance(dtype, x[at], some)
+        close(out[at], u.process64(x[at], 1, some), rel, floor)
+        close(grad[at], u.process64(x[at], 1, some, d[at]), U[dtype] + 2.0 ** -22, TINY[dtype])
+    same = x.clone()
+    assert torch.equal(vh.logits_process(same, out=same, **r), out)

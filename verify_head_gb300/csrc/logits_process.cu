@@ -26,15 +26,18 @@
 // over its threads.
 //
 // Outputs that are the inputs, whose marked places would be lost that way, and
-// small calls with long histories: one kernel (k_process) that counts like this
-// and changes a marked place in its slot's registers, so that every slot is
-// read and written once, by one thread.  Most warps have a marked place in some
-// lane and wait for it.
+// long histories of small calls or of most of the vocabulary: one kernel
+// (k_process) that counts like this and changes a marked place in its slot's
+// registers, so that every slot is read and written once, by one thread.  Most
+// warps have a marked place in some lane and wait for it.  With long histories
+// its CTAs have 1,024 threads and chunks to match, so that fewer of them look
+// through the same one.
 //
 //     us                                        small    in registers    two kernels
 //     4 x 248320 fp32, history 1500               5.1             5.5            8.3
 //     129 x 40001 fp16 to fp32, masked, 700      11.7            13.3           16.6
-//     4 x 248320 fp32, history 8000              11.9             9.6
+//     4 x 248320 fp32, history 8000              11.9             7.4
+//     201 x 65536 fp16, masked, 9951                             35             59
 //     256 x 248320 bf16, histories of 4096       69.4            94             58
 //
 // Bound: memory (the logits once in and once out).  256 x 248320 bf16: 43 us
@@ -43,6 +46,7 @@
 // filled and written again, long after the stream has left L2.  The gradient of
 // 2048 x 65536: 89 us (0.90) and, with 512 tokens, 110.
 #include <algorithm>
+#include <type_traits>
 
 #include "vh_row_kernels.h"
 #include "vh_rows.cuh"
@@ -56,13 +60,17 @@ constexpr int kStreamSlots = 4;  // slots per thread, all asked for at once; in 
 constexpr int kUnroll = 2;       // (four: as fast or slower)
 constexpr int kMaxRows = 8;      // of a sequence per CTA
 // Calls of up to so many CTAs of k_process_stream are small (129 x 40001, 645: above; 16 x 248320, 976: 10.0 us in registers, 9.4 in
-// two kernels), and histories of up to kFewTokens are short (4 x 248320 with 3000: 6.4 us listed, 6.3 in registers; 129 x 40001 with
-// 1500: 12.9 and 14.6, with 3000: 16.6 and 15.9).
+// two kernels), and histories of up to kFewTokens are short (4 x 248320 with 3000: 6.4 us listed, 6.1 in registers; 129 x 40001 with
+// 1500: 12.9 and 14.6).  In registers they want 256 threads (in place 64 sequences of 4 rows of 248320, 512 tokens: 69 us, 77 with
+// 1,024; 2048 x 65536: 158 and 183), longer ones 1,024 (4 x 248320 with 8000: 9.7 and 7.4; 33 x 40001 with 20000: 21 and 12).
 constexpr int kOneLaunch = 800;
 constexpr int kFewTokens = 2048;
-constexpr int kPerSm = 4;       // CTAs of k_process
-constexpr int kPerSmSmall = 5;  // and of k_process_small (four: 129 x 40001 12.6 us, in more than one wave; 4 x 248320 5.0)
-constexpr int kChunk = 8192;    // places of a CTA of k_process at most (a multiple of 128)
+// Larger calls with one or two rows per sequence and more than kLongTokens, more than 1 / kDense of the vocabulary, are changed in
+// registers too (135 sequences of 2 x 248320, 14815 tokens: 126 us, 152 in two kernels; 45 x 178281, 24762: 30 and 43; but 619 x 2 x
+// 29595, 3232: 97 and 80; 270 x 248320, 7000: 147 and 135; 64 x 4 x 248320, 16000: 129 and 111).
+constexpr int kLongTokens = 4096, kDense = 20;
+constexpr int kPerSmSmall = 5;  // CTAs of k_process_small per SM (four: 129 x 40001 12.6 us, in more than one wave; 4 x 248320 5.0)
+constexpr int kChunkPerThread = 32;  // places of a CTA of k_process at most, for each of its threads
 constexpr int kBefore = 128;    // places of k_process_small's table before its chunk (a slot's at least, whole words of 16 bytes)
 constexpr int kMostNarrow = 32767;  // tokens that 16-bit counts hold, beside the prompt's bit
 constexpr uint32_t kInPrompt = 0x80000000u;
@@ -294,12 +302,12 @@ __global__ void __launch_bounds__(kThreadsP) k_process_stream(const Args a, int 
         s[k].store(r, e0 + k * kStep, lo, n, c0, inv_temp, [](int, int) { return 0u; }, [](int, float v) { return v; });
 }
 
-template <typename T, typename TO, bool GRAD, bool WIDE>
-__global__ void __launch_bounds__(kThreadsP, kPerSm) k_process(const Args a) {
+template <typename T, typename TO, bool GRAD, bool WIDE, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_process(const Args a) {
     extern __shared__ __align__(16) uint32_t s_words[];
     __shared__ int s_draft[kMaxRows];
     constexpr int VEC = Row<T, TO>::VEC;
-    constexpr int kStep = kThreadsP * VEC;
+    constexpr int kStep = THREADS * VEC;
     rows_wait();
     const unsigned int part = blockIdx.x / a.chunks;
     const int seq = (int)(part / a.groups);
@@ -321,14 +329,14 @@ __global__ void __launch_bounds__(kThreadsP, kPerSm) k_process(const Args a) {
     const int32_t* h = a.r.history != nullptr ? a.r.history + (size_t)seq * a.r.history_stride : nullptr;
     int t[BATCH];
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) t[k] = h != nullptr && tid + k * kThreadsP < a.r.history_width ? h[tid + k * kThreadsP] : -1;
+    for (int k = 0; k < BATCH; ++k) t[k] = h != nullptr && tid + k * THREADS < a.r.history_width ? h[tid + k * THREADS] : -1;
     const int len = h == nullptr ? 0 : a.r.history_len != nullptr ? min(a.r.history_len[seq], a.r.history_width) : a.r.history_width;
     const int prompt = h != nullptr && a.r.prompt_len != nullptr ? a.r.prompt_len[seq] : 0;
     const int32_t* bias_ids = biased ? a.r.bias_ids + (size_t)seq * a.r.n_bias : nullptr;
     const int first_bias = biased && tid < a.r.n_bias ? bias_ids[tid] : -1;
     const int32_t* draft = a.r.draft_ids != nullptr && a.per_seq > 1 ? a.r.draft_ids + (size_t)seq * (a.per_seq - 1) : nullptr;
 
-    for (int i = tid; i < (int)(Marks<WIDE>::bytes(a.chunk, biased) / 16); i += kThreadsP)
+    for (int i = tid; i < (int)(Marks<WIDE>::bytes(a.chunk, biased) / 16); i += THREADS)
         reinterpret_cast<uint4*>(s_words)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (draft != nullptr && tid < j1 - 1 - j0) s_draft[tid] = draft[j0 + tid];
     __syncthreads();
@@ -337,16 +345,16 @@ __global__ void __launch_bounds__(kThreadsP, kPerSm) k_process(const Args a) {
         const long long at = (long long)token - c0;
         return at >= 0 && at < n ? (int)at : -1;
     };
-    for (int base = tid; base < len; base += kThreadsP * BATCH) {
+    for (int base = tid; base < len; base += THREADS * BATCH) {
         int next[BATCH];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            const int i = base + (k + BATCH) * kThreadsP;
+            const int i = base + (k + BATCH) * THREADS;
             next[k] = i < len ? h[i] : -1;
         }
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            const int i = base + k * kThreadsP, at = place(t[k]);
+            const int i = base + k * THREADS, at = place(t[k]);
             if (i < len && at >= 0) {
                 c.add(at, i < prompt);
                 c.mark(at);
@@ -355,14 +363,14 @@ __global__ void __launch_bounds__(kThreadsP, kPerSm) k_process(const Args a) {
         }
     }
     if (biased)
-        for (int i = tid; i < a.r.n_bias; i += kThreadsP) {
+        for (int i = tid; i < a.r.n_bias; i += THREADS) {
             const int at = place(i == tid ? first_bias : bias_ids[i]);
             if (at < 0) continue;
             c.bias(at, i);
             c.mark(at);
         }
     if (draft != nullptr)
-        for (int i = tid; i < j1 - 1; i += kThreadsP) {
+        for (int i = tid; i < j1 - 1; i += THREADS) {
             const int at = place(draft[i]);
             if (at < 0) continue;
             if (i < j0) c.add(at, false);  // before all of the CTA's rows
@@ -765,29 +773,37 @@ static cudaError_t run(const ProcessArgs& p, cudaStream_t s) {
     if (marks == 0) return launch(k_process_stream<T, TO, GRAD>, stream, kThreadsP, 0, 0, s, a, stream_chunks, false);
 
     // The rows of a sequence share a look through its history while the machine is filled.
-    constexpr long long kResident = 152 * kPerSm;
-    a.rows = std::min(a.per_seq, kMaxRows);
-    while (a.rows > 1 && (long long)S * cut(a.per_seq, a.rows) * cut(a.V, 4096) < kResident) a.rows = (a.rows + 1) / 2;
-    a.groups = cut(a.per_seq, a.rows);
-    const long long units = (long long)S * a.groups;
+    auto share = [&](int threads) {
+        const long long resident = 152 * 1024 / threads;
+        a.rows = std::min(a.per_seq, kMaxRows);
+        while (a.rows > 1 && (long long)S * cut(a.per_seq, a.rows) * cut(a.V, threads * 16) < resident) a.rows = (a.rows + 1) / 2;
+        a.groups = cut(a.per_seq, a.rows);
+        return (long long)S * a.groups;
+    };
 
     if (p.out != p.in && stream <= kOneLaunch && tokens <= kFewTokens) {
         constexpr int kPlaces = kThreadsP * VEC * kStreamSlots, kListed = kPlaces + VEC;
         a.chunks = stream_chunks;
-        return launch(k_process_small<T, TO, GRAD>, units * a.chunks, kThreadsP,
+        return launch(k_process_small<T, TO, GRAD>, share(kThreadsP) * a.chunks, kThreadsP,
                       Marks<false>::bytes(kPlaces + kBefore, biased) + (size_t)std::min<long long>(marks, kListed) * 2,
                       Marks<false>::bytes(kPlaces + kBefore, true) + kListed * 2, s, a);
     }
-    if (p.out == p.in || stream <= kOneLaunch) {
-        a.chunks = (int)std::max<long long>(cut(a.V, kChunk), std::min<long long>(cut(a.V, 1024), kResident / units));
-        a.chunk = cut(cut(a.V, a.chunks), 128) * 128;
-        a.chunks = cut(a.V, a.chunk);
-        return tokens <= kMostNarrow ? launch(k_process<T, TO, GRAD, false>, units * a.chunks, kThreadsP, Marks<false>::bytes(a.chunk, biased),
-                                              Marks<false>::bytes(kChunk, true), s, a)
-                                     : launch(k_process<T, TO, GRAD, true>, units * a.chunks, kThreadsP, Marks<true>::bytes(a.chunk, biased),
-                                              Marks<true>::bytes(kChunk, true), s, a);
+    if (p.out == p.in || stream <= kOneLaunch || (a.per_seq <= 2 && tokens > kLongTokens && marks * kDense > a.V)) {
+        auto go = [&](auto kernel, auto wide, int threads) {
+            using M = Marks<decltype(wide)::value>;
+            const int most = threads * kChunkPerThread;
+            const long long units = share(threads);
+            a.chunks = (int)std::max<long long>(cut(a.V, most), std::min<long long>(cut(a.V, threads * 4), 152 * 1024 / threads / units));
+            a.chunk = cut(cut(a.V, a.chunks), 128) * 128;
+            a.chunks = cut(a.V, a.chunk);
+            return launch(kernel, units * a.chunks, threads, M::bytes(a.chunk, biased), M::bytes(most, true), s, a);
+        };
+        if (tokens <= kFewTokens) return go(k_process<T, TO, GRAD, false, kThreadsP>, std::false_type(), kThreadsP);
+        return tokens <= kMostNarrow ? go(k_process<T, TO, GRAD, false, 1024>, std::false_type(), 1024)
+                                     : go(k_process<T, TO, GRAD, true, 1024>, std::true_type(), 1024);
     }
 
+    const long long units = share(kThreadsP);
     a.hashed = marks <= kHashed;
     a.table = a.hashed ? 128 : kRange;
     while (a.hashed && a.table * 3ll < marks * 4) a.table *= 2;
