@@ -226,7 +226,8 @@ def test_temperatures_next_to_zero(vh, L, S):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("S,m,V,L", [(300, 1, 20011, 5000), (150, 2, 16384, 4200), (40, 2, 70003, 6000)])
+@pytest.mark.parametrize("S,m,V,L", [(300, 1, 20011, 5000), (150, 2, 16384, 4200), (40, 2, 70003, 6000), (200, 1, 70003, 40000),
+                                     (160, 3, 70003, 33000)])
 def test_long_histories_of_many_sequences(vh, S, m, V, L, dtype):
     """Histories of a good part of the vocabulary, on both sides of a twentieth and of 4096 tokens; a few sequences are compared."""
     g = torch.Generator().manual_seed(S)
