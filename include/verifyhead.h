@@ -37,17 +37,23 @@
  *    4-bit tables) before that kernel has finished; everything else is read
  *    only after it has, but hidden rows and candidate ids partly on the
  *    read-only path.  A kernel lets its dependent start early only if it
- *    signals so (griddepcontrol.launch_dependents).  What a copy wrote, or a
- *    kernel that does not signal early, is seen complete; do not write a
- *    weight table, hidden rows or candidate ids from a kernel that signals
- *    early right before a call.  Of this library's calls those that write
- *    rows or lists of ids for general use do not signal early
- *    (vh_add_rmsnorm; dx of vh_add_rmsnorm_grad; dlogits; log probabilities
- *    with alternatives; vh_nvfp4_pack; vh_nvfp4_quantize, _tile, _dequantize
- *    and _matmul; processed logits): a table, rows or a list that they
- *    write can be the next call's.  The draft and verify kernels signal early:
- *    their ids may be any later call's row_ids or draft_ids, and its cand_ids
- *    after a call or an operation that does not signal.
+ *    signals so (griddepcontrol.launch_dependents).  What a copy wrote is
+ *    seen complete; do not write a weight table, hidden rows or candidate ids
+ *    from a kernel that signals early right before a call.  Of this library's
+ *    calls those that write rows or lists of ids for general use do not signal
+ *    early (vh_add_rmsnorm; dx of vh_add_rmsnorm_grad; dlogits; log
+ *    probabilities with alternatives; vh_nvfp4_pack; vh_nvfp4_quantize, _tile,
+ *    _dequantize and _matmul; processed logits): rows or a list that they
+ *    write can be the next call's, and both matrices of vh_nvfp4_matmul, which
+ *    reads nothing ahead of the previous kernel's end.  As the weight table of
+ *    a head call, which does, what a kernel wrote is guaranteed complete once
+ *    another operation that does not signal early lies between the two (a
+ *    kernel of another library, a copy, one of the calls just listed): without
+ *    one the head starts when all blocks of that kernel have ended, and CUDA
+ *    orders their writes before its reads only by the wait that the table does
+ *    not take.  The draft and verify kernels signal early: their ids may be any
+ *    later call's row_ids or draft_ids, and its cand_ids after a call or an
+ *    operation that does not signal.
  *  - The same sources also build as libverifyhead_debug.so (-DVH_DEBUG): an
  *    identical ABI whose kernels check their row indices on the device and
  *    report a failed check in the workspace error word (bit 2) instead of
@@ -546,8 +552,9 @@ VH_API vh_status vh_head_logprobs(const void* hidden, const void* W_full, const 
  *       the low half of byte i);
  *   [16384 + (k/4)*512 + (r%32)*16 + (r/32)*4 + k%4]: the scale (e4m3, >= 0).
  * Blocks past H are zero; lines past the last row may hold anything.
- * Rows made by these calls may be any call's rows or table: no kernel that
- * writes them lets the next one start early.
+ * Rows made by these calls may be any call's rows, and vh_nvfp4_matmul's table:
+ * no kernel that writes them lets the next one start early.  For the table of a
+ * head call see the conventions above.
  * ------------------------------------------------------------------------ */
 
 /* ceil(rows / 128) * ceil(H / 256) * 18432; 0 unless rows >= 1 and 16 <= H <= 65536, H % 16 == 0. */
@@ -596,8 +603,7 @@ VH_API vh_status vh_nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales
  *     y[t,v] = x_g(t) * w_g(v) * sum_h (code * scale of X)[t,h] * (code * scale of W)[v,h]
  * on the block-scaled 4-bit tensor cores, fp32 accumulation, one rounding to
  * dtype.  g is a row's entry of the array, or the number where that is NULL.
- * W is read before the previous kernel of the stream has finished (see
- * mtp_draft_head_argmax), X and the arrays after.
+ * Everything is read after the previous kernel of the stream has finished.
  *
  *  x        device, tiled [T][H], 16-byte aligned
  *  w        device, tiled [V][H], 16-byte aligned
