@@ -259,7 +259,10 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
-    __syncthreads();
+    if (split > 1)
+        cluster_sync();  // every CTA of the cluster runs: the others may write to its shared memory
+    else
+        __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = bars->tmem_base;
     // rows of X of tile `tx`, as the MMA takes them
