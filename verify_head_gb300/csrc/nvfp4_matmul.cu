@@ -13,14 +13,15 @@
 //
 // Bound: the stream of W for few rows (4 x 248320 x 2048 44.5 us, 0.97 of the copy rate), what L2 gives an SM for many (4096 x 8192 x
 // 8192 88 us, 6.2 PFLOP/s; the pairs below).  Up to 32 rows of X a stage has 32 lines of X and there are eight stages of W, so
-// that enough of it is on its way; with few tiles a cluster shares the records of one (1 x 4096 x 4096 5.8 us, 9.9 with a CTA each).
+// that enough of it is on its way; with few tiles a cluster shares the records of one (1 x 4096 x 4096 5.9 us, 9.9 with a CTA each).
 //
-// Every wait is bounded; on expiry the CTA's flag is set, the tiles concerned become NaN, copies in flight are waited for, and
-// TMEM is freed.
+// Every wait is bounded; on expiry the CTA's flag is set, the tiles concerned become NaN, copies in flight are waited for
+// (vh_ring.cuh), and TMEM is freed.
 #include <algorithm>
 #include <atomic>
 
 #include "vh_nvfp4_tiles.h"
+#include "vh_ring.cuh"
 #include "vh_row_kernels.h"
 #include "vh_rows.cuh"
 #include "vh_tc.cuh"
@@ -57,6 +58,8 @@ struct alignas(8) Bars {
     unsigned long long mma_done;
     unsigned int tmem_base;
     unsigned int err;
+    unsigned int asked[2][2];  // records of W and of X that each CTA of a pair has asked for (in the leader's)
+    unsigned int peer_err;
 };
 
 struct Args {
@@ -302,9 +305,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
                 __syncwarp();
             }
         }
-        // copies in flight, should the kernel end early
-        if (is_w && leader)
-            for (uint32_t j = (it > (uint32_t)STAGES ? it - STAGES : 0); j < it; ++j) mbar_drain(&bars->full[j % STAGES], (j / STAGES) & 1u);
+        if (leader) bars->asked[is_w ? 0 : 1][0] = it;
         __syncwarp();
     } else if (warp == 1) {
         // The whole warp runs the loop, so that addresses and descriptors stay in uniform registers; one lane issues.  (With the
@@ -419,6 +420,10 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
     }
     tc_fence_before();
     __syncthreads();
+    if (bars->err != 0u) {
+        if (threadIdx.x == 0) ring::settle<STAGES, 1>(bars->full, {bars->asked[0][0]}, {bars->asked[1][0]}, 0u, 0u);
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
@@ -470,7 +475,7 @@ __global__ void __launch_bounds__(kThreadsM, 1)
         mbar_init(&bars->tmem_full[0], 1);
         mbar_init(&bars->tmem_empty[0], 2 * kEpiWarps);  // of both CTAs
         mbar_init(&bars->mma_done, 1);
-        bars->err = 0u;
+        bars->err = bars->peer_err = 0u;
         ptx::fence_barrier_init();
     }
     if (warp == 1) {
@@ -523,8 +528,9 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                 __syncwarp();
             }
         }
-        if (rank == 0 && is_w && leader)  // the leader's barriers see both CTAs' loads
-            for (uint32_t j = (it > (uint32_t)STAGES ? it - STAGES : 0); j < it; ++j) mbar_drain(&bars->full[j % STAGES], (j / STAGES) & 1u);
+        if (leader)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(smem_u32(&bars->asked[is_w ? 0 : 1][rank]), 0)), "r"(it)
+                         : "memory");
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
@@ -621,7 +627,16 @@ __global__ void __launch_bounds__(kThreadsM, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && bars->err != 0u)  // both have to know
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(smem_u32(&bars->peer_err), rank ^ 1u)), "r"(1u) : "memory");
+    __syncwarp();
     cluster_sync();  // no CTA leaves while its peer may still signal or read it
+    if ((bars->err | bars->peer_err) != 0u) {
+        if (rank == 0 && threadIdx.x == 0)  // the leader's barriers see both CTAs' copies
+            ring::settle<STAGES, 2>(bars->full, bars->asked[0], bars->asked[1], kTileBytes, kStage - kTileBytes);
+        __syncwarp();
+        cluster_sync();
+    }
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
