@@ -611,8 +611,9 @@ VH_API vh_status vh_nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales
  *  x_scale, w_scale  finite; ignored where the array is given
  *  y        device, dtype [T][V] (out), y_stride >= V elements between rows
  *  1 <= T, V <= 2^31 - 1024;  16 <= H <= 65536, H % 16 == 0
- * Should a wait inside the kernel expire, the tiles concerned are NaN; the call
- * has no workspace, and so no error word.
+ * Should a wait inside the kernel expire (two seconds; each begins after the
+ * previous kernel's end), the tiles concerned are NaN; the call has no
+ * workspace, and so no error word.
  */
 VH_API vh_status vh_nvfp4_matmul(const uint8_t* x, float x_scale, const float* x_scales, const uint8_t* w, float w_scale,
                                  const float* w_scales, int T, int V, int H, int dtype, void* y, int64_t y_stride,

@@ -17,8 +17,8 @@ def vh():
     return vh
 
 
-# up to 32 rows, up to 128, pairs
-SHAPES = [(8, 30000, 1024), (100, 30000, 512), (260, 40000, 512)]
+# up to 32 rows, up to 128, more, pairs
+SHAPES = [(8, 30000, 1024), (100, 30000, 512), (260, 40000, 512), (1024, 8192, 2048)]
 WRITERS = ["tile", "quantize", "quantize, then log probabilities"]
 
 

@@ -15,8 +15,8 @@
 // 8192 88 us, 6.2 PFLOP/s; the pairs below).  Up to 32 rows of X a stage has 32 lines of X and there are eight stages of W, so
 // that enough of it is on its way; with few tiles a cluster shares the records of one (1 x 4096 x 4096 5.9 us, 9.9 with a CTA each).
 //
-// Every wait is bounded; on expiry the CTA's flag is set, the tiles concerned become NaN, copies in flight are waited for
-// (vh_ring.cuh), and TMEM is freed.
+// Every wait is bounded, by a limit that begins when the previous kernel has ended; on expiry the CTA's flag is set, the tiles
+// concerned become NaN, copies in flight are waited for (vh_ring.cuh), and TMEM is freed.
 #include <algorithm>
 #include <atomic>
 
@@ -310,6 +310,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
     } else if (warp == 1) {
         // The whole warp runs the loop, so that addresses and descriptors stay in uniform registers; one lane issues.  (With the
         // loop in one lane every instruction's operands were moved there first: 12 instructions took 1,400 cycles a stage.)
+        rows_wait();  // nothing comes before: else the first wait's limit would count the previous kernel's time
         const bool leader = elect_one();
         const uint32_t base = smem_u32(smem);
         uint32_t it = 0, local = 0;
@@ -534,6 +535,7 @@ __global__ void __launch_bounds__(kThreadsM, 1)
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
+            rows_wait();
             const bool leader = elect_one();
             const uint32_t base = smem_u32(smem);
             uint32_t it = 0, local = 0;
