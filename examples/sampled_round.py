@@ -42,6 +42,8 @@ def main():
                  allowed=ints(2 ** 31 - 1, rows, V // 32))
     out = vh.logits_process(logits, **rules)
     tokens = torch.multinomial(torch.softmax(out.float(), 1), 1, generator=g)[:, 0].int()
+    words = rules["allowed"].gather(1, (tokens // 32).long()[:, None])[:, 0]
+    assert bool(((words >> (tokens % 32)) & 1).all())  # nothing that the grammar forbids
     logprob, entropy, lse, best, _ = vh.logits_logprobs(out, tokens, 1)
     greedy = best.view(B, K + 1)[3]  # the last sequence's temperature is 0
     print(f"tokens {tokens.view(B, K + 1)[:3].tolist()}, greedy {greedy.tolist()}; mean log probability {float(logprob.mean()):.3f}")
@@ -49,7 +51,7 @@ def main():
     # Train: -mean(advantage * logprob), back through the processing and the head.
     advantage = torch.randn(rows, generator=g, device="cuda")
     d = vh.logits_logprobs_grad(out, tokens, lse, entropy, -advantage / rows)
-    d = vh.logits_process_grad(d, logits, dlogits=d, **rules)
+    d = vh.logits_process_grad(d, logits, **rules)  # (dlogits=d saves the buffer, and takes longer)
     dhidden = d @ vh.nvfp4_dequantize(codes, scales, g_head)
     print(f"|dlogits| {float(d.float().norm()):.4f} |dhidden| {float(dhidden.float().norm()):.4f}")
     assert bool(torch.isfinite(dhidden).all())
