@@ -1066,7 +1066,7 @@ def logits_process(logits, history=None, history_len=None, prompt_len=None, draf
     draft_ids [S,R/S-1] int32: row j also counts the first j; repetition, frequency, presence, temperature [S] fp32
     (temperature 0: greedy, as 1); bias_ids [S,n] int32 with bias [S,n] fp32 (the last entry of an id counts); allowed
     [R,>=ceil(V/32)] int32, bit v % 32 of word v / 32.  Every rule may be None.
-    out: logits' type or fp32, may be `logits` itself.  -> out"""
+    out: logits' type or fp32, may be `logits` itself (which takes longer).  -> out"""
     if stream is None and out is not None:
         m = _compiled_calls()
         if m:
@@ -1099,7 +1099,7 @@ def logits_process_grad(dout, logits, history=None, history_len=None, prompt_len
                         frequency=None, presence=None, bias_ids=None, bias=None, allowed=None, temperature=None, dlogits=None,
                         stream=None):
     """Gradient of logits_process with respect to the logits, from dout [R,V] of their type (0 where not allowed); dlogits
-    may be `dout` itself.  The other arguments as there.  -> dlogits"""
+    may be `dout` itself (which takes longer).  The other arguments as there.  -> dlogits"""
     if stream is None and dlogits is not None:
         m = _compiled_calls()
         if m:
