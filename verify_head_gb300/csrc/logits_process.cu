@@ -39,6 +39,11 @@
 //     4 x 248320 fp32, history 8000              11.9             7.4
 //     201 x 65536 fp16, masked, 9951                             35             59
 //     256 x 248320 bf16, histories of 4096       69.4            94             58
+//     256 x 248320 bf16, histories of 512                        69             45
+//     2048 x 65536 bf16, histories of 512                       152            105
+//     gradient of 2048 x 65536, 512                             179            110
+//
+// (The second column of the last three is what these calls take in place.)
 //
 // Bound: memory (the logits once in and once out).  256 x 248320 bf16: 43 us
 // without a history (255 MB: 0.89 of the copy rate), 45 with 512 tokens, 58 with
@@ -69,7 +74,9 @@ constexpr int kFewTokens = 2048;
 // registers too (135 sequences of 2 x 248320, 14815 tokens: 126 us, 152 in two kernels; 45 x 178281, 24762: 30 and 43; but 619 x 2 x
 // 29595, 3232: 97 and 80; 270 x 248320, 7000: 147 and 135; 64 x 4 x 248320, 16000: 129 and 111).
 constexpr int kLongTokens = 4096, kDense = 20;
-constexpr int kPerSmSmall = 5;  // CTAs of k_process_small per SM (four: 129 x 40001 12.6 us, in more than one wave; 4 x 248320 5.0)
+// CTAs of k_process_small per SM (four: 129 x 40001 12.6 us, in more than one wave; 4 x 248320 5.0).  That is 48 registers a thread,
+// for which the instances spill up to 48 bytes.
+constexpr int kPerSmSmall = 5;
 constexpr int kChunkPerThread = 32;  // places of a CTA of k_process at most, for each of its threads
 constexpr int kBefore = 128;    // places of k_process_small's table before its chunk (a slot's at least, whole words of 16 bytes)
 constexpr int kMostNarrow = 32767;  // tokens that 16-bit counts hold, beside the prompt's bit
@@ -111,7 +118,8 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* words, long long at,
 }
 __device__ __forceinline__ bool bit_at(const uint32_t* words, long long at) { return ((words[at >> 5] >> (at & 31)) & 1u) != 0u; }
 
-// Of a temperature; a finite number also where that is below 2^-128, since 0 times it has to be 0.
+// Of a temperature; a finite number also where that is below 2^-128, since 0 times it has to be 0.  The product with it is off by two
+// roundings of 2^-24, where a quotient would be by one.
 __device__ __forceinline__ float inverse(float temp) {
     return temp > 0.0f ? fminf(__fdiv_rn(1.0f, temp), 3.40282347e38f) : 1.0f;
 }

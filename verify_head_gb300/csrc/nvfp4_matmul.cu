@@ -11,8 +11,8 @@
 // neighbours of a row.  (One row after the other for all, the rows' scales by shuffles: 256 x 248320 x 2048 took 113 us, and
 // 104 with a quarter of the contraction: the epilogue set the pace.)
 //
-// Bound: the stream of W for few rows (4 x 248320 x 2048 44.5 us, 0.97 of the copy rate), what L2 gives an SM for many (4096 x 8192 x
-// 8192 88 us, 6.2 PFLOP/s; the pairs below).  Up to 32 rows of X a stage has 32 lines of X and there are eight stages of W, so
+// Bound: the stream of W for few rows (4 x 248320 x 2048 44.5 us, 0.97 of the copy rate); for many no unit's limit but the waits of
+// the pairs below (4096 x 8192 x 8192 94 us, 5.9 PFLOP/s).  Up to 32 rows of X a stage has 32 lines of X and there are eight stages of W, so
 // that enough of it is on its way; with few tiles a cluster shares the records of one (1 x 4096 x 4096 5.9 us, 9.9 with a CTA each).
 //
 // Every wait is bounded, by a limit that begins when the previous kernel has ended; on expiry the CTA's flag is set, the tiles
@@ -437,10 +437,11 @@ __global__ void __launch_bounds__(kThreadsM, 1) k_matmul(const Args a) {
 // CTA's TMEM has the accumulators of its own rows of W and the scales of all rows of X, 32 rows to a column and a record's in four
 // columns (tcgen05.cp writes four at a time, at a multiple of four).
 //
-// A stage is 38 KiB per CTA for 512 cycles of MMAs, a little more than an SM is given by L2 (64 bytes a cycle): 0.39 us, 6.2
-// PFLOP/s.  Two accumulators of 256 columns would leave the scales no room: there is one, and the epilogue takes all of it into
-// registers, in two halves, the second before it hands it back; every tile waits for that and the writing of the first, about
-// 2.2 us.  (Pairs on one record, with two accumulators: 4096 x 8192 x 8192 138 us, 88 with two;
+// A stage is 38 KiB per CTA for 512 cycles of MMAs and takes about 700.  Two accumulators of 256 columns would leave the scales no
+// room: there is one, and the epilogue takes all of it into registers, in two halves, the second before it hands it back; every
+// tile waits for that and the writing of the first, about 2.2 us of the 13.4 that one takes with 32 records (4096 x 8192 x 8192, seven
+// tiles to a pair).  No unit is at its limit there: tensor pipe 60% busy, L2 to SM 35% of its rate (1.3 GB, 45 bytes a cycle and
+// SM), L2 slices 45%.  (Pairs on one record, with two accumulators: 4096 x 8192 x 8192 138 us, 88 with two records in the same run;
 // 256 x 248320 x 2048 84 and 87; what one CTA per tile does as well.)
 //
 // The records come by tensor maps over the buffer's bytes, since those copies may signal the leader's barrier.

@@ -19,9 +19,12 @@
 //
 // A thread has blocks of 16 elements in registers (32 bytes of 16-bit types),
 // so a row is read once, whatever finds its scale: a row's threads are one
-// warp or several of a CTA.  16384 x 2048 bf16: 20.7 us to 4 bits (86 MB:
-// 0.62 of the copy rate; bound by issue slots, 69%, 15 instructions per
-// element) and 15.2 us back (0.84).
+// warp or several of a CTA.  16384 x 2048 bf16: 20.1 us to 4 bits (86 MB:
+// 0.64 of the copy rate; no unit at its limit: 69% of the issue slots, 15
+// instructions per element, with 40% of the warps that an SM holds) and 14.7
+// us back (0.88), 15.4 from tiles.  Rows that lie off 32 bytes (a pitch of 2049)
+// go element by element: 40 us, and 182 back.  Row-major to tiles: 248320 x
+// 2048 in 106 us (572 MB: 0.81).
 #include <algorithm>
 
 #include "vh_nvfp4_tiles.h"
